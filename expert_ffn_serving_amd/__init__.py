@@ -25,6 +25,8 @@ CFG_TIMING = 1
 CFG_SYNC_HOST = 2
 T_DECODE_GATEUP, T_DECODE_DOWN, T_PREFILL_GATEUP, T_PREFILL_DOWN = 0, 1, 2, 3
 HOST_ISA_SCALAR, HOST_ISA_AVX2, HOST_ISA_AVX512F, HOST_ISA_AVX512_BF16 = 0, 1, 2, 3
+DT_BF16, DT_F16, DT_F32 = 0, 1, 2
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_SWIGLU = 0, 1, 2, 3, 4
 HOST_ISA_NAMES = {0: "scalar", 1: "avx2+fma", 2: "avx512f", 3: "avx512-bf16"}
 
 EFF_OK, EFF_EINVAL, EFF_ENOMEM, EFF_EHIP, EFF_ECAPTURE, EFF_ESTATE, EFF_EDEVICE = 0, -1, -2, -3, -4, -5, -6
@@ -101,6 +103,15 @@ def lib():
             "eff_get_host_info": (I32, [VP, VP]),
             "eff_set_host_isa": (I32, [VP, I32]),
             "eff_slot_ptr": (I32, [VP, I32, VP]),
+            "eff_matmul_workspace": (I64, [VP, I32]),
+            "eff_matmul": (I32, [VP] * 9 + [ctypes.c_size_t, VP]),
+            "eff_matmul_backward": (I32, [VP] * 10 + [ctypes.c_size_t, VP]),
+            "eff_sort_tokens_workspace": (I64, [I64, I32]),
+            "eff_sort_tokens": (I32, [VP, I64, I32, VP, VP, VP, VP, ctypes.c_size_t, VP]),
+            "eff_dispatch_tokens": (I32, [I32, VP, I64, VP, I64, I32, I64, VP, I64, I64, VP]),
+            "eff_dispatch_tokens_backward": (I32, [I32, VP, I64, I64, VP, I64, I32, I64, VP, I64, VP]),
+            "eff_combine_tokens": (I32, [I32, VP, I64, I64, VP, VP, I64, I32, I64, VP, I64, VP, I64, VP]),
+            "eff_combine_tokens_backward": (I32, [I32, VP, I64, VP, I64, I64, VP, VP, I64, I32, I64, VP, I64, VP, VP]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -360,3 +371,7 @@ class Engine:
         out = ctypes.c_void_p()
         _check(lib().eff_slot_ptr(self.h, slot, ctypes.byref(out)))
         return out.value
+
+
+from .ops import (combine_tokens, combine_tokens_backward, dispatch_tokens, dispatch_tokens_backward,  # noqa: E402,F401
+                  grouped_matmul, grouped_matmul_backward, matmul, matmul_backward, sort_tokens)

@@ -15,8 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libeff.so")
 BUILD = os.path.join(HERE, "_build")
 
-HIP_SOURCES = ["k_cache.hip", "k_route.hip", "k_decode.hip", "k_prefill.hip"]
-CPP_SOURCES = ["engine.cpp", "host_exec.cpp"]
+HIP_SOURCES = ["k_cache.hip", "k_route.hip", "k_decode.hip", "k_prefill.hip", "k_matmul.hip", "k_tokens.hip"]
+CPP_SOURCES = ["engine.cpp", "host_exec.cpp", "ops.cpp"]
 
 ARCH = "gfx950"
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function"]

@@ -327,4 +327,61 @@ int64_t qstar_host(int64_t m, int64_t f);
 // host executor
 void host_ffn(eff_engine* e, int layer, const uint16_t* x, const int32_t* cpu_ids, int B, float* y);
 int host_isa_best();
+
+// ---- operators without an engine (ops.cpp, k_matmul.hip, k_tokens.hip) -------------------------------
+
+// How rows and weights pair up in one launch of products.
+enum {
+  MM_DENSE = 0,
+  MM_ROW_GROUPS = 1,  // rows offsets[e]..offsets[e+1]-1 of x go with w[e]
+  MM_K_GROUPS = 2     // y[e] sums over k = offsets[e]..offsets[e+1]-1 (weight gradients of the groups)
+};
+
+// y[m,n] = act(sum_k x(m,k) w(n,k) + bias[n]) + residual[m,n]; strides in elements.  With EFF_ACT_SWIGLU w has
+// 2N rows (gate, up).  M: rows of all groups (MM_ROW_GROUPS); K: the k of all groups (MM_K_GROUPS).
+struct MmArgs {
+  const void* x;
+  int64_t sxm, sxk;
+  const void* w;
+  int64_t swn, swk, swg;  // swg: between groups (MM_ROW_GROUPS)
+  int64_t M, N, K;
+  const int32_t* offsets;
+  const void* bias;
+  const void* residual;
+  int64_t ldr;
+  void* y;
+  int64_t ldy, syg;  // syg: between groups (MM_K_GROUPS)
+  void* pre;
+  int64_t ldp;
+  int dtype, y_f32, act, mode, groups;
+};
+hipError_t launch_matmul(const MmArgs& a, hipStream_t s);
+
+// dz = dy * act'(pre) [M, N or 2N] rounded to dtype (dz null: not written) and its column sums per group (dbias null: none)
+struct MmGrad {
+  const void* dy;
+  int64_t ldy;
+  const void* pre;
+  int64_t ldp;
+  void* dz;
+  int64_t lddz;
+  void* dbias;
+  const int32_t* offsets;
+  int64_t M, N;
+  int dtype, dy_f32, act, groups;
+};
+hipError_t launch_matmul_dz(const MmGrad& a, hipStream_t s);
+
+int64_t sort_workspace(int64_t n, int E);
+hipError_t tokens_setup();
+hipError_t launch_sort_tokens(const int32_t* ids, int64_t n, int E, int32_t* offsets, int32_t* order, int32_t* pos,
+                              int32_t* hist, hipStream_t s);
+hipError_t launch_dispatch_tokens(int dtype, const void* x, int64_t ldx, const int32_t* pos, int64_t T, int K, int64_t H,
+                                  void* xs, int64_t ldxs, int64_t rows, hipStream_t s);
+hipError_t launch_combine_tokens(int dtype, const void* ys, int64_t ldys, int64_t rows, const int32_t* pos, const float* w,
+                                 int64_t T, int K, int64_t H, const void* residual, int64_t ldr, void* out, int64_t ldo,
+                                 hipStream_t s);
+hipError_t launch_combine_tokens_grad(int dtype, const void* dout, int64_t ldd, const void* ys, int64_t ldys, int64_t rows,
+                                      const int32_t* pos, const float* w, int64_t T, int K, int64_t H, void* dys,
+                                      int64_t lddys, float* dw, hipStream_t s);
 }  // namespace eff

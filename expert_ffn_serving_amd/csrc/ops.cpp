@@ -1,0 +1,219 @@
+// C entry points of the operators that need no engine: products with their epilogue and gradients, tokens
+// sorted by expert and back.  Argument checks, workspace layout and launches; the kernels are in
+// k_matmul.hip and k_tokens.hip.
+#include <algorithm>
+#include <mutex>
+
+#include "eff_internal.h"
+
+using namespace eff;
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int kMaxDevices = 64;
+
+int bad(const char* fn, const char* why) { return fail(EFF_EINVAL, std::string(fn) + ": " + why); }
+
+// kernel attributes, once per device
+int setup(const char* fn) {
+  static std::once_flag once[kMaxDevices];
+  static hipError_t result[kMaxDevices];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return fail(EFF_EHIP, std::string(fn) + ": no HIP device");
+  std::call_once(once[dev], [&] { result[dev] = tokens_setup(); });
+  if (result[dev] != hipSuccess) return fail(EFF_EHIP, std::string(fn) + ": " + hipGetErrorString(result[dev]));
+  return EFF_OK;
+}
+
+// a launch that was refused before it reached the device is the caller's sizes
+int launched(const char* fn, hipError_t err) {
+  if (err == hipSuccess) return EFF_OK;
+  if (err == hipErrorInvalidConfiguration) return fail(EFF_EINVAL, std::string(fn) + ": too many output tiles for one launch");
+  return fail(EFF_EHIP, std::string(fn) + ": " + hipGetErrorString(err));
+}
+
+int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// nullptr if the description is sound, else what is wrong with it
+const char* check_desc(const eff_matmul_desc* d) {
+  if (!d) return "the description is NULL";
+  if (d->dtype != EFF_DT_BF16 && d->dtype != EFF_DT_F16) return "dtype must be EFF_DT_BF16 or EFF_DT_F16";
+  if (d->out_dtype != d->dtype && d->out_dtype != EFF_DT_F32) return "out_dtype must be dtype or EFF_DT_F32";
+  if (d->act < EFF_ACT_NONE || d->act > EFF_ACT_SWIGLU) return "unknown activation";
+  if (d->groups < 0 || d->groups > kMaxExperts) return "groups must be in [0, 4096]";
+  if (d->m < 0 || d->m >= kMaxDim || d->n < 1 || d->k < 1 || d->k >= kMaxDim) return "m >= 0, n >= 1, k >= 1, each below 2^31";
+  const int64_t nw = d->act == EFF_ACT_SWIGLU ? 2 * d->n : d->n;
+  if (nw >= kMaxDim) return "W's rows must be below 2^31";
+  return nullptr;
+}
+
+int64_t w_rows(const eff_matmul_desc* d) { return d->act == EFF_ACT_SWIGLU ? 2 * d->n : d->n; }
+bool inputs_ld_bad(int64_t ld) { return ld < 0; }
+
+// the backward pass materialises dz unless it is dy itself
+bool needs_dz(const eff_matmul_desc* d) { return d->act != EFF_ACT_NONE || d->out_dtype != d->dtype; }
+int64_t dz_bytes(const eff_matmul_desc* d) { return needs_dz(d) ? align256(d->m * w_rows(d) * 2) : 0; }
+
+int check_ws(const char* fn, int64_t need, const void* ws, size_t bytes) {
+  if (need <= 0) return EFF_OK;
+  if (!ws || (int64_t)bytes < need) return fail(EFF_EINVAL, std::string(fn) + ": needs " + std::to_string(need) + " bytes of workspace");
+  if ((uintptr_t)ws % 256) return bad(fn, "the workspace must be 256-byte aligned");
+  return EFF_OK;
+}
+
+const char* check_rows(int dtype, int64_t T, int K, int64_t H, int64_t rows) {
+  if (dtype < EFF_DT_BF16 || dtype > EFF_DT_F32) return "unknown dtype";
+  if (T < 0 || K < 1 || K > kMaxTopK || T * K >= kMaxDim || T >= kMaxDim) return "T >= 0, 1 <= K <= 32, T*K below 2^31";
+  if (H < 1 || H >= kMaxDim || rows < 0 || rows >= kMaxDim) return "H >= 1, rows >= 0, each below 2^31";
+  return nullptr;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t eff_matmul_workspace(const eff_matmul_desc* d, int backward) {
+  if (const char* why = check_desc(d)) return bad("eff_matmul_workspace", why);
+  return backward ? dz_bytes(d) : 0;
+}
+
+int eff_matmul(const eff_matmul_desc* d, const void* x, const void* w, const void* bias, const void* residual,
+               const int32_t* offsets, void* y, void* pre, void* workspace, size_t workspace_bytes, eff_stream_t stream) {
+  const char* fn = "eff_matmul";
+  if (const char* why = check_desc(d)) return bad(fn, why);
+  if (d->m == 0) return EFF_OK;
+  if (!x || !w || !y) return bad(fn, "x, w and y are needed");
+  if ((d->groups > 0) != (offsets != nullptr)) return bad(fn, "offsets go with groups");
+  const int64_t nw = w_rows(d);
+  if (inputs_ld_bad(d->ld_x) || inputs_ld_bad(d->ld_w) || inputs_ld_bad(d->ld_residual) || d->stride_w < 0) return bad(fn, "negative stride");
+  if (d->m > 1 && (d->ld_y < d->n || (pre && d->ld_pre < nw))) return bad(fn, "rows of an output overlap");
+  if (int rc = check_ws(fn, eff_matmul_workspace(d, 0), workspace, workspace_bytes)) return rc;
+  MmArgs a = {};
+  a.dtype = d->dtype;
+  a.mode = d->groups ? MM_ROW_GROUPS : MM_DENSE;
+  a.groups = d->groups;
+  a.offsets = offsets;
+  a.x = x, a.sxm = d->ld_x, a.sxk = 1;
+  a.w = w, a.swn = d->ld_w, a.swk = 1, a.swg = d->stride_w;
+  a.M = d->m, a.N = d->n, a.K = d->k;
+  a.bias = bias, a.residual = residual, a.ldr = d->ld_residual;
+  a.y = y, a.ldy = d->ld_y, a.y_f32 = d->out_dtype == EFF_DT_F32;
+  a.pre = pre, a.ldp = d->ld_pre, a.act = d->act;
+  return launched(fn, launch_matmul(a, (hipStream_t)stream));
+}
+
+int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x, const void* w, const void* pre,
+                        const int32_t* offsets, void* dx, void* dw, void* dbias, void* workspace, size_t workspace_bytes,
+                        eff_stream_t stream) {
+  const char* fn = "eff_matmul_backward";
+  if (const char* why = check_desc(d)) return bad(fn, why);
+  const bool rows = d->m > 0;
+  if ((d->groups > 0) != (offsets != nullptr)) return bad(fn, "offsets go with groups");
+  if (rows && (!dy || (dx && !w) || (dw && !x))) return bad(fn, "dy is needed, w for dx, x for dw");
+  if (rows && d->act != EFF_ACT_NONE && !pre) return bad(fn, "pre is needed with an activation");
+  const int64_t nw = w_rows(d);
+  if (inputs_ld_bad(d->ld_x) || inputs_ld_bad(d->ld_w) || inputs_ld_bad(d->ld_y) || inputs_ld_bad(d->ld_pre) || d->stride_w < 0)
+    return bad(fn, "negative stride");
+  if ((dx && d->m > 1 && d->ld_dx < d->k) || (dw && nw > 1 && d->ld_dw < d->k) ||
+      (dw && d->groups > 1 && d->stride_dw < (nw - 1) * std::max(d->ld_dw, d->k) + d->k))
+    return bad(fn, "rows of an output overlap");
+  if (int rc = check_ws(fn, eff_matmul_workspace(d, 1), workspace, workspace_bytes)) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  MmGrad g = {};
+  g.dtype = d->dtype, g.dy_f32 = d->out_dtype == EFF_DT_F32, g.act = d->act;
+  g.M = d->m, g.N = d->n;
+  g.dy = dy, g.ldy = d->ld_y, g.pre = pre, g.ldp = d->ld_pre;
+  g.offsets = offsets, g.groups = d->groups;
+  g.dbias = dbias;
+  const void* dz = dy;
+  int64_t lddz = d->ld_y;
+  if (needs_dz(d) && (dx || dw)) {
+    g.dz = workspace, g.lddz = nw;
+    dz = workspace, lddz = nw;
+  }
+  if (g.dz || dbias)
+    if (int rc = launched(fn, launch_matmul_dz(g, s))) return rc;
+  MmArgs a = {};
+  a.dtype = d->dtype;
+  a.groups = d->groups;
+  a.offsets = offsets;
+  if (dx && rows) {  // dx[m,k] = sum over W's rows n of dz[m,n] w[n,k]
+    a.mode = d->groups ? MM_ROW_GROUPS : MM_DENSE;
+    a.x = dz, a.sxm = lddz, a.sxk = 1;
+    a.w = w, a.swn = 1, a.swk = d->ld_w, a.swg = d->stride_w;
+    a.M = d->m, a.N = d->k, a.K = nw;
+    a.y = dx, a.ldy = d->ld_dx;
+    if (int rc = launched(fn, launch_matmul(a, s))) return rc;
+  }
+  if (dw) {  // dw[n,k] = sum over rows m of dz[m,n] x[m,k]
+    a.mode = d->groups ? MM_K_GROUPS : MM_DENSE;
+    a.x = dz, a.sxm = 1, a.sxk = lddz;
+    a.w = x, a.swn = 1, a.swk = d->ld_x, a.swg = 0;
+    a.M = nw, a.N = d->k, a.K = d->m;
+    a.y = dw, a.ldy = d->ld_dw, a.syg = d->stride_dw;
+    if (int rc = launched(fn, launch_matmul(a, s))) return rc;
+  }
+  return EFF_OK;
+}
+
+int64_t eff_sort_tokens_workspace(int64_t n, int num_experts) {
+  if (n < 0 || n >= kMaxDim || num_experts < 1 || num_experts > kMaxExperts)
+    return bad("eff_sort_tokens_workspace", "0 <= n < 2^31, 1 <= num_experts <= 4096");
+  return sort_workspace(n, num_experts);
+}
+
+int eff_sort_tokens(const int32_t* ids, int64_t n, int num_experts, int32_t* offsets, int32_t* order, int32_t* pos,
+                    void* workspace, size_t workspace_bytes, eff_stream_t stream) {
+  const char* fn = "eff_sort_tokens";
+  const int64_t need = eff_sort_tokens_workspace(n, num_experts);
+  if (need < 0) return (int)need;
+  if (!offsets || (n > 0 && (!ids || !order || !pos))) return bad(fn, "ids, offsets, order and pos are needed");
+  if (int rc = check_ws(fn, need, workspace, workspace_bytes)) return rc;
+  if (int rc = setup(fn)) return rc;
+  return launched(fn, launch_sort_tokens(ids, n, num_experts, offsets, order, pos, (int32_t*)workspace, (hipStream_t)stream));
+}
+
+int eff_dispatch_tokens(int dtype, const void* x, int64_t ld_x, const int32_t* pos, int64_t T, int K, int64_t H, void* xs,
+                        int64_t ld_xs, int64_t rows, eff_stream_t stream) {
+  const char* fn = "eff_dispatch_tokens";
+  if (const char* why = check_rows(dtype, T, K, H, rows)) return bad(fn, why);
+  if (T == 0 || rows == 0) return EFF_OK;
+  if (!x || !pos || !xs) return bad(fn, "x, pos and xs are needed");
+  if (ld_x < 0 || (rows > 1 && ld_xs < H)) return bad(fn, "negative stride, or rows of an output overlap");
+  return launched(fn, launch_dispatch_tokens(dtype, x, ld_x, pos, T, K, H, xs, ld_xs, rows, (hipStream_t)stream));
+}
+
+int eff_dispatch_tokens_backward(int dtype, const void* dxs, int64_t ld_dxs, int64_t rows, const int32_t* pos, int64_t T, int K,
+                                 int64_t H, void* dx, int64_t ld_dx, eff_stream_t stream) {
+  const char* fn = "eff_dispatch_tokens_backward";
+  if (const char* why = check_rows(dtype, T, K, H, rows)) return bad(fn, why);
+  if (T == 0) return EFF_OK;
+  if ((!dxs && rows > 0) || !pos || !dx) return bad(fn, "dxs, pos and dx are needed");
+  if (ld_dxs < 0 || (T > 1 && ld_dx < H)) return bad(fn, "negative stride, or rows of an output overlap");
+  return launched(fn, launch_combine_tokens(dtype, dxs, ld_dxs, rows, pos, nullptr, T, K, H, nullptr, 0, dx, ld_dx, (hipStream_t)stream));
+}
+
+int eff_combine_tokens(int dtype, const void* ys, int64_t ld_ys, int64_t rows, const int32_t* pos, const float* w, int64_t T,
+                       int K, int64_t H, const void* residual, int64_t ld_residual, void* out, int64_t ld_out,
+                       eff_stream_t stream) {
+  const char* fn = "eff_combine_tokens";
+  if (const char* why = check_rows(dtype, T, K, H, rows)) return bad(fn, why);
+  if (T == 0) return EFF_OK;
+  if ((!ys && rows > 0) || !pos || !w || !out) return bad(fn, "ys, pos, w and out are needed");
+  if (ld_ys < 0 || ld_residual < 0 || (T > 1 && ld_out < H)) return bad(fn, "negative stride, or rows of an output overlap");
+  return launched(fn, launch_combine_tokens(dtype, ys, ld_ys, rows, pos, w, T, K, H, residual, ld_residual, out, ld_out, (hipStream_t)stream));
+}
+
+int eff_combine_tokens_backward(int dtype, const void* dout, int64_t ld_dout, const void* ys, int64_t ld_ys, int64_t rows,
+                                const int32_t* pos, const float* w, int64_t T, int K, int64_t H, void* dys, int64_t ld_dys,
+                                float* dw, eff_stream_t stream) {
+  const char* fn = "eff_combine_tokens_backward";
+  if (const char* why = check_rows(dtype, T, K, H, rows)) return bad(fn, why);
+  if (T == 0) return EFF_OK;
+  if (!dout || !pos || !w || (rows > 0 && (!dys || (dw && !ys)))) return bad(fn, "dout, pos, w and dys are needed, ys for dw");
+  if (ld_dout < 0 || ld_ys < 0 || (rows > 1 && ld_dys < H)) return bad(fn, "negative stride, or rows of an output overlap");
+  return launched(fn, launch_combine_tokens_grad(dtype, dout, ld_dout, ys, ld_ys, rows, pos, w, T, K, H, dys, ld_dys, dw, (hipStream_t)stream));
+}
+
+}  // extern "C"

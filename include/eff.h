@@ -375,6 +375,94 @@ int eff_reset_stats(eff_engine* e);
 /* Device pointer of slot s (for tests: slot bytes must equal the host record). */
 int eff_slot_ptr(eff_engine* e, int slot, const void** out);
 
+/* ---- Operators around the routed step: dense products, tokens sorted by expert and back, experts' products.
+ *
+ * No engine: sizes, strides and pointers come with the call.  They only enqueue on `stream`, allocate nothing,
+ * wait for nothing and keep nothing from one call for the next, so they may be captured into a HIP graph; calls on
+ * different streams do not interfere (each has the caller's own workspace).  `stream` and every device pointer
+ * belong to the current device.  Matrices are row-major with unit stride inside a row and ld_* elements between
+ * rows.  Outputs must not overlap inputs or each other, except where stated.  Results do not depend on
+ * timing: no float atomics, fixed order of every sum for a given problem (sizes, types, alignment). */
+
+/* Types of these operators' tensors. */
+enum { EFF_DT_BF16 = 0, EFF_DT_F16 = 1, EFF_DT_F32 = 2 };
+
+/* Activations of a product's epilogue, z the product plus bias, in fp32. */
+enum {
+  EFF_ACT_NONE = 0,
+  EFF_ACT_SILU = 1,      /* z / (1 + exp(-z)) */
+  EFF_ACT_GELU = 2,      /* z * Phi(z) (erf) */
+  EFF_ACT_GELU_TANH = 3, /* z/2 * (1 + tanh(sqrt(2/pi) * (z + 0.044715 z^3))) */
+  EFF_ACT_SWIGLU = 4     /* W has 2n rows, gate then up: silu(gate) * up, the expert's own form ([Edge0]) */
+};
+
+/* One product y = act(x W^T + bias) + residual, or `groups` of them.  nw = 2n with EFF_ACT_SWIGLU, else n.
+ *   x [m,k], W [nw,k], bias [nw], residual [m,n], y [m,n], pre [m,nw] (z itself, for the backward pass)
+ * groups = 0: one W for every row.  groups = E >= 1: W is [E,nw,k], bias [E,nw], and rows offsets[e] ..
+ * offsets[e+1]-1 of x, residual, y and pre belong to W[e] (offsets: device int32 [E+1], ascending, as
+ * eff_sort_tokens writes them; values outside [0,m] are clamped).  Rows in no group are not read and their
+ * outputs are left as they were. */
+typedef struct eff_matmul_desc {
+  int32_t dtype;     /* x, W, bias, residual, pre and their gradients: EFF_DT_BF16 or EFF_DT_F16 */
+  int32_t out_dtype; /* y (and dy): dtype, or EFF_DT_F32 (router logits) */
+  int32_t act;       /* EFF_ACT_* */
+  int32_t groups;    /* 0, or 1..4096 */
+  int64_t m, n, k;   /* m >= 0; n, k >= 1; m, nw, k < 2^31 */
+  int64_t ld_x, ld_w, ld_y, ld_residual, ld_pre; /* ld_residual 0: one row for every row of y */
+  int64_t stride_w;  /* elements between two groups' W */
+  int64_t ld_dx, ld_dw, stride_dw; /* eff_matmul_backward's outputs */
+} eff_matmul_desc;
+
+/* Workspace bytes that eff_matmul (backward = 0) or eff_matmul_backward (1) needs for this problem at most, a
+ * multiple of 256, 0 if none; EFF_EINVAL for a bad description. */
+int64_t eff_matmul_workspace(const eff_matmul_desc* d, int backward);
+
+/* y (and pre if not NULL).  Products of the 16-bit values are exact and summed in fp32; bias, activation and
+ * residual are fp32; each output is rounded once.  y may be the residual itself (same pointer and ld).
+ * bias, residual, pre may be NULL; offsets only with groups; workspace: 256-byte aligned.
+ * Errors: EFF_EINVAL (nothing launched), EFF_EHIP. */
+int eff_matmul(const eff_matmul_desc* d, const void* x, const void* w, const void* bias, const void* residual,
+               const int32_t* offsets, void* y, void* pre, void* workspace, size_t workspace_bytes,
+               eff_stream_t stream);
+
+/* Gradients of eff_matmul, dz = dy * act'(pre):
+ *   dx [m,k] = dz W;   dw [nw,k] = dz^T x;   dbias [nw] = the sum of dz's rows;   the residual's is dy itself.
+ * With groups, each over the group's own rows (a group without rows: zeros); rows of dx in no group are left as
+ * they were.  dy has ld_y, pre ld_pre (needed unless EFF_ACT_NONE).  Outputs may be NULL; x is needed for dw, w for
+ * dx.  dz is rounded to dtype once where it enters dx and dw (fp32 in dbias).  m = 0 writes zeros to dw and dbias. */
+int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x, const void* w, const void* pre,
+                        const int32_t* offsets, void* dx, void* dw, void* dbias, void* workspace,
+                        size_t workspace_bytes, eff_stream_t stream);
+
+/* Tokens sorted by expert: a stable counting sort of the n = T*K routed pairs (pair t*K+k, ids as eff_route writes
+ * them).  offsets int32 [E+1]: expert e's pairs take places offsets[e] .. offsets[e+1]-1 in ascending pair order;
+ * order int32 [n]: the pair at a place (-1 behind offsets[E]); pos int32 [n]: the place of a pair.  An id outside
+ * [0,E) is unrouted (the -1 of a pair computed elsewhere): no place, pos = -1.  E <= 4096, 0 <= n < 2^31. */
+int64_t eff_sort_tokens_workspace(int64_t n, int num_experts);
+int eff_sort_tokens(const int32_t* ids, int64_t n, int num_experts, int32_t* offsets, int32_t* order, int32_t* pos,
+                    void* workspace, size_t workspace_bytes, eff_stream_t stream);
+
+/* Rows of T tokens and their places.  dtype: EFF_DT_* of the rows; K <= 32; pos int32 [T,K] as eff_sort_tokens
+ * writes it, every place at most once; a place outside [0,rows) is skipped like an unrouted pair.
+ * dispatch: xs[pos[t,k],:] = x[t,:].  Rows of xs without a pair are left as they were.
+ * backward: dx[t,:] = sum over k ascending of dxs[pos[t,k],:], fp32, rounded once (no pair: zeros). */
+int eff_dispatch_tokens(int dtype, const void* x, int64_t ld_x, const int32_t* pos, int64_t T, int K, int64_t H,
+                        void* xs, int64_t ld_xs, int64_t rows, eff_stream_t stream);
+int eff_dispatch_tokens_backward(int dtype, const void* dxs, int64_t ld_dxs, int64_t rows, const int32_t* pos,
+                                 int64_t T, int K, int64_t H, void* dx, int64_t ld_dx, eff_stream_t stream);
+
+/* combine: out[t,:] = residual[t,:] + sum over k ascending of w[t,k] * ys[pos[t,k],:], fp32, rounded once.
+ * w fp32 [T,K]; residual may be NULL (ld_residual 0: one row for all), and out may be the residual itself.
+ * Weights and rows of unrouted pairs are not used, whatever they hold.
+ * backward: dys[pos[t,k],:] = w[t,k] * dout[t,:] (other rows left as they were) and, if not NULL, dw fp32 [T,K] =
+ * <dout[t,:], ys[pos[t,k],:]> in fp32 (0 for an unrouted pair); the residual's gradient is dout itself. */
+int eff_combine_tokens(int dtype, const void* ys, int64_t ld_ys, int64_t rows, const int32_t* pos, const float* w,
+                       int64_t T, int K, int64_t H, const void* residual, int64_t ld_residual, void* out,
+                       int64_t ld_out, eff_stream_t stream);
+int eff_combine_tokens_backward(int dtype, const void* dout, int64_t ld_dout, const void* ys, int64_t ld_ys,
+                                int64_t rows, const int32_t* pos, const float* w, int64_t T, int K, int64_t H,
+                                void* dys, int64_t ld_dys, float* dw, eff_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
