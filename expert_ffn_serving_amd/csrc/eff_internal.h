@@ -354,6 +354,7 @@ struct MmArgs {
   void* pre;
   int64_t ldp;
   int dtype, y_f32, act, mode, groups;
+  int vec;  // set by launch_matmul: the epilogue's rows are whole 16-byte vectors
 };
 hipError_t launch_matmul(const MmArgs& a, hipStream_t s);
 

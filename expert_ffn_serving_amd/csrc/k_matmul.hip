@@ -4,8 +4,10 @@
 // (dz^T, x^T) differ in the strides of the two operands.  Products of 16-bit values are exact in fp32 and
 // the matrix cores add them in fp32; each output is rounded once.
 #include <algorithm>
+#include <atomic>
 
 #include "eff_internal.h"
+#include "lds_dma.h"
 
 namespace eff {
 namespace {
@@ -121,6 +123,71 @@ __device__ inline bool find_tile(const int32_t* offsets, int E, int64_t m, int t
 template <typename T>
 __device__ inline float ld(const void* p, int64_t i) { return (float)reinterpret_cast<const T*>(p)[i]; }
 
+// ---- epilogue of CL consecutive columns n.. of row m -----------------------------------------------------
+// z: the sums (SwiGLU: gate, u: up); nb: the group's place in bias; yo: its place in y.  With a.vec every row of
+// bias, residual, pre and y is a whole number of CL-wide vectors.
+
+template <typename T, int CL>
+__device__ inline void get_cl(const void* p, int64_t i, int left, bool vec, float* o) {
+  typedef T V __attribute__((ext_vector_type(CL)));
+  const T* s = reinterpret_cast<const T*>(p) + i;
+  if (vec) {
+    const V v = *reinterpret_cast<const V*>(s);
+#pragma unroll
+    for (int e = 0; e < CL; ++e) o[e] = (float)v[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < CL; ++e) o[e] = e < left ? (float)s[e] : 0.f;
+  }
+}
+template <typename T, int CL>
+__device__ inline void put_cl(void* p, int64_t i, int left, bool vec, const float* v) {
+  typedef T V __attribute__((ext_vector_type(CL)));
+  T* d = reinterpret_cast<T*>(p) + i;
+  if (vec) {
+    V o;
+#pragma unroll
+    for (int e = 0; e < CL; ++e) o[e] = (T)v[e];
+    *reinterpret_cast<V*>(d) = o;
+  } else {
+#pragma unroll
+    for (int e = 0; e < CL; ++e)
+      if (e < left) d[e] = (T)v[e];
+  }
+}
+
+template <typename T, int CL, bool GLU>
+__device__ inline void mm_finish(const MmArgs& a, int64_t m, int64_t n, int64_t nb, int64_t yo, float* z, float* u) {
+  if (n >= a.N) return;
+  const int left = (int)min((int64_t)CL, a.N - n);
+  const bool vec = a.vec;
+  float t[CL];
+  if (a.bias) {
+    get_cl<T, CL>(a.bias, nb + n, left, vec, t);
+#pragma unroll
+    for (int e = 0; e < CL; ++e) z[e] += t[e];
+    if (GLU) {
+      get_cl<T, CL>(a.bias, nb + a.N + n, left, vec, t);
+#pragma unroll
+      for (int e = 0; e < CL; ++e) u[e] += t[e];
+    }
+  }
+  if (a.pre) {
+    put_cl<T, CL>(a.pre, m * a.ldp + n, left, vec, z);
+    if (GLU) put_cl<T, CL>(a.pre, m * a.ldp + a.N + n, left, vec, u);
+  }
+#pragma unroll
+  for (int e = 0; e < CL; ++e) z[e] = GLU ? act_silu(z[e]) * u[e] : act_one(a.act, z[e]);
+  if (a.residual) {
+    get_cl<T, CL>(a.residual, m * a.ldr + n, left, vec, t);
+#pragma unroll
+    for (int e = 0; e < CL; ++e) z[e] += t[e];
+  }
+  const int64_t o = yo + m * a.ldy + n;
+  if (a.y_f32) put_cl<float, CL>(a.y, o, left, vec, z);
+  else put_cl<T, CL>(a.y, o, left, vec, z);
+}
+
 // ---- any strides, any alignment ------------------------------------------------------------------------
 // Workgroup = 64 rows x 64 columns (SwiGLU: 32 gate and 32 up columns), 4 waves of 32 x 32, 32 k at a time
 // staged through registers with every bound checked.
@@ -188,33 +255,253 @@ k_mm_any(MmArgs a) {
     __syncthreads();
   }
   // lane: row m = wm + 16 i + r, columns 16 j + 4 q + c of its wave
+  const int64_t nb = (int64_t)g * (GLU ? 2 * a.N : a.N);
+  const int64_t yo = a.mode == MM_K_GROUPS ? g * a.syg : 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int64_t m = m0 + wm + i * 16 + r;
     if (m >= m1) continue;
 #pragma unroll
-    for (int j = 0; j < (GLU ? 1 : 2); ++j)
+    for (int j = 0; j < (GLU ? 1 : 2); ++j) {
+      const int64_t n = GLU ? n0 + (wn >> 1) + 4 * q : n0 + wn + j * 16 + 4 * q;
+      float z[4], u[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int64_t n = GLU ? n0 + (wn >> 1) + 4 * q + c : n0 + wn + j * 16 + 4 * q + c;
-        if (n >= a.N) continue;
-        const int64_t nb = (int64_t)g * (GLU ? 2 * a.N : a.N);
-        float z = acc[i][j][c], y;
-        if (a.bias) z += ld<T>(a.bias, nb + n);
-        if (a.pre) reinterpret_cast<T*>(a.pre)[m * a.ldp + n] = (T)z;
-        if (GLU) {
-          float u = acc[i][1][c];
-          if (a.bias) u += ld<T>(a.bias, nb + a.N + n);
-          if (a.pre) reinterpret_cast<T*>(a.pre)[m * a.ldp + a.N + n] = (T)u;
-          y = act_silu(z) * u;
-        } else {
-          y = act_one(a.act, z);
-        }
-        if (a.residual) y += ld<T>(a.residual, m * a.ldr + n);
-        const int64_t o = (a.mode == MM_K_GROUPS ? g * a.syg : 0) + m * a.ldy + n;
-        if (a.y_f32) reinterpret_cast<float*>(a.y)[o] = y;
-        else reinterpret_cast<T*>(a.y)[o] = (T)y;
+        z[c] = acc[i][j][c];
+        if (GLU) u[c] = acc[i][1][c];
       }
+      mm_finish<T, 4, GLU>(a, m, n, nb, yo, z, u);
+    }
+  }
+}
+
+// ---- aligned operands: tiles through LDS ---------------------------------------------------------------
+//
+// Workgroup = BM rows x BN columns, WM x WN waves of (BM/WM) x (BN/WN), 64 k per step.  Both operands go to LDS by
+// direct 16-byte copies (no registers), S steps deep; one barrier per step.  An operand is either k-contiguous
+// (LDS: rows of 64 k) or contiguous along its own index (LDS: 64 k rows of BM or BN values, read back transposed by
+// ds_read_b64_tr_b16: lane l of a group of 16 gets value l%4 of the 8 bytes that lanes l/4, 4 + l/4, .. address).
+// A copy writes LDS in lane order, so bank conflicts are avoided by permuting which 16 bytes a lane fetches: chunk c
+// of a row sits at chunk c ^ f(row), f chosen so that the lanes that read together hit different banks.
+//
+// The weights are the matrix core's first operand, so a lane holds 4 consecutive columns of one row per product;
+// with k-contiguous weights the LDS rows are dealt to the products so that a lane's columns of all of them are
+// consecutive: whole 16-byte stores (and residual loads) in the epilogue.
+constexpr int kBK = 64;
+
+__device__ const uint4 g_zero16[1] = {{0u, 0u, 0u, 0u}};  // what a copy past the last k reads
+
+template <int N>
+__device__ inline void wait_and_meet() {
+  // this wave's copies but the last N are in LDS and its LDS reads are done; then all waves' are
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+template <typename T>
+struct Half4;
+template <>
+struct Half4<bf16_t> {
+  typedef bf16_t V __attribute__((ext_vector_type(4)));
+};
+template <>
+struct Half4<f16_t> {
+  typedef f16_t V __attribute__((ext_vector_type(4)));
+};
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ inline s16x4_t read_tr(const void* lds) {
+  typedef __attribute__((address_space(3))) s16x4_t* P;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)lds);
+}
+
+// 16-byte chunk `phys` of LDS row `row` holds the row's chunk phys ^ swizzle
+template <int GRP>  // k-contiguous operand whose row slices are read as 4 rows of each of 4 groups of GRP rows (1: 16 rows)
+__device__ inline int swz_rows(int row) {
+  return GRP == 1 ? row & 7 : (row & 3) | (((row / GRP) & 1) << 2);
+}
+// operand contiguous along its index, LDS row = k: pairs of chunks (32 bytes) move
+__device__ inline int swz_k(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+
+template <int BM_, int BN_, int WM_, int WN_, int S_>
+struct TileCfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, TH = 64 * WM_ * WN_;
+};
+
+template <typename T, class C, bool XK, bool WK, bool GLU>
+__global__ void __launch_bounds__(C::TH)
+k_mm_tile(MmArgs a) {
+  typedef typename Vec8<T>::V V8;
+  constexpr int BM = C::BM, BN = C::BN, S = C::S, TH = C::TH;
+  constexpr int TM = BM / C::WM, TN = BN / C::WN, MT = TM / 16, NT = TN / 16;
+  constexpr int HALVES = GLU ? 2 : 1, NTH = NT / HALVES, TNH = TN / HALVES, BNH = BN / HALVES;
+  constexpr int RUN = NTH * 4;                       // a lane's consecutive columns (k-contiguous weights)
+  constexpr int XB = BM * kBK * 2, WB = BN * kBK * 2, STEP = XB + WB;
+  constexpr int SX = BM * 8 / TH, SW = BN * 8 / TH;  // copies of one thread per step
+  static_assert(BM * 8 % TH == 0 && BN * 8 % TH == 0 && NT % HALVES == 0, "tile");
+  extern __shared__ __attribute__((aligned(128))) uint8_t s_tile[];
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % C::WM, wn = wave / C::WM;
+
+  // which tile
+  const int nt = (int)((a.N + BNH - 1) / BNH);
+  int g = 0, mt_i, nt_i;
+  int64_t m0, m1, k0 = 0, k1 = a.K;
+  if (a.mode == MM_ROW_GROUPS) {
+    mt_i = blockIdx.x / nt;
+    nt_i = blockIdx.x % nt;
+    const bool found = find_tile<BM, TH>(a.offsets, a.groups, a.M, mt_i, reinterpret_cast<int*>(s_tile), &g, &m0, &m1);
+    if (!found) return;
+    __syncthreads();
+  } else {
+    mt_i = blockIdx.x / nt;
+    nt_i = blockIdx.x % nt;
+    m0 = (int64_t)mt_i * BM;
+    m1 = min(a.M, m0 + BM);
+    if (a.mode == MM_K_GROUPS) {
+      g = blockIdx.y;
+      group_rows(a.offsets, g, a.K, &k0, &k1);
+    }
+  }
+  const int64_t n0 = (int64_t)nt_i * BNH;
+
+  // this thread's copies: source of step 0 and bytes between steps
+  const T* x = reinterpret_cast<const T*>(a.x);
+  const T* w = reinterpret_cast<const T*>(a.w) + (a.mode == MM_ROW_GROUPS ? g * a.swg : 0);
+  const char *px[SX], *pw[SW];
+  int kx[SX], kw[SW];  // the copy's first k inside a step
+#pragma unroll
+  for (int i = 0; i < SX; ++i) {
+    const int idx = i * TH + tid;
+    if (XK) {
+      const int row = idx >> 3, c = (idx & 7) ^ swz_rows<1>(row);
+      kx[i] = c * 8;
+      px[i] = reinterpret_cast<const char*>(x + min(m0 + row, m1 - 1) * a.sxm + k0 + c * 8);
+    } else {
+      constexpr int CH = BM / 8;
+      const int k = idx / CH, p = idx % CH, c = ((((p >> 1) ^ swz_k(k)) << 1) | (p & 1)) % CH;
+      kx[i] = k;
+      px[i] = reinterpret_cast<const char*>(x + (k0 + k) * a.sxk + min(m0 + c * 8, a.M - 8));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < SW; ++i) {
+    const int idx = i * TH + tid;
+    if (WK) {
+      const int row = idx >> 3, c = (idx & 7) ^ swz_rows<RUN>(row);
+      const int col = (row / TN) * TNH + (row % TNH);
+      const int64_t wr = min(n0 + col, a.N - 1) + (GLU && (row % TN) >= TNH ? a.N : 0);
+      kw[i] = c * 8;
+      pw[i] = reinterpret_cast<const char*>(w + wr * a.swn + k0 + c * 8);
+    } else {
+      constexpr int CH = BN / 8;
+      const int k = idx / CH, p = idx % CH, c = ((((p >> 1) ^ swz_k(k)) << 1) | (p & 1)) % CH;
+      kw[i] = k;
+      pw[i] = reinterpret_cast<const char*>(w + (k0 + k) * a.swk + min(n0 + c * 8, a.N - 8));
+    }
+  }
+  const int64_t stepx = XK ? kBK * 2 : a.sxk * (kBK * 2), stepw = WK ? kBK * 2 : a.swk * (kBK * 2);
+  const uint32_t lds0 = lds_address(s_tile);
+  const int64_t klen = k1 - k0;
+  const int steps = (int)((klen + kBK - 1) / kBK);
+
+  auto issue = [&](int t) {
+    const uint32_t base = lds0 + (t % S) * STEP + wave * 1024;
+    const int left = (int)min((int64_t)kBK, klen - (int64_t)t * kBK);
+    if (left == kBK) {
+#pragma unroll
+      for (int i = 0; i < SX; ++i) lds_copy16(px[i], base + i * (TH * 16));
+#pragma unroll
+      for (int i = 0; i < SW; ++i) lds_copy16(pw[i], base + XB + i * (TH * 16));
+    } else {
+      const char* zero = reinterpret_cast<const char*>(g_zero16);
+#pragma unroll
+      for (int i = 0; i < SX; ++i) lds_copy16(kx[i] < left ? px[i] : zero, base + i * (TH * 16));
+#pragma unroll
+      for (int i = 0; i < SW; ++i) lds_copy16(kw[i] < left ? pw[i] : zero, base + XB + i * (TH * 16));
+    }
+#pragma unroll
+    for (int i = 0; i < SX; ++i) px[i] += stepx;
+#pragma unroll
+    for (int i = 0; i < SW; ++i) pw[i] += stepw;
+  };
+
+  f32x4_t acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  auto frag_x = [&](const uint8_t* b, int i, int ks) -> V8 {
+    if (XK) {
+      const int row = wm * TM + i * 16 + r;
+      return *reinterpret_cast<const V8*>(b + row * 128 + (((ks * 4 + q) ^ swz_rows<1>(row)) << 4));
+    } else {
+      // lane: k row ks*32 + q*8 + r/4 (and + 4), columns 4 (r%4) of its 16
+      constexpr int CH = BM / 8;
+      const int k = ks * 32 + q * 8 + (r >> 2), col = wm * TM + i * 16 + (r & 3) * 4;
+      const int pair = ((col >> 4) ^ swz_k(k)) % (CH / 2);
+      const uint8_t* p = b + k * (BM * 2) + pair * 32 + (col & 15) * 2;
+      const s16x4_t lo = read_tr(p), hi = read_tr(p + 4 * (BM * 2));
+      return __builtin_bit_cast(V8, (s16x8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  };
+  auto frag_w = [&](const uint8_t* b, int j, int ks) -> V8 {
+    if (WK) {
+      const int row = wn * TN + (j / NTH) * TNH + (r >> 2) * RUN + (j % NTH) * 4 + (r & 3);
+      return *reinterpret_cast<const V8*>(b + XB + row * 128 + (((ks * 4 + q) ^ swz_rows<RUN>(row)) << 4));
+    } else {
+      constexpr int CH = BN / 8;
+      const int k = ks * 32 + q * 8 + (r >> 2), col = wn * TN + j * 16 + (r & 3) * 4;
+      const int pair = ((col >> 4) ^ swz_k(k)) % (CH / 2);
+      const uint8_t* p = b + XB + k * (BN * 2) + pair * 32 + (col & 15) * 2;
+      const s16x4_t lo = read_tr(p), hi = read_tr(p + 4 * (BN * 2));
+      return __builtin_bit_cast(V8, (s16x8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  };
+
+#pragma unroll
+  for (int t = 0; t < S - 1; ++t)
+    if (t < steps) issue(t);
+  for (int t = 0; t < steps; ++t) {
+    if (t + S - 2 < steps) wait_and_meet<(S - 2) * (SX + SW)>();
+    else wait_and_meet<0>();
+    if (t + S - 1 < steps) issue(t + S - 1);
+    const uint8_t* b = s_tile + (t % S) * STEP;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      V8 fw[NT], fx[MT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fw[j] = frag_w(b, j, ks);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fx[i] = frag_x(b, i, ks);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = mfma(fw[j], fx[i], acc[i][j]);
+    }
+  }
+
+  // epilogue: lane's rows wm*TM + 16 i + r; columns in runs of CL
+  constexpr int CL = WK && RUN % 8 == 0 ? 8 : 4, NC = NTH * 4 / CL;
+  const int64_t nb = (int64_t)g * (GLU ? 2 * a.N : a.N);
+  const int64_t yo = a.mode == MM_K_GROUPS ? g * a.syg : 0;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = m0 + wm * TM + i * 16 + r;
+    if (m >= m1) continue;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int64_t n = n0 + wn * TNH + (WK ? q * RUN + c * CL : c * 16 + q * 4);
+      float z[CL], u[CL];
+#pragma unroll
+      for (int e = 0; e < CL; ++e) {
+        z[e] = acc[i][(c * CL + e) / 4][e & 3];
+        if (GLU) u[e] = acc[i][NTH + (c * CL + e) / 4][e & 3];
+      }
+      mm_finish<T, CL, GLU>(a, m, n, nb, yo, z, u);
+    }
   }
 }
 
@@ -283,21 +570,75 @@ int64_t row_tiles(const MmArgs& a, int64_t BM) {
 // workgroups of one launch: their threads stay below 2^32
 constexpr int64_t kMaxTiles = (int64_t)1 << 22;
 
+bool aligned16(std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> sizes, int bytes) {
+  for (const void* p : ptrs)
+    if ((uintptr_t)p % 16) return false;
+  for (int64_t v : sizes)
+    if (v * bytes % 16) return false;
+  return true;
+}
+
+// lets a kernel use `bytes` of dynamic LDS, once per device (a bit each; calls may race, the attribute is the same)
+hipError_t allow_lds(const void* fn, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  const uint64_t bit = (uint64_t)1 << (dev & 63);
+  if (done->load(std::memory_order_acquire) & bit) return hipSuccess;
+  err = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == hipSuccess) done->fetch_or(bit, std::memory_order_release);
+  return err;
+}
+
+template <typename T, class C, bool XK, bool WK, bool GLU>
+hipError_t launch_tile_c(const MmArgs& a, hipStream_t s) {
+  const int64_t tiles = ceil_div(a.N, GLU ? C::BN / 2 : C::BN) * row_tiles(a, C::BM);
+  if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
+  constexpr int lds = C::S * (C::BM + C::BN) * kBK * 2;
+  auto* fn = &k_mm_tile<T, C, XK, WK, GLU>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t set = allow_lds(reinterpret_cast<const void*>(fn), lds, &done);
+  if (set != hipSuccess) return set;
+  hipLaunchKernelGGL(fn, dim3((unsigned)tiles, a.mode == MM_K_GROUPS ? (unsigned)a.groups : 1u), dim3(C::TH), lds, s, a);
+  return hipGetLastError();
+}
+
+template <typename T, bool XK, bool WK, bool GLU>
+hipError_t launch_tile(const MmArgs& a, hipStream_t s) {
+  typedef TileCfg<256, 256, 2, 4, 2> Big;
+  typedef TileCfg<128, 128, 2, 2, 2> Mid;
+  typedef TileCfg<64, 128, 1, 4, 3> Low;
+  const int64_t z = a.mode == MM_K_GROUPS ? a.groups : 1, n = GLU ? 2 * a.N : a.N;
+  const int64_t rows = a.mode == MM_ROW_GROUPS ? a.M / std::max<int64_t>(1, std::min<int64_t>(a.groups, a.M)) : a.M;
+  if (rows > 128 && ceil_div(rows, 256) * ceil_div(n, 256) * z >= 200) return launch_tile_c<T, Big, XK, WK, GLU>(a, s);
+  if (rows > 64) return launch_tile_c<T, Mid, XK, WK, GLU>(a, s);
+  return launch_tile_c<T, Low, XK, WK, GLU>(a, s);
+}
+
 }  // namespace
 
-hipError_t launch_matmul(const MmArgs& a, hipStream_t s) {
-  const bool glu = a.act == EFF_ACT_SWIGLU;
-  const int64_t tiles = ceil_div(a.N, glu ? kAnyBN / 2 : kAnyBN) * row_tiles(a, kAnyBM);
-  if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
-  const dim3 g((unsigned)tiles, a.mode == MM_K_GROUPS ? (unsigned)a.groups : 1u);
-  auto go = [&](auto t) {
+hipError_t launch_matmul(const MmArgs& in, hipStream_t s) {
+  MmArgs a = in;
+  const bool glu = a.act == EFF_ACT_SWIGLU, xk = a.sxk == 1, wk = a.swk == 1;
+  // 16-byte copies: aligned matrices whose contiguous side is whole vectors
+  const bool direct = aligned16({a.x, a.w}, {xk ? a.sxm : a.sxk, wk ? a.swn : a.swk, a.swg, xk ? a.K : 0, xk ? 0 : a.M, wk ? 0 : a.N}, 2) &&
+                      (xk || !wk);
+  a.vec = aligned16({a.y, a.bias, a.residual, a.pre}, {a.N, a.ldy, a.syg, a.residual ? a.ldr : 0, a.pre ? a.ldp : 0}, 2);
+  auto go = [&](auto t) -> hipError_t {
     typedef decltype(t) T;
+    if (direct) {
+      if (xk && wk) return glu ? launch_tile<T, true, true, true>(a, s) : launch_tile<T, true, true, false>(a, s);
+      if (xk) return launch_tile<T, true, false, false>(a, s);
+      return launch_tile<T, false, false, false>(a, s);
+    }
+    const int64_t tiles = ceil_div(a.N, glu ? kAnyBN / 2 : kAnyBN) * row_tiles(a, kAnyBM);
+    if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
+    const dim3 g((unsigned)tiles, a.mode == MM_K_GROUPS ? (unsigned)a.groups : 1u);
     if (glu) hipLaunchKernelGGL((k_mm_any<T, true>), g, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_mm_any<T, false>), g, dim3(256), 0, s, a);
+    return hipGetLastError();
   };
-  if (a.dtype == EFF_DT_BF16) go(bf16_t{});
-  else go(f16_t{});
-  return hipGetLastError();
+  return a.dtype == EFF_DT_BF16 ? go(bf16_t{}) : go(f16_t{});
 }
 
 hipError_t launch_matmul_dz(const MmGrad& a, hipStream_t s) {
