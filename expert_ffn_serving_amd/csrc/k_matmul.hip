@@ -287,26 +287,15 @@ k_mm_any(MmArgs a) {
 // The weights are the matrix core's first operand, so a lane holds 4 consecutive columns of one row per product;
 // with k-contiguous weights the LDS rows are dealt to the products so that a lane's columns of all of them are
 // consecutive: whole 16-byte stores (and residual loads) in the epilogue.
-constexpr int kBK = 64;
-
 __device__ const uint4 g_zero16[1] = {{0u, 0u, 0u, 0u}};  // what a copy past the last k reads
 
-template <int N>
-__device__ inline void wait_and_meet() {
-  // this wave's copies but the last N are in LDS and its LDS reads are done; then all waves' are
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+// this wave's LDS reads are done, then every wave's; nothing moves across
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
-template <typename T>
-struct Half4;
-template <>
-struct Half4<bf16_t> {
-  typedef bf16_t V __attribute__((ext_vector_type(4)));
-};
-template <>
-struct Half4<f16_t> {
-  typedef f16_t V __attribute__((ext_vector_type(4)));
-};
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 
@@ -316,29 +305,42 @@ __device__ inline s16x4_t read_tr(const void* lds) {
 }
 
 // 16-byte chunk `phys` of LDS row `row` holds the row's chunk phys ^ swizzle
-template <int GRP>  // k-contiguous operand whose row slices are read as 4 rows of each of 4 groups of GRP rows (1: 16 rows)
+// (k-contiguous operand of BK k a row, whose rows are read 16 at a time, as 4 rows of each of 4 runs of GRP rows with
+// GRP > 1: 8 lanes hit 8 different 16-byte places of the 128 bytes of all banks)
+template <int BK, int GRP>
 __device__ inline int swz_rows(int row) {
+  if (BK == 32) return GRP == 1 ? (row >> 1) & 3 : ((row >> 1) & 1) | (((row / GRP) & 1) << 1);
   return GRP == 1 ? row & 7 : (row & 3) | (((row / GRP) & 1) << 2);
 }
 // operand contiguous along its index, LDS row = k: pairs of chunks (32 bytes) move
 __device__ inline int swz_k(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
 
-template <int BM_, int BN_, int WM_, int WN_, int S_>
+// BM x BN tile, WM x WN waves, BK k per step, S steps in LDS; PP: two groups of 4 waves take turns (below)
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_, bool PP_>
 struct TileCfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_, TH = 64 * WM_ * WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_, TH = 64 * WM_ * WN_;
+  static constexpr bool PP = PP_;
 };
+
+// subtiles of 16 rows per wave that the epilogue's LDS holds at once
+template <class C>
+constexpr int rows_fit(int mt) {
+  int ip = mt;
+  while (ip > 1 && C::WM * 16 * ip * (C::BN + 4) * 4 > C::S * (C::BM + C::BN) * C::BK * 2) ip /= 2;
+  return ip;
+}
 
 template <typename T, class C, bool XK, bool WK, bool GLU>
 __global__ void __launch_bounds__(C::TH)
 k_mm_tile(MmArgs a) {
   typedef typename Vec8<T>::V V8;
-  constexpr int BM = C::BM, BN = C::BN, S = C::S, TH = C::TH;
+  constexpr int BM = C::BM, BN = C::BN, S = C::S, TH = C::TH, BK = C::BK, KS = BK / 32, CK = BK / 8;
   constexpr int TM = BM / C::WM, TN = BN / C::WN, MT = TM / 16, NT = TN / 16;
   constexpr int HALVES = GLU ? 2 : 1, NTH = NT / HALVES, TNH = TN / HALVES, BNH = BN / HALVES;
   constexpr int RUN = NTH * 4;                       // a lane's consecutive columns (k-contiguous weights)
-  constexpr int XB = BM * kBK * 2, WB = BN * kBK * 2, STEP = XB + WB;
-  constexpr int SX = BM * 8 / TH, SW = BN * 8 / TH;  // copies of one thread per step
-  static_assert(BM * 8 % TH == 0 && BN * 8 % TH == 0 && NT % HALVES == 0, "tile");
+  constexpr int XB = BM * BK * 2, WB = BN * BK * 2, STEP = XB + WB;
+  constexpr int SX = BM * CK / TH, SW = BN * CK / TH, CP = SX + SW;  // copies of one thread per step
+  static_assert(BM * CK % TH == 0 && BN * CK % TH == 0 && NT % HALVES == 0, "tile");
   extern __shared__ __attribute__((aligned(128))) uint8_t s_tile[];
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -375,7 +377,7 @@ k_mm_tile(MmArgs a) {
   for (int i = 0; i < SX; ++i) {
     const int idx = i * TH + tid;
     if (XK) {
-      const int row = idx >> 3, c = (idx & 7) ^ swz_rows<1>(row);
+      const int row = idx / CK, c = (idx % CK) ^ swz_rows<BK, 1>(row);
       kx[i] = c * 8;
       px[i] = reinterpret_cast<const char*>(x + min(m0 + row, m1 - 1) * a.sxm + k0 + c * 8);
     } else {
@@ -389,7 +391,7 @@ k_mm_tile(MmArgs a) {
   for (int i = 0; i < SW; ++i) {
     const int idx = i * TH + tid;
     if (WK) {
-      const int row = idx >> 3, c = (idx & 7) ^ swz_rows<RUN>(row);
+      const int row = idx / CK, c = (idx % CK) ^ swz_rows<BK, RUN>(row);
       const int col = (row / TN) * TNH + (row % TNH);
       const int64_t wr = min(n0 + col, a.N - 1) + (GLU && (row % TN) >= TNH ? a.N : 0);
       kw[i] = c * 8;
@@ -401,15 +403,15 @@ k_mm_tile(MmArgs a) {
       pw[i] = reinterpret_cast<const char*>(w + (k0 + k) * a.swk + min(n0 + c * 8, a.N - 8));
     }
   }
-  const int64_t stepx = XK ? kBK * 2 : a.sxk * (kBK * 2), stepw = WK ? kBK * 2 : a.swk * (kBK * 2);
+  const int64_t stepx = XK ? BK * 2 : a.sxk * (BK * 2), stepw = WK ? BK * 2 : a.swk * (BK * 2);
   const uint32_t lds0 = lds_address(s_tile);
   const int64_t klen = k1 - k0;
-  const int steps = (int)((klen + kBK - 1) / kBK);
+  const int steps = (int)((klen + BK - 1) / BK);
 
   auto issue = [&](int t) {
     const uint32_t base = lds0 + (t % S) * STEP + wave * 1024;
-    const int left = (int)min((int64_t)kBK, klen - (int64_t)t * kBK);
-    if (left == kBK) {
+    const int left = (int)min((int64_t)BK, klen - (int64_t)t * BK);
+    if (left == BK) {
 #pragma unroll
       for (int i = 0; i < SX; ++i) lds_copy16(px[i], base + i * (TH * 16));
 #pragma unroll
@@ -436,7 +438,7 @@ k_mm_tile(MmArgs a) {
   auto frag_x = [&](const uint8_t* b, int i, int ks) -> V8 {
     if (XK) {
       const int row = wm * TM + i * 16 + r;
-      return *reinterpret_cast<const V8*>(b + row * 128 + (((ks * 4 + q) ^ swz_rows<1>(row)) << 4));
+      return *reinterpret_cast<const V8*>(b + row * (BK * 2) + (((ks * 4 + q) ^ swz_rows<BK, 1>(row)) << 4));
     } else {
       // lane: k row ks*32 + q*8 + r/4 (and + 4), columns 4 (r%4) of its 16
       constexpr int CH = BM / 8;
@@ -450,7 +452,7 @@ k_mm_tile(MmArgs a) {
   auto frag_w = [&](const uint8_t* b, int j, int ks) -> V8 {
     if (WK) {
       const int row = wn * TN + (j / NTH) * TNH + (r >> 2) * RUN + (j % NTH) * 4 + (r & 3);
-      return *reinterpret_cast<const V8*>(b + XB + row * 128 + (((ks * 4 + q) ^ swz_rows<RUN>(row)) << 4));
+      return *reinterpret_cast<const V8*>(b + XB + row * (BK * 2) + (((ks * 4 + q) ^ swz_rows<BK, RUN>(row)) << 4));
     } else {
       constexpr int CH = BN / 8;
       const int k = ks * 32 + q * 8 + (r >> 2), col = wn * TN + j * 16 + (r & 3) * 4;
@@ -461,46 +463,105 @@ k_mm_tile(MmArgs a) {
     }
   };
 
+  V8 fw[NT], fx[MT];
+  auto read = [&](int t, int ks) {
+    const uint8_t* b = s_tile + (t % S) * STEP;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fw[j] = frag_w(b, j, ks);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) fx[i] = frag_x(b, i, ks);
+  };
+  auto multiply = [&] {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = mfma(fw[j], fx[i], acc[i][j]);
+  };
+  // this wave's copies of every step up to the last CP * N issued ones are in LDS
+  auto arrived = [&](bool all) {
+    if (all) vm_wait<0>();
+    else vm_wait<(S - 2) * CP>();
+  };
+
 #pragma unroll
   for (int t = 0; t < S - 1; ++t)
     if (t < steps) issue(t);
-  for (int t = 0; t < steps; ++t) {
-    if (t + S - 2 < steps) wait_and_meet<(S - 2) * (SX + SW)>();
-    else wait_and_meet<0>();
-    if (t + S - 1 < steps) issue(t + S - 1);
-    const uint8_t* b = s_tile + (t % S) * STEP;
+  if constexpr (C::PP) {
+    // Two groups of 4 waves, one of each on every SIMD, half a step apart: while one group multiplies (at raised
+    // priority) the other reads its next operands from LDS and issues copies.  A barrier ends each half.
+    static_assert(TH == 512, "two groups of 4 waves");
+    const bool second = wave >= 4;
+    arrived(S - 1 > steps);
+    meet();
+    if (second) meet();
+    for (int t = 0; t < steps; ++t) {
+      const bool tail = t + S - 1 >= steps;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      V8 fw[NT], fx[MT];
+      for (int ks = 0; ks < KS; ++ks) {
+        if (ks == 0 && !tail) issue(t + S - 1);
+        read(t, ks);
+        if (ks == KS - 1 && second) arrived(tail);
+        meet();
+        __builtin_amdgcn_s_setprio(1);
+        multiply();
+        __builtin_amdgcn_s_setprio(0);
+        if (ks == KS - 1 && !second) arrived(tail);
+        meet();
+      }
+    }
+    if (!second) meet();
+  } else {
+    for (int t = 0; t < steps; ++t) {
+      arrived(t + S - 1 > steps);
+      meet();
+      if (t + S - 1 < steps) issue(t + S - 1);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) fw[j] = frag_w(b, j, ks);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fx[i] = frag_x(b, i, ks);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mfma(fw[j], fx[i], acc[i][j]);
+      for (int ks = 0; ks < KS; ++ks) {
+        read(t, ks);
+        multiply();
+      }
     }
   }
 
-  // epilogue: lane's rows wm*TM + 16 i + r; columns in runs of CL
-  constexpr int CL = WK && RUN % 8 == 0 ? 8 : 4, NC = NTH * 4 / CL;
+  // Epilogue through LDS, RP rows at a time: the sums change from the matrix core's layout to whole rows, so that
+  // bias, residual, pre and y move as 16-byte vectors, a row's side by side.
+  constexpr int LDC = BN + 4;
+  constexpr int IP = rows_fit<C>(MT) ;
+  constexpr int RP = C::WM * 16 * IP, VR = BNH / 8, ROUND = TH / VR;
+  static_assert(TH % VR == 0 && RP % ROUND == 0, "rows of a round");
+  float* s_c = reinterpret_cast<float*>(s_tile);
   const int64_t nb = (int64_t)g * (GLU ? 2 * a.N : a.N);
   const int64_t yo = a.mode == MM_K_GROUPS ? g * a.syg : 0;
+  const int64_t n = n0 + (tid % VR) * 8;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t m = m0 + wm * TM + i * 16 + r;
-    if (m >= m1) continue;
+  for (int p = 0; p < MT / IP; ++p) {
+    meet();
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t n = n0 + wn * TNH + (WK ? q * RUN + c * CL : c * 16 + q * 4);
-      float z[CL], u[CL];
+    for (int i = 0; i < IP; ++i)
 #pragma unroll
-      for (int e = 0; e < CL; ++e) {
-        z[e] = acc[i][(c * CL + e) / 4][e & 3];
-        if (GLU) u[e] = acc[i][NTH + (c * CL + e) / 4][e & 3];
+      for (int j = 0; j < NT; ++j) {
+        const int col = (j / NTH) * BNH + wn * TNH + (WK ? q * RUN + (j % NTH) * 4 : (j % NTH) * 16 + q * 4);
+        *reinterpret_cast<f32x4_t*>(s_c + ((wm * IP + i) * 16 + r) * LDC + col) = acc[p * IP + i][j];
       }
-      mm_finish<T, CL, GLU>(a, m, n, nb, yo, z, u);
+    meet();
+#pragma unroll 1
+    for (int rr = tid / VR; rr < RP; rr += ROUND) {
+      const int64_t m = m0 + (rr / (16 * IP)) * TM + p * (16 * IP) + rr % (16 * IP);
+      if (m >= m1) continue;
+      const float* c = s_c + rr * LDC + (tid % VR) * 8;
+      float z[8], u[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(c + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[4 * h + e] = v[e];
+        if (GLU) {
+          const f32x4_t v2 = *reinterpret_cast<const f32x4_t*>(c + BNH + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u[4 * h + e] = v2[e];
+        }
+      }
+      mm_finish<T, 8, GLU>(a, m, n, nb, yo, z, u);
     }
   }
 }
@@ -594,7 +655,7 @@ template <typename T, class C, bool XK, bool WK, bool GLU>
 hipError_t launch_tile_c(const MmArgs& a, hipStream_t s) {
   const int64_t tiles = ceil_div(a.N, GLU ? C::BN / 2 : C::BN) * row_tiles(a, C::BM);
   if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
-  constexpr int lds = C::S * (C::BM + C::BN) * kBK * 2;
+  constexpr int lds = C::S * (C::BM + C::BN) * C::BK * 2;
   auto* fn = &k_mm_tile<T, C, XK, WK, GLU>;
   static std::atomic<uint64_t> done{0};
   const hipError_t set = allow_lds(reinterpret_cast<const void*>(fn), lds, &done);
@@ -605,9 +666,9 @@ hipError_t launch_tile_c(const MmArgs& a, hipStream_t s) {
 
 template <typename T, bool XK, bool WK, bool GLU>
 hipError_t launch_tile(const MmArgs& a, hipStream_t s) {
-  typedef TileCfg<256, 256, 2, 4, 2> Big;
-  typedef TileCfg<128, 128, 2, 2, 2> Mid;
-  typedef TileCfg<64, 128, 1, 4, 3> Low;
+  typedef TileCfg<256, 256, 2, 4, 64, 2, true> Big;
+  typedef TileCfg<128, 128, 2, 2, 64, 2, false> Mid;
+  typedef TileCfg<64, 128, 1, 4, 64, 3, false> Low;
   const int64_t z = a.mode == MM_K_GROUPS ? a.groups : 1, n = GLU ? 2 * a.N : a.N;
   const int64_t rows = a.mode == MM_ROW_GROUPS ? a.M / std::max<int64_t>(1, std::min<int64_t>(a.groups, a.M)) : a.M;
   if (rows > 128 && ceil_div(rows, 256) * ceil_div(n, 256) * z >= 200) return launch_tile_c<T, Big, XK, WK, GLU>(a, s);
