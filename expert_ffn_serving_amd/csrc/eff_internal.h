@@ -354,11 +354,13 @@ struct MmArgs {
   void* pre;
   int64_t ldp;
   int dtype, y_f32, act, mode, groups;
-  int vec;  // set by launch_matmul: the epilogue's rows are whole 16-byte vectors
+  int x_padded;  // every row of x in memory is zero up to a multiple of 8 values
+  int vec;       // set by launch_matmul: the epilogue's rows are whole 16-byte vectors
 };
 hipError_t launch_matmul(const MmArgs& a, hipStream_t s);
 
-// dz = dy * act'(pre) [M, N or 2N] rounded to dtype (dz null: not written) and its column sums per group (dbias null: none)
+// dz = dy * act'(pre) [M, N or 2N] rounded to dtype (dz null: not written), its rows zeroed up to lddz, and its column
+// sums per group (part and dbias null: none; part: matmul_dz_tiles rows of fp32)
 struct MmGrad {
   const void* dy;
   int64_t ldy;
@@ -366,11 +368,13 @@ struct MmGrad {
   int64_t ldp;
   void* dz;
   int64_t lddz;
+  float* part;
   void* dbias;
   const int32_t* offsets;
-  int64_t M, N;
+  int64_t M, N, tiles;
   int dtype, dy_f32, act, groups;
 };
+int64_t matmul_dz_tiles(int64_t M, int groups);
 hipError_t launch_matmul_dz(const MmGrad& a, hipStream_t s);
 
 int64_t sort_workspace(int64_t n, int E);

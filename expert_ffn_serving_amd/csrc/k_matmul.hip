@@ -120,6 +120,53 @@ __device__ inline bool find_tile(const int32_t* offsets, int E, int64_t m, int t
   return *group >= 0;
 }
 
+// Prefix sums of the groups' tile counts into pre[0..E] (16 ints behind them are scratch); returns their number.
+// Every thread of the workgroup takes part.
+template <int BM>
+__device__ inline int group_prefix(const int32_t* offsets, int E, int64_t m, int* pre) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nt = blockDim.x;
+  int* s = pre + E + 1;
+  int run = 0;
+  for (int e0 = 0; e0 < E; e0 += nt) {
+    const int e = e0 + tid;
+    int mine = 0;
+    if (e < E) {
+      int64_t lo, hi;
+      group_rows(offsets, e, m, &lo, &hi);
+      mine = (int)((hi - lo + BM - 1) / BM);
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 63) s[wave] = incl;
+    __syncthreads();
+    int before = run, all = 0;
+    for (int i = 0; i < nt >> 6; ++i) {
+      before += i < wave ? s[i] : 0;
+      all += s[i];
+    }
+    if (e < E) pre[e] = before + incl - mine;
+    run += all;
+    __syncthreads();
+  }
+  if (tid == 0) pre[E] = run;
+  __syncthreads();
+  return run;
+}
+// the group that tile `t` < pre[E] belongs to: the last e with pre[e] <= t
+__device__ inline int group_of_tile(const int* pre, int E, int t) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
 template <typename T>
 __device__ inline float ld(const void* p, int64_t i) { return (float)reinterpret_cast<const T*>(p)[i]; }
 
@@ -371,6 +418,7 @@ k_mm_tile(MmArgs a) {
   // this thread's copies: source of step 0 and bytes between steps
   const T* x = reinterpret_cast<const T*>(a.x);
   const T* w = reinterpret_cast<const T*>(a.w) + (a.mode == MM_ROW_GROUPS ? g * a.swg : 0);
+  const int64_t xcols = a.x_padded ? (a.M + 7) & ~(int64_t)7 : a.M;  // x contiguous along m
   const char *px[SX], *pw[SW];
   int kx[SX], kw[SW];  // the copy's first k inside a step
 #pragma unroll
@@ -384,7 +432,7 @@ k_mm_tile(MmArgs a) {
       constexpr int CH = BM / 8;
       const int k = idx / CH, p = idx % CH, c = ((((p >> 1) ^ swz_k(k)) << 1) | (p & 1)) % CH;
       kx[i] = k;
-      px[i] = reinterpret_cast<const char*>(x + (k0 + k) * a.sxk + min(m0 + c * 8, a.M - 8));
+      px[i] = reinterpret_cast<const char*>(x + (k0 + k) * a.sxk + min(m0 + c * 8, xcols - 8));
     }
   }
 #pragma unroll
@@ -566,59 +614,232 @@ k_mm_tile(MmArgs a) {
   }
 }
 
+// ---- few rows --------------------------------------------------------------------------------------------
+//
+// Up to 16 MT rows of x against 16 rows of W per workgroup (SwiGLU: 8 gate and 8 up rows), the k split over its waves:
+// bound by the stream of W, so every wave keeps U chunks of 64 k (2 KiB of W each) in flight in registers and nothing
+// waits for a barrier before the end, where the waves' sums meet in LDS in wave order.  The lane of W row r and k group
+// q takes 32 consecutive bytes of a chunk: k = 16 q .. 16 q + 15 (the order of k inside a product is free as long as
+// both operands share it), so a chunk is one 128-byte line of every row.
+// With groups the workgroups walk the groups' tiles by themselves (prefix sums of the tile counts in LDS), so none
+// is launched for tiles that do not exist.
+template <int MT>
+constexpr int few_unroll() { return MT == 1 ? 4 : 2; }
+
+template <typename T, int MT, bool GLU>
+__global__ void __launch_bounds__(1024)
+k_mm_few(MmArgs a, int slices) {
+  typedef typename Vec8<T>::V V8;
+  constexpr int U = few_unroll<MT>(), BM = 16 * MT;
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_few[];
+  f32x4_t* s_acc = reinterpret_cast<f32x4_t*>(s_few);                       // [waves][MT][64]
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+  int* s_pre = reinterpret_cast<int*>(s_few + waves * MT * 1024);           // groups + 1 prefix sums, 16 more
+  const bool grouped = a.mode == MM_ROW_GROUPS;
+  int64_t tiles = grouped ? 0 : (a.M + BM - 1) / BM;
+  if (grouped) tiles = group_prefix<BM>(a.offsets, a.groups, a.M, s_pre);
+  const T* x = reinterpret_cast<const T*>(a.x);
+  const int K = (int)a.K, chunks = (K + 63) / 64;
+
+  for (int64_t job = blockIdx.x; job < tiles * slices; job += gridDim.x) {
+    const int tile = (int)(job / slices), n0 = (int)(job % slices) * (GLU ? 8 : 16);
+    int g = 0;
+    int64_t m0 = (int64_t)tile * BM, m1 = min(a.M, m0 + BM);
+    if (grouped) {
+      g = group_of_tile(s_pre, a.groups, tile);
+      int64_t lo, hi;
+      group_rows(a.offsets, g, a.M, &lo, &hi);
+      m0 = lo + (int64_t)(tile - s_pre[g]) * BM;
+      m1 = min(hi, m0 + BM);
+    }
+    const int64_t col = min((int64_t)n0 + (GLU ? r & 7 : r), a.N - 1);
+    const T* w = reinterpret_cast<const T*>(a.w) + g * a.swg + (col + (GLU && r >= 8 ? a.N : 0)) * a.swn + q * 16;
+    const T* xr[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) xr[i] = x + min(m0 + i * 16 + r, m1 - 1) * a.sxm + q * 16;
+    f32x4_t acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    V8 fw[U][2], fx[U][MT][2];
+    // chunk c of this wave's into slot s; past the end the first chunk again (not used)
+    auto load = [&](int c, int s) {
+      const int k = c < chunks ? c * 64 : 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int kk = k + q * 16 + h * 8 < K ? k + h * 8 : -(q * 16);      // past the last k: the row's first values
+        fw[s][h] = *reinterpret_cast<const V8*>(w + kk);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) fx[s][i][h] = *reinterpret_cast<const V8*>(xr[i] + kk);
+      }
+    };
+    auto use = [&](int c, int s) {
+      if (c >= chunks) return;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (c * 64 + 64 > K && c * 64 + q * 16 + h * 8 >= K) {              // nothing there: zeros on both sides
+          fw[s][h] = V8{};
+#pragma unroll
+          for (int i = 0; i < MT; ++i) fx[s][i][h] = V8{};
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i] = mfma(fw[s][h], fx[s][i][h], acc[i]);
+      }
+    };
+#pragma unroll
+    for (int s = 0; s < U; ++s) load(wave + s * waves, s);
+    for (int c = wave; c < chunks; c += U * waves) {
+#pragma unroll
+      for (int s = 0; s < U; ++s) {
+        use(c + s * waves, s);
+        load(c + (s + U) * waves, s);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) s_acc[(wave * MT + i) * 64 + lane] = acc[i];
+    __syncthreads();
+    // one wave per 16 rows of x: lane's row m = r, W rows 4 q .. 4 q + 3 of the slice
+    for (int i = wave; i < MT; i += waves) {
+      f32x4_t sum = s_acc[i * 64 + lane];
+      for (int v = 1; v < waves; ++v) sum += s_acc[(v * MT + i) * 64 + lane];
+      float z[4], u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        z[e] = sum[e];
+        if (GLU) u[e] = __shfl_down(z[e], 32);
+      }
+      const int64_t m = m0 + i * 16 + r;
+      if (m < m1 && (!GLU || q < 2)) mm_finish<T, 4, GLU>(a, m, n0 + 4 * q, (int64_t)g * (GLU ? 2 * a.N : a.N), 0, z, u);
+    }
+    __syncthreads();
+  }
+}
+
 // ---- dz and dbias --------------------------------------------------------------------------------------
+//
+// One pass over dy and pre: a workgroup takes 64 rows of one group and 64 VEC columns, each of its 4 waves every
+// fourth row.  It writes dz rounded to T (the operand that dx and dw multiply; columns up to lddz are zeroed, so that
+// dz's rows are whole 16-byte vectors) and the columns' fp32 sums over its rows, which a second kernel adds up in row
+// order.  Bound by HBM: every value is read once and written once.
+constexpr int kDzRows = 64;
 
-// dz = dy * act'(pre) at (m, n) in fp32; SwiGLU: the gate's and the up's
-template <typename T, typename D>
-__device__ inline float dz_at(const MmGrad& a, int64_t m, int64_t n, float* up) {
-  const float d = ld<D>(a.dy, m * a.ldy + n);
-  if (a.act == EFF_ACT_SWIGLU) {
-    const float gate = ld<T>(a.pre, m * a.ldp + n), u = ld<T>(a.pre, m * a.ldp + a.N + n);
-    *up = d * act_silu(gate);
-    return d * u * dact_silu(gate);
+template <typename T, int VEC>
+__device__ inline void load_row(const void* p, int64_t i, float* o) {
+  if constexpr (VEC == 1) {
+    o[0] = (float)reinterpret_cast<const T*>(p)[i];
+  } else {
+    typedef T V __attribute__((ext_vector_type(VEC)));
+    const V v = *reinterpret_cast<const V*>(reinterpret_cast<const T*>(p) + i);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = (float)v[e];
   }
-  return a.act == EFF_ACT_NONE ? d : d * dact_one(a.act, ld<T>(a.pre, m * a.ldp + n));
+}
+template <typename T, int VEC>
+__device__ inline void store_row(void* p, int64_t i, const float* v) {
+  if constexpr (VEC == 1) {
+    reinterpret_cast<T*>(p)[i] = (T)v[0];
+  } else {
+    typedef T V __attribute__((ext_vector_type(VEC)));
+    V o;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = (T)v[e];
+    *reinterpret_cast<V*>(reinterpret_cast<T*>(p) + i) = o;
+  }
 }
 
-// grid: (ceil(N / 256), rows).  dz rounded to T: the operand that dx and dw multiply.
-template <typename T, typename D>
+template <typename T, typename D, int VEC>
 __global__ void __launch_bounds__(256)
-k_mm_dz(MmGrad a) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= a.N) return;
-  T* dz = reinterpret_cast<T*>(a.dz);
-  for (int64_t m = blockIdx.y; m < a.M; m += gridDim.y) {
-    float up = 0.f;
-    const float v = dz_at<T, D>(a, m, n, &up);
-    dz[m * a.lddz + n] = (T)v;
-    if (a.act == EFF_ACT_SWIGLU) dz[m * a.lddz + a.N + n] = (T)up;
+k_mm_dz(MmGrad a, int cols) {
+  __shared__ float s_sum[2][4][64][VEC];
+  __shared__ int s_f[8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tile = blockIdx.x / cols;
+  const int64_t n = ((int64_t)(blockIdx.x % cols) * 64 + lane) * VEC;
+  int g;
+  int64_t m0 = (int64_t)tile * kDzRows, m1 = min(a.M, m0 + kDzRows);
+  if (a.offsets && !find_tile<kDzRows, 256>(a.offsets, a.groups, a.M, tile, s_f, &g, &m0, &m1)) return;
+  const bool glu = a.act == EFF_ACT_SWIGLU;
+  const int64_t nw = glu ? 2 * a.N : a.N;
+  float sum[VEC], sup[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) sum[e] = sup[e] = 0.f;
+  if (n < a.N)
+    for (int64_t m = m0 + wave; m < m1; m += 4) {
+      float d[VEC], z[VEC], u[VEC];
+      load_row<D, VEC>(a.dy, m * a.ldy + n, d);
+      if (a.act != EFF_ACT_NONE) {
+        load_row<T, VEC>(a.pre, m * a.ldp + n, z);
+        if (glu) {
+          load_row<T, VEC>(a.pre, m * a.ldp + a.N + n, u);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float up = d[e] * act_silu(z[e]);
+            d[e] = d[e] * u[e] * dact_silu(z[e]);
+            u[e] = up;
+            sup[e] += up;
+          }
+          if (a.dz) store_row<T, VEC>(a.dz, m * a.lddz + a.N + n, u);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) d[e] *= dact_one(a.act, z[e]);
+        }
+      }
+      if (a.dz) store_row<T, VEC>(a.dz, m * a.lddz + n, d);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum[e] += d[e];
+    }
+  // the zeros behind a row
+  if (a.dz && blockIdx.x % cols == 0 && nw + lane < a.lddz)
+    for (int64_t m = m0 + wave; m < m1; m += 4) reinterpret_cast<T*>(a.dz)[m * a.lddz + nw + lane] = (T)0.f;
+  if (!a.part) return;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    s_sum[0][wave][lane][e] = sum[e];
+    s_sum[1][wave][lane][e] = sup[e];
+  }
+  __syncthreads();
+  const int h = wave;   // wave 0: the sums, wave 1: SwiGLU's second half
+  if (h > (glu ? 1 : 0) || n >= a.N) return;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    float v = s_sum[h][0][lane][e];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) v += s_sum[h][w][lane][e];
+    a.part[(int64_t)tile * nw + h * a.N + n + e] = v;
   }
 }
 
-// grid: (ceil(N / 64), groups).  Column sums of dz over the group's rows: 4 waves take every fourth row, then
-// their sums meet in wave order.
-template <typename T, typename D>
+// grid: (ceil(nw / 64), groups).  A group's tiles' sums added in row order by 4 waves (tile t by wave t % 4), then in
+// wave order.
+template <typename T>
 __global__ void __launch_bounds__(256)
 k_mm_dbias(MmGrad a) {
-  __shared__ float s[2][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t n = (int64_t)blockIdx.x * 64 + lane;
-  int64_t lo = 0, hi = a.M;
-  if (a.offsets) group_rows(a.offsets, blockIdx.y, a.M, &lo, &hi);
-  float sum = 0.f, sup = 0.f;
-  if (n < a.N)
-    for (int64_t m = lo + wave; m < hi; m += 4) {
-      float up = 0.f;
-      sum += dz_at<T, D>(a, m, n, &up);
-      sup += up;
+  __shared__ float s_sum[4][64];
+  __shared__ int s_before[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.y;
+  const int64_t nw = a.act == EFF_ACT_SWIGLU ? 2 * a.N : a.N, n = (int64_t)blockIdx.x * 64 + lane;
+  int64_t lo = 0, hi = a.M, first = 0;
+  if (a.offsets) {  // tiles of the groups before this one
+    int before = 0;
+    for (int i = threadIdx.x; i < e; i += 256) {
+      group_rows(a.offsets, i, a.M, &lo, &hi);
+      before += (int)((hi - lo + kDzRows - 1) / kDzRows);
     }
-  s[0][wave][lane] = sum;
-  s[1][wave][lane] = sup;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) before += __shfl_xor(before, o);
+    if (lane == 0) s_before[wave] = before;
+    __syncthreads();
+    first = s_before[0] + s_before[1] + s_before[2] + s_before[3];
+    group_rows(a.offsets, e, a.M, &lo, &hi);
+  }
+  const int64_t count = (hi - lo + kDzRows - 1) / kDzRows, last = min(first + count, a.tiles);
+  float sum = 0.f;
+  if (n < nw)
+    for (int64_t t = first + wave; t < last; t += 4) sum += a.part[t * nw + n];
+  s_sum[wave][lane] = sum;
   __syncthreads();
-  if (wave || n >= a.N) return;
-  T* db = reinterpret_cast<T*>(a.dbias) + (int64_t)blockIdx.y * (a.act == EFF_ACT_SWIGLU ? 2 * a.N : a.N);
-  db[n] = (T)((s[0][0][lane] + s[0][1][lane]) + (s[0][2][lane] + s[0][3][lane]));
-  if (a.act == EFF_ACT_SWIGLU) db[a.N + n] = (T)((s[1][0][lane] + s[1][1][lane]) + (s[1][2][lane] + s[1][3][lane]));
+  if (wave || n >= nw) return;
+  reinterpret_cast<T*>(a.dbias)[(int64_t)e * nw + n] = (T)((s_sum[0][lane] + s_sum[1][lane]) + (s_sum[2][lane] + s_sum[3][lane]));
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -664,6 +885,20 @@ hipError_t launch_tile_c(const MmArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <typename T, int MT, bool GLU>
+hipError_t launch_few(const MmArgs& a, hipStream_t s) {
+  const int64_t slices = ceil_div(a.N, GLU ? 8 : 16), jobs = slices * row_tiles(a, 16 * MT);
+  if (slices * 16 > (int64_t)1 << 30 || jobs > (int64_t)1 << 40) return hipErrorInvalidConfiguration;
+  // waves per workgroup: about 16 per CU over the launch, each with at least two chunks of k
+  int waves = 16;
+  while (waves > 1 && (jobs * waves > 8192 || waves * 128 > a.K + 127)) waves /= 2;
+  const bool grouped = a.mode == MM_ROW_GROUPS;
+  const int64_t grid = std::min<int64_t>(jobs, grouped ? 256 * (32 / waves) : kMaxTiles);
+  const int lds = waves * MT * 1024 + (grouped ? (a.groups + 1 + 16) * 4 : 0);
+  hipLaunchKernelGGL((k_mm_few<T, MT, GLU>), dim3((unsigned)grid), dim3(64 * waves), lds, s, a, (int)slices);
+  return hipGetLastError();
+}
+
 template <typename T, bool XK, bool WK, bool GLU>
 hipError_t launch_tile(const MmArgs& a, hipStream_t s) {
   typedef TileCfg<256, 256, 2, 4, 64, 2, true> Big;
@@ -671,6 +906,10 @@ hipError_t launch_tile(const MmArgs& a, hipStream_t s) {
   typedef TileCfg<64, 128, 1, 4, 64, 3, false> Low;
   const int64_t z = a.mode == MM_K_GROUPS ? a.groups : 1, n = GLU ? 2 * a.N : a.N;
   const int64_t rows = a.mode == MM_ROW_GROUPS ? a.M / std::max<int64_t>(1, std::min<int64_t>(a.groups, a.M)) : a.M;
+  if constexpr (XK && WK) {
+    if (rows <= 16) return launch_few<T, 1, GLU>(a, s);
+    if (rows <= 32) return launch_few<T, 2, GLU>(a, s);
+  }
   if (rows > 128 && ceil_div(rows, 256) * ceil_div(n, 256) * z >= 200) return launch_tile_c<T, Big, XK, WK, GLU>(a, s);
   if (rows > 64) return launch_tile_c<T, Mid, XK, WK, GLU>(a, s);
   return launch_tile_c<T, Low, XK, WK, GLU>(a, s);
@@ -682,7 +921,7 @@ hipError_t launch_matmul(const MmArgs& in, hipStream_t s) {
   MmArgs a = in;
   const bool glu = a.act == EFF_ACT_SWIGLU, xk = a.sxk == 1, wk = a.swk == 1;
   // 16-byte copies: aligned matrices whose contiguous side is whole vectors
-  const bool direct = aligned16({a.x, a.w}, {xk ? a.sxm : a.sxk, wk ? a.swn : a.swk, a.swg, xk ? a.K : 0, xk ? 0 : a.M, wk ? 0 : a.N}, 2) &&
+  const bool direct = aligned16({a.x, a.w}, {xk ? a.sxm : a.sxk, wk ? a.swn : a.swk, a.swg, xk && !(a.x_padded && !wk) ? a.K : 0, xk || a.x_padded ? 0 : a.M, wk ? 0 : a.N}, 2) &&
                       (xk || !wk);
   a.vec = aligned16({a.y, a.bias, a.residual, a.pre}, {a.N, a.ldy, a.syg, a.residual ? a.ldr : 0, a.pre ? a.ldp : 0}, 2);
   auto go = [&](auto t) -> hipError_t {
@@ -702,16 +941,27 @@ hipError_t launch_matmul(const MmArgs& in, hipStream_t s) {
   return a.dtype == EFF_DT_BF16 ? go(bf16_t{}) : go(f16_t{});
 }
 
-hipError_t launch_matmul_dz(const MmGrad& a, hipStream_t s) {
+// row tiles of the pass over dz, and of its partial sums
+int64_t matmul_dz_tiles(int64_t M, int groups) {
+  return groups ? M / kDzRows + std::min<int64_t>(groups, M) : ceil_div(M, kDzRows);
+}
+
+hipError_t launch_matmul_dz(const MmGrad& in, hipStream_t s) {
+  MmGrad a = in;
+  a.tiles = matmul_dz_tiles(a.M, a.offsets ? a.groups : 0);
+  const int64_t nw = a.act == EFF_ACT_SWIGLU ? 2 * a.N : a.N;
+  const bool vec = aligned16({a.dy, a.act ? a.pre : nullptr, a.dz}, {a.N, a.ldy, a.act ? a.ldp : 0, a.lddz}, 2);
+  const int64_t cols = ceil_div(a.N, vec ? 512 : 64);
+  if (cols * a.tiles > kMaxTiles || ceil_div(nw, 64) > kMaxTiles) return hipErrorInvalidConfiguration;
   auto go = [&](auto t, auto d) {
     typedef decltype(t) T;
     typedef decltype(d) D;
-    if (a.dz && a.M > 0)
-      hipLaunchKernelGGL((k_mm_dz<T, D>), dim3((unsigned)ceil_div(a.N, 256), (unsigned)std::min<int64_t>(a.M, 65535)), dim3(256),
-                         0, s, a);
+    if (a.M > 0) {
+      if (vec) hipLaunchKernelGGL((k_mm_dz<T, D, 8>), dim3((unsigned)(cols * a.tiles)), dim3(256), 0, s, a, (int)cols);
+      else hipLaunchKernelGGL((k_mm_dz<T, D, 1>), dim3((unsigned)(cols * a.tiles)), dim3(256), 0, s, a, (int)cols);
+    }
     if (a.dbias)
-      hipLaunchKernelGGL((k_mm_dbias<T, D>), dim3((unsigned)ceil_div(a.N, 64), (unsigned)(a.offsets ? a.groups : 1)), dim3(256), 0,
-                         s, a);
+      hipLaunchKernelGGL((k_mm_dbias<T>), dim3((unsigned)ceil_div(nw, 64), (unsigned)(a.offsets ? a.groups : 1)), dim3(256), 0, s, a);
   };
   if (a.dtype == EFF_DT_BF16) {
     if (a.dy_f32) go(bf16_t{}, float{});

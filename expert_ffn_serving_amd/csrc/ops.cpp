@@ -53,7 +53,9 @@ bool inputs_ld_bad(int64_t ld) { return ld < 0; }
 
 // the backward pass materialises dz unless it is dy itself
 bool needs_dz(const eff_matmul_desc* d) { return d->act != EFF_ACT_NONE || d->out_dtype != d->dtype; }
-int64_t dz_bytes(const eff_matmul_desc* d) { return needs_dz(d) ? align256(d->m * w_rows(d) * 2) : 0; }
+int64_t dz_ld(const eff_matmul_desc* d) { return (w_rows(d) + 7) / 8 * 8; }
+int64_t dz_bytes(const eff_matmul_desc* d) { return needs_dz(d) ? align256(d->m * dz_ld(d) * 2) : 0; }
+int64_t part_bytes(const eff_matmul_desc* d) { return align256(matmul_dz_tiles(d->m, d->groups) * w_rows(d) * 4); }
 
 int check_ws(const char* fn, int64_t need, const void* ws, size_t bytes) {
   if (need <= 0) return EFF_OK;
@@ -75,7 +77,7 @@ extern "C" {
 
 int64_t eff_matmul_workspace(const eff_matmul_desc* d, int backward) {
   if (const char* why = check_desc(d)) return bad("eff_matmul_workspace", why);
-  return backward ? dz_bytes(d) : 0;
+  return backward ? dz_bytes(d) + part_bytes(d) : 0;
 }
 
 int eff_matmul(const eff_matmul_desc* d, const void* x, const void* w, const void* bias, const void* residual,
@@ -129,9 +131,10 @@ int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x,
   const void* dz = dy;
   int64_t lddz = d->ld_y;
   if (needs_dz(d) && (dx || dw)) {
-    g.dz = workspace, g.lddz = nw;
-    dz = workspace, lddz = nw;
+    g.dz = workspace, g.lddz = dz_ld(d);
+    dz = workspace, lddz = g.lddz;
   }
+  if (dbias) g.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + dz_bytes(d));
   if (g.dz || dbias)
     if (int rc = launched(fn, launch_matmul_dz(g, s))) return rc;
   MmArgs a = {};
@@ -140,7 +143,7 @@ int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x,
   a.offsets = offsets;
   if (dx && rows) {  // dx[m,k] = sum over W's rows n of dz[m,n] w[n,k]
     a.mode = d->groups ? MM_ROW_GROUPS : MM_DENSE;
-    a.x = dz, a.sxm = lddz, a.sxk = 1;
+    a.x = dz, a.sxm = lddz, a.sxk = 1, a.x_padded = g.dz != nullptr;
     a.w = w, a.swn = 1, a.swk = d->ld_w, a.swg = d->stride_w;
     a.M = d->m, a.N = d->k, a.K = nw;
     a.y = dx, a.ldy = d->ld_dx;
@@ -148,7 +151,7 @@ int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x,
   }
   if (dw) {  // dw[n,k] = sum over rows m of dz[m,n] x[m,k]
     a.mode = d->groups ? MM_K_GROUPS : MM_DENSE;
-    a.x = dz, a.sxm = 1, a.sxk = lddz;
+    a.x = dz, a.sxm = 1, a.sxk = lddz, a.x_padded = g.dz != nullptr;
     a.w = x, a.swn = 1, a.swk = d->ld_x, a.swg = 0;
     a.M = nw, a.N = d->k, a.K = d->m;
     a.y = dw, a.ldy = d->ld_dw, a.syg = d->stride_dw;
