@@ -73,14 +73,15 @@ __device__ inline void group_rows(const int32_t* offsets, int e, int64_t m, int6
   *hi = max(*lo, clamp_offset(offsets[e + 1], m));
 }
 
-// The row tile `tile` of the groups' tiles in group order (BM rows each, every group's last one ragged):
-// its group and rows, or false past the last.  All threads of the workgroup (NT of them) take part.
-template <int BM, int NT>
+// The row tile `tile` of the groups' tiles in group order (BM rows each, every group's last one ragged): its group and
+// rows, or false past the last.  All threads of the workgroup take part; s: 20 ints of LDS, free again on return.
+// Tiles are numbered without gaps, so the launch's spare workgroups come last, where they cost nothing (numbered by
+// rows, with the spare ones in between and no scan, 16 tokens over 512 experts took 107 us and not 91).
+template <int BM>
 __device__ inline bool find_tile(const int32_t* offsets, int E, int64_t m, int tile, int* s, int* group, int64_t* row0,
                                  int64_t* row1) {
-  // s: NT/64 + 4 ints of LDS
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (E + NT - 1) / NT, e0 = min(E, tid * per), e1 = min(E, e0 + per);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nt = blockDim.x;
+  const int per = (E + nt - 1) / nt, e0 = min(E, tid * per), e1 = min(E, e0 + per);
   int mine = 0;
   for (int e = e0; e < e1; ++e) {
     int64_t lo, hi;
@@ -94,77 +95,30 @@ __device__ inline bool find_tile(const int32_t* offsets, int E, int64_t m, int t
     if (lane >= o) incl += u;
   }
   if (lane == 63) s[wave] = incl;
-  if (tid == 0) s[NT / 64] = -1;
+  if (tid == 0) s[16] = -1;
   __syncthreads();
-  int before = incl - mine;
-  for (int i = 0; i < wave; ++i) before += s[i];
-  if (tile >= before && tile < before + mine) {
-    int at = before;
+  int at = incl - mine;
+  for (int i = 0; i < wave; ++i) at += s[i];
+  if (tile >= at && tile < at + mine) {
     for (int e = e0; e < e1; ++e) {
       int64_t lo, hi;
       group_rows(offsets, e, m, &lo, &hi);
       const int n = (int)((hi - lo + BM - 1) / BM);
       if (tile < at + n) {
-        s[NT / 64] = e;
-        s[NT / 64 + 1] = (int)(lo + (int64_t)(tile - at) * BM);
-        s[NT / 64 + 2] = (int)min(hi, lo + (int64_t)(tile - at + 1) * BM);
+        s[16] = e;
+        s[17] = (int)(lo + (int64_t)(tile - at) * BM);
+        s[18] = (int)min(hi, lo + (int64_t)(tile - at + 1) * BM);
         break;
       }
       at += n;
     }
   }
   __syncthreads();
-  *group = s[NT / 64];
-  *row0 = s[NT / 64 + 1];
-  *row1 = s[NT / 64 + 2];
-  return *group >= 0;
-}
-
-// Prefix sums of the groups' tile counts into pre[0..E] (16 ints behind them are scratch); returns their number.
-// Every thread of the workgroup takes part.
-template <int BM>
-__device__ inline int group_prefix(const int32_t* offsets, int E, int64_t m, int* pre) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nt = blockDim.x;
-  int* s = pre + E + 1;
-  int run = 0;
-  for (int e0 = 0; e0 < E; e0 += nt) {
-    const int e = e0 + tid;
-    int mine = 0;
-    if (e < E) {
-      int64_t lo, hi;
-      group_rows(offsets, e, m, &lo, &hi);
-      mine = (int)((hi - lo + BM - 1) / BM);
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int u = __shfl_up(incl, o);
-      if (lane >= o) incl += u;
-    }
-    if (lane == 63) s[wave] = incl;
-    __syncthreads();
-    int before = run, all = 0;
-    for (int i = 0; i < nt >> 6; ++i) {
-      before += i < wave ? s[i] : 0;
-      all += s[i];
-    }
-    if (e < E) pre[e] = before + incl - mine;
-    run += all;
-    __syncthreads();
-  }
-  if (tid == 0) pre[E] = run;
+  *group = s[16];
+  *row0 = s[17];
+  *row1 = s[18];
   __syncthreads();
-  return run;
-}
-// the group that tile `t` < pre[E] belongs to: the last e with pre[e] <= t
-__device__ inline int group_of_tile(const int* pre, int E, int t) {
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
+  return *group >= 0;
 }
 
 template <typename T>
@@ -245,7 +199,6 @@ __global__ void __launch_bounds__(256)
 k_mm_any(MmArgs a) {
   typedef typename Vec8<T>::V V8;
   __shared__ T s_x[kAnyBM][kAnyLD], s_w[kAnyBN][kAnyLD];
-  __shared__ int s_f[8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4, r = lane & 15;
   constexpr int NC = GLU ? kAnyBN / 2 : kAnyBN;  // output columns of the tile
   const int nt = (int)((a.N + NC - 1) / NC), tile = blockIdx.x / nt;
@@ -253,7 +206,7 @@ k_mm_any(MmArgs a) {
   int g = 0;
   int64_t m0, m1, k0 = 0, k1 = a.K;
   if (a.mode == MM_ROW_GROUPS) {
-    if (!find_tile<kAnyBM, 256>(a.offsets, a.groups, a.M, tile, s_f, &g, &m0, &m1)) return;
+    if (!find_tile<kAnyBM>(a.offsets, a.groups, a.M, tile, reinterpret_cast<int*>(s_x), &g, &m0, &m1)) return;
   } else {
     m0 = (int64_t)tile * kAnyBM;
     m1 = min(a.M, m0 + kAnyBM);
@@ -400,9 +353,7 @@ k_mm_tile(MmArgs a) {
   if (a.mode == MM_ROW_GROUPS) {
     mt_i = blockIdx.x / nt;
     nt_i = blockIdx.x % nt;
-    const bool found = find_tile<BM, TH>(a.offsets, a.groups, a.M, mt_i, reinterpret_cast<int*>(s_tile), &g, &m0, &m1);
-    if (!found) return;
-    __syncthreads();
+    if (!find_tile<BM>(a.offsets, a.groups, a.M, mt_i, reinterpret_cast<int*>(s_tile), &g, &m0, &m1)) return;
   } else {
     mt_i = blockIdx.x / nt;
     nt_i = blockIdx.x % nt;
@@ -617,101 +568,84 @@ k_mm_tile(MmArgs a) {
 // ---- few rows --------------------------------------------------------------------------------------------
 //
 // Up to 16 MT rows of x against 16 rows of W per workgroup (SwiGLU: 8 gate and 8 up rows), the k split over its waves:
-// bound by the stream of W, so every wave keeps U chunks of 64 k (2 KiB of W each) in flight in registers and nothing
+// bound by the stream of W, so every wave keeps kFewU chunks of 64 k (2 KiB of W each) in flight in registers and nothing
 // waits for a barrier before the end, where the waves' sums meet in LDS in wave order.  The lane of W row r and k group
 // q takes 32 consecutive bytes of a chunk: k = 16 q .. 16 q + 15 (the order of k inside a product is free as long as
 // both operands share it), so a chunk is one 128-byte line of every row.
-// With groups the workgroups walk the groups' tiles by themselves (prefix sums of the tile counts in LDS), so none
-// is launched for tiles that do not exist.
-template <int MT>
-constexpr int few_unroll() { return MT == 1 ? 4 : 2; }
+constexpr int kFewU = 2;
 
 template <typename T, int MT, bool GLU>
 __global__ void __launch_bounds__(1024)
 k_mm_few(MmArgs a, int slices) {
   typedef typename Vec8<T>::V V8;
-  constexpr int U = few_unroll<MT>(), BM = 16 * MT;
+  constexpr int U = kFewU, BM = 16 * MT;
   extern __shared__ __attribute__((aligned(16))) uint8_t s_few[];
   f32x4_t* s_acc = reinterpret_cast<f32x4_t*>(s_few);                       // [waves][MT][64]
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
-  int* s_pre = reinterpret_cast<int*>(s_few + waves * MT * 1024);           // groups + 1 prefix sums, 16 more
-  const bool grouped = a.mode == MM_ROW_GROUPS;
-  int64_t tiles = grouped ? 0 : (a.M + BM - 1) / BM;
-  if (grouped) tiles = group_prefix<BM>(a.offsets, a.groups, a.M, s_pre);
+  const int tile = blockIdx.x / slices, n0 = (int)(blockIdx.x % slices) * (GLU ? 8 : 16);
+  int g = 0;
+  int64_t m0 = (int64_t)tile * BM, m1 = min(a.M, m0 + BM);
+  if (a.mode == MM_ROW_GROUPS && !find_tile<BM>(a.offsets, a.groups, a.M, tile, reinterpret_cast<int*>(s_few), &g, &m0, &m1)) return;
   const T* x = reinterpret_cast<const T*>(a.x);
   const int K = (int)a.K, chunks = (K + 63) / 64;
-
-  for (int64_t job = blockIdx.x; job < tiles * slices; job += gridDim.x) {
-    const int tile = (int)(job / slices), n0 = (int)(job % slices) * (GLU ? 8 : 16);
-    int g = 0;
-    int64_t m0 = (int64_t)tile * BM, m1 = min(a.M, m0 + BM);
-    if (grouped) {
-      g = group_of_tile(s_pre, a.groups, tile);
-      int64_t lo, hi;
-      group_rows(a.offsets, g, a.M, &lo, &hi);
-      m0 = lo + (int64_t)(tile - s_pre[g]) * BM;
-      m1 = min(hi, m0 + BM);
+  const int64_t col = min((int64_t)n0 + (GLU ? r & 7 : r), a.N - 1);
+  const T* w = reinterpret_cast<const T*>(a.w) + g * a.swg + (col + (GLU && r >= 8 ? a.N : 0)) * a.swn + q * 16;
+  const T* xr[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) xr[i] = x + min(m0 + i * 16 + r, m1 - 1) * a.sxm + q * 16;
+  f32x4_t acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  V8 fw[U][2], fx[U][MT][2];
+  // chunk c of this wave's into slot s; past the end the first chunk again (not used)
+  auto load = [&](int c, int s) {
+    const int k = c < chunks ? c * 64 : 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int kk = k + q * 16 + h * 8 < K ? k + h * 8 : -(q * 16);      // past the last k: the row's first values
+      fw[s][h] = *reinterpret_cast<const V8*>(w + kk);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fx[s][i][h] = *reinterpret_cast<const V8*>(xr[i] + kk);
     }
-    const int64_t col = min((int64_t)n0 + (GLU ? r & 7 : r), a.N - 1);
-    const T* w = reinterpret_cast<const T*>(a.w) + g * a.swg + (col + (GLU && r >= 8 ? a.N : 0)) * a.swn + q * 16;
-    const T* xr[MT];
+  };
+  auto use = [&](int c, int s) {
+    if (c >= chunks) return;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) xr[i] = x + min(m0 + i * 16 + r, m1 - 1) * a.sxm + q * 16;
-    f32x4_t acc[MT];
+    for (int h = 0; h < 2; ++h) {
+      if (c * 64 + 64 > K && c * 64 + q * 16 + h * 8 >= K) {              // nothing there: zeros on both sides
+        fw[s][h] = V8{};
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    V8 fw[U][2], fx[U][MT][2];
-    // chunk c of this wave's into slot s; past the end the first chunk again (not used)
-    auto load = [&](int c, int s) {
-      const int k = c < chunks ? c * 64 : 0;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int kk = k + q * 16 + h * 8 < K ? k + h * 8 : -(q * 16);      // past the last k: the row's first values
-        fw[s][h] = *reinterpret_cast<const V8*>(w + kk);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) fx[s][i][h] = *reinterpret_cast<const V8*>(xr[i] + kk);
+        for (int i = 0; i < MT; ++i) fx[s][i][h] = V8{};
       }
-    };
-    auto use = [&](int c, int s) {
-      if (c >= chunks) return;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (c * 64 + 64 > K && c * 64 + q * 16 + h * 8 >= K) {              // nothing there: zeros on both sides
-          fw[s][h] = V8{};
-#pragma unroll
-          for (int i = 0; i < MT; ++i) fx[s][i][h] = V8{};
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i] = mfma(fw[s][h], fx[s][i][h], acc[i]);
-      }
-    };
-#pragma unroll
-    for (int s = 0; s < U; ++s) load(wave + s * waves, s);
-    for (int c = wave; c < chunks; c += U * waves) {
-#pragma unroll
-      for (int s = 0; s < U; ++s) {
-        use(c + s * waves, s);
-        load(c + (s + U) * waves, s);
-      }
+      for (int i = 0; i < MT; ++i) acc[i] = mfma(fw[s][h], fx[s][i][h], acc[i]);
     }
+  };
 #pragma unroll
-    for (int i = 0; i < MT; ++i) s_acc[(wave * MT + i) * 64 + lane] = acc[i];
-    __syncthreads();
-    // one wave per 16 rows of x: lane's row m = r, W rows 4 q .. 4 q + 3 of the slice
-    for (int i = wave; i < MT; i += waves) {
-      f32x4_t sum = s_acc[i * 64 + lane];
-      for (int v = 1; v < waves; ++v) sum += s_acc[(v * MT + i) * 64 + lane];
-      float z[4], u[4];
+  for (int s = 0; s < U; ++s) load(wave + s * waves, s);
+  for (int c = wave; c < chunks; c += U * waves) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        z[e] = sum[e];
-        if (GLU) u[e] = __shfl_down(z[e], 32);
-      }
-      const int64_t m = m0 + i * 16 + r;
-      if (m < m1 && (!GLU || q < 2)) mm_finish<T, 4, GLU>(a, m, n0 + 4 * q, (int64_t)g * (GLU ? 2 * a.N : a.N), 0, z, u);
+    for (int s = 0; s < U; ++s) {
+      use(c + s * waves, s);
+      load(c + (s + U) * waves, s);
     }
-    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) s_acc[(wave * MT + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  // one wave per 16 rows of x: lane's row m = r, W rows 4 q .. 4 q + 3 of the slice
+  for (int i = wave; i < MT; i += waves) {
+    f32x4_t sum = s_acc[i * 64 + lane];
+    for (int v = 1; v < waves; ++v) sum += s_acc[(v * MT + i) * 64 + lane];
+    float z[4], u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      z[e] = sum[e];
+      if (GLU) u[e] = __shfl_down(z[e], 32);
+    }
+    const int64_t m = m0 + i * 16 + r;
+    if (m < m1 && (!GLU || q < 2)) mm_finish<T, 4, GLU>(a, m, n0 + 4 * q, (int64_t)g * (GLU ? 2 * a.N : a.N), 0, z, u);
   }
 }
 
@@ -751,13 +685,12 @@ template <typename T, typename D, int VEC>
 __global__ void __launch_bounds__(256)
 k_mm_dz(MmGrad a, int cols) {
   __shared__ float s_sum[2][4][64][VEC];
-  __shared__ int s_f[8];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tile = blockIdx.x / cols;
   const int64_t n = ((int64_t)(blockIdx.x % cols) * 64 + lane) * VEC;
   int g;
   int64_t m0 = (int64_t)tile * kDzRows, m1 = min(a.M, m0 + kDzRows);
-  if (a.offsets && !find_tile<kDzRows, 256>(a.offsets, a.groups, a.M, tile, s_f, &g, &m0, &m1)) return;
+  if (a.offsets && !find_tile<kDzRows>(a.offsets, a.groups, a.M, tile, reinterpret_cast<int*>(s_sum), &g, &m0, &m1)) return;
   const bool glu = a.act == EFF_ACT_SWIGLU;
   const int64_t nw = glu ? 2 * a.N : a.N;
   float sum[VEC], sup[VEC];
@@ -845,8 +778,9 @@ k_mm_dbias(MmGrad a) {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // row tiles of BM rows: dense, or at most this many over the groups
+int64_t group_tiles(int64_t M, int64_t groups, int64_t BM) { return M / BM + std::min(groups, M); }
 int64_t row_tiles(const MmArgs& a, int64_t BM) {
-  return a.mode == MM_ROW_GROUPS ? a.M / BM + std::min<int64_t>(a.groups, a.M) : ceil_div(a.M, BM);
+  return a.mode == MM_ROW_GROUPS ? group_tiles(a.M, a.groups, BM) : ceil_div(a.M, BM);
 }
 
 // workgroups of one launch: their threads stay below 2^32
@@ -873,7 +807,7 @@ hipError_t allow_lds(const void* fn, int bytes, std::atomic<uint64_t>* done) {
 }
 
 template <typename T, class C, bool XK, bool WK, bool GLU>
-hipError_t launch_tile_c(const MmArgs& a, hipStream_t s) {
+hipError_t launch_tile_c(MmArgs a, hipStream_t s) {
   const int64_t tiles = ceil_div(a.N, GLU ? C::BN / 2 : C::BN) * row_tiles(a, C::BM);
   if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
   constexpr int lds = C::S * (C::BM + C::BN) * C::BK * 2;
@@ -886,16 +820,13 @@ hipError_t launch_tile_c(const MmArgs& a, hipStream_t s) {
 }
 
 template <typename T, int MT, bool GLU>
-hipError_t launch_few(const MmArgs& a, hipStream_t s) {
+hipError_t launch_few(MmArgs a, hipStream_t s) {
   const int64_t slices = ceil_div(a.N, GLU ? 8 : 16), jobs = slices * row_tiles(a, 16 * MT);
-  if (slices * 16 > (int64_t)1 << 30 || jobs > (int64_t)1 << 40) return hipErrorInvalidConfiguration;
+  if (jobs > kMaxTiles) return hipErrorInvalidConfiguration;
   // waves per workgroup: about 16 per CU over the launch, each with at least two chunks of k
   int waves = 16;
   while (waves > 1 && (jobs * waves > 8192 || waves * 128 > a.K + 127)) waves /= 2;
-  const bool grouped = a.mode == MM_ROW_GROUPS;
-  const int64_t grid = std::min<int64_t>(jobs, grouped ? 256 * (32 / waves) : kMaxTiles);
-  const int lds = waves * MT * 1024 + (grouped ? (a.groups + 1 + 16) * 4 : 0);
-  hipLaunchKernelGGL((k_mm_few<T, MT, GLU>), dim3((unsigned)grid), dim3(64 * waves), lds, s, a, (int)slices);
+  hipLaunchKernelGGL((k_mm_few<T, MT, GLU>), dim3((unsigned)jobs), dim3(64 * waves), std::max(waves * MT * 1024, 1024), s, a, (int)slices);
   return hipGetLastError();
 }
 
@@ -907,8 +838,10 @@ hipError_t launch_tile(const MmArgs& a, hipStream_t s) {
   const int64_t z = a.mode == MM_K_GROUPS ? a.groups : 1, n = GLU ? 2 * a.N : a.N;
   const int64_t rows = a.mode == MM_ROW_GROUPS ? a.M / std::max<int64_t>(1, std::min<int64_t>(a.groups, a.M)) : a.M;
   if constexpr (XK && WK) {
-    if (rows <= 16) return launch_few<T, 1, GLU>(a, s);
-    if (rows <= 32) return launch_few<T, 2, GLU>(a, s);
+    // the tiles' waves share x, the split of k fills the chip when there are few tiles
+    const bool fill = row_tiles(a, 64) * ceil_div(n, 128) >= 512;
+    if (rows <= 16 && !fill) return launch_few<T, 1, GLU>(a, s);
+    if (rows <= 32 && !fill) return launch_few<T, 2, GLU>(a, s);
   }
   if (rows > 128 && ceil_div(rows, 256) * ceil_div(n, 256) * z >= 200) return launch_tile_c<T, Big, XK, WK, GLU>(a, s);
   if (rows > 64) return launch_tile_c<T, Mid, XK, WK, GLU>(a, s);
@@ -943,7 +876,7 @@ hipError_t launch_matmul(const MmArgs& in, hipStream_t s) {
 
 // row tiles of the pass over dz, and of its partial sums
 int64_t matmul_dz_tiles(int64_t M, int groups) {
-  return groups ? M / kDzRows + std::min<int64_t>(groups, M) : ceil_div(M, kDzRows);
+  return groups ? group_tiles(M, groups, kDzRows) : ceil_div(M, kDzRows);
 }
 
 hipError_t launch_matmul_dz(const MmGrad& in, hipStream_t s) {

@@ -130,6 +130,8 @@ def test_bad_tensors(eff):
         lambda: eff.matmul_backward(y.half(), x, w, dx=x), lambda: eff.matmul_backward(y, x, w, dx=z(1, 16).expand(4, 16)),
         lambda: eff.grouped_matmul(x, w, off, y), lambda: eff.grouped_matmul(x, z(2, 8, 16), z(2, d=torch.int32), y),
         lambda: eff.grouped_matmul(x, z(2, 8, 16), off.long(), y), lambda: eff.grouped_matmul(x, z(2, 8, 16), off.cpu(), y),
+        lambda: eff.grouped_matmul_backward(y, x, z(2, 8, 16), off, dw=z(1, 8, 16).expand(2, 8, 16)),
+        lambda: eff.grouped_matmul(x, z(0, 8, 16), z(1, d=torch.int32), y), lambda: eff.grouped_matmul(x, z(2, 8, 32)[..., ::2], off, y),
         lambda: eff.sort_tokens(ids.long(), off, ids.view(-1), pos), lambda: eff.sort_tokens(ids, off, z(7, d=torch.int32), pos),
         lambda: eff.sort_tokens(ids, off, ids.view(-1), z(2, 4, d=torch.int32)), lambda: eff.sort_tokens(ids, off[:1], ids.view(-1), pos),
         lambda: eff.sort_tokens(ids, z(4098, d=torch.int32), z(8, d=torch.int32), pos), lambda: eff.sort_tokens(ids.t(), off, z(8, d=torch.int32), pos),
