@@ -354,10 +354,17 @@ struct MmArgs {
   void* pre;
   int64_t ldp;
   int dtype, y_f32, act, mode, groups;
-  int x_padded;  // every row of x in memory is zero up to a multiple of 8 values
-  int vec;       // set by launch_matmul: the epilogue's rows are whole 16-byte vectors
+  int xk, wk;              // whether x and w are contiguous along k (sxk, swk = 1) or along their own index (sxm, swn = 1)
+  int x_padded, w_padded;  // every row in memory is zero up to a multiple of 8 values
+  // set by launch_matmul
+  int vec;      // the epilogue's rows are whole 16-byte vectors
+  float* part;  // sums of a split k: [splits][M][w rows of ceil(N / 8) * 8 values each]; y is written by a second kernel
+  int64_t ldpart;
+  int split_steps;  // steps of 64 k of one split
 };
-hipError_t launch_matmul(const MmArgs& a, hipStream_t s);
+// workspace that launch_matmul needs, from the sizes and strides alone
+int64_t matmul_workspace(const MmArgs& a);
+hipError_t launch_matmul(const MmArgs& a, void* workspace, hipStream_t s);
 
 // dz = dy * act'(pre) [M, N or 2N] rounded to dtype (dz null: not written), its rows zeroed up to lddz, and its column
 // sums per group (part and dbias null: none; part: matmul_dz_tiles rows of fp32)

@@ -5,6 +5,7 @@
 // the matrix cores add them in fp32; each output is rounded once.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "eff_internal.h"
 #include "lds_dma.h"
@@ -223,24 +224,39 @@ k_mm_any(MmArgs a) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
-  for (int64_t kb = k0; kb < k1; kb += kAnyBK) {
+  T vx[8], vw[8];
+  // this thread's values of the step at kb; consecutive lanes along whichever index is contiguous in memory
+  auto place = [&](int z, int along_k, int rows, int* rr, int* kk) {
+    const int i = z * 256 + tid;
+    *rr = along_k ? i / kAnyBK : i % rows;
+    *kk = along_k ? i % kAnyBK : i / rows;
+  };
+  auto load = [&](int64_t kb) {
 #pragma unroll
     for (int z = 0; z < 8; ++z) {
-      const int i = z * 256 + tid;
-      // consecutive lanes along whichever index is contiguous in memory
-      int rr = a.sxk == 1 ? i / kAnyBK : i % kAnyBM, kk = a.sxk == 1 ? i % kAnyBK : i / kAnyBM;
-      T v = (T)0.f;
-      if (m0 + rr < m1 && kb + kk < k1) v = x[(m0 + rr) * a.sxm + (kb + kk) * a.sxk];
-      s_x[rr][kk] = v;
-      rr = a.swk == 1 ? i / kAnyBK : i % kAnyBN;
-      kk = a.swk == 1 ? i % kAnyBK : i / kAnyBN;
-      v = (T)0.f;
+      int rr, kk;
+      place(z, a.xk, kAnyBM, &rr, &kk);
+      vx[z] = (T)0.f;
+      if (m0 + rr < m1 && kb + kk < k1) vx[z] = x[(m0 + rr) * a.sxm + (kb + kk) * a.sxk];
+      place(z, a.wk, kAnyBN, &rr, &kk);
       // tile columns: per wave 32, with SwiGLU 16 gate then 16 up
       const int64_t c = GLU ? n0 + (rr >> 5) * 16 + (rr & 15) : n0 + rr;
       const int64_t wr = c + (GLU && (rr & 16) ? a.N : 0);
-      if (c < a.N && kb + kk < k1) v = w[wr * a.swn + (kb + kk) * a.swk];
-      s_w[rr][kk] = v;
+      vw[z] = (T)0.f;
+      if (c < a.N && kb + kk < k1) vw[z] = w[wr * a.swn + (kb + kk) * a.swk];
     }
+  };
+  if (k0 < k1) load(k0);
+  for (int64_t kb = k0; kb < k1; kb += kAnyBK) {
+#pragma unroll
+    for (int z = 0; z < 8; ++z) {
+      int rr, kk;
+      place(z, a.xk, kAnyBM, &rr, &kk);
+      s_x[rr][kk] = vx[z];
+      place(z, a.wk, kAnyBN, &rr, &kk);
+      s_w[rr][kk] = vw[z];
+    }
+    if (kb + kAnyBK < k1) load(kb + kAnyBK);  // in flight while this step's products run
     __syncthreads();
     V8 fx[2], fw[2];
 #pragma unroll
@@ -362,6 +378,9 @@ k_mm_tile(MmArgs a) {
     if (a.mode == MM_K_GROUPS) {
       g = blockIdx.y;
       group_rows(a.offsets, g, a.K, &k0, &k1);
+    } else if (a.part) {  // this split's share of the k
+      k0 = (int64_t)blockIdx.y * a.split_steps * 64;
+      k1 = min(a.K, k0 + (int64_t)a.split_steps * 64);
     }
   }
   const int64_t n0 = (int64_t)nt_i * BNH;
@@ -370,6 +389,7 @@ k_mm_tile(MmArgs a) {
   const T* x = reinterpret_cast<const T*>(a.x);
   const T* w = reinterpret_cast<const T*>(a.w) + (a.mode == MM_ROW_GROUPS ? g * a.swg : 0);
   const int64_t xcols = a.x_padded ? (a.M + 7) & ~(int64_t)7 : a.M;  // x contiguous along m
+  const int64_t wcols = a.w_padded ? (a.N + 7) & ~(int64_t)7 : a.N;  // w contiguous along n
   const char *px[SX], *pw[SW];
   int kx[SX], kw[SW];  // the copy's first k inside a step
 #pragma unroll
@@ -399,7 +419,7 @@ k_mm_tile(MmArgs a) {
       constexpr int CH = BN / 8;
       const int k = idx / CH, p = idx % CH, c = ((((p >> 1) ^ swz_k(k)) << 1) | (p & 1)) % CH;
       kw[i] = k;
-      pw[i] = reinterpret_cast<const char*>(w + (k0 + k) * a.swk + min(n0 + c * 8, a.N - 8));
+      pw[i] = reinterpret_cast<const char*>(w + (k0 + k) * a.swk + min(n0 + c * 8, wcols - 8));
     }
   }
   const int64_t stepx = XK ? BK * 2 : a.sxk * (BK * 2), stepw = WK ? BK * 2 : a.swk * (BK * 2);
@@ -560,9 +580,64 @@ k_mm_tile(MmArgs a) {
           for (int e = 0; e < 4; ++e) u[4 * h + e] = v2[e];
         }
       }
-      mm_finish<T, 8, GLU>(a, m, n, nb, yo, z, u);
+      if (a.part) {
+        float* o = a.part + ((int64_t)blockIdx.y * a.M + m) * a.ldpart + n;
+        if (n < a.N) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            *reinterpret_cast<f32x4_t*>(o + 4 * h) = f32x4_t{z[4 * h], z[4 * h + 1], z[4 * h + 2], z[4 * h + 3]};
+            if (GLU) *reinterpret_cast<f32x4_t*>(o + a.ldpart / 2 + 4 * h) = f32x4_t{u[4 * h], u[4 * h + 1], u[4 * h + 2], u[4 * h + 3]};
+          }
+        }
+      } else {
+        mm_finish<T, 8, GLU>(a, m, n, nb, yo, z, u);
+      }
     }
   }
+}
+
+// A split k's sums added in order of k, and the epilogue.  grid: ceil(M * vectors / 256); a thread takes 8 columns.
+template <typename T, bool GLU>
+__global__ void __launch_bounds__(256)
+k_mm_join(MmArgs a, int splits) {
+  const int64_t vr = (a.N + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.M * vr) return;
+  const int64_t m = i / vr, n = i % vr * 8;
+  float z[8], u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = u[e] = 0.f;
+  const float* p = a.part + m * a.ldpart + n;
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s, p += a.M * a.ldpart)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + 4 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[4 * h + e] += v[e];
+      if (GLU) {
+        const f32x4_t v2 = *reinterpret_cast<const f32x4_t*>(p + a.ldpart / 2 + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[4 * h + e] += v2[e];
+      }
+    }
+  mm_finish<T, 8, GLU>(a, m, n, 0, 0, z, u);
+}
+
+// ---- operands that cannot be copied 16 bytes at a time ---------------------------------------------------
+// rows x cols values with any stride into rows of ldp (a multiple of 8) values, zeros behind cols; rows = groups *
+// group_rows.  A thread writes 16 bytes.  Reading and writing the matrix once more is what this costs; the general
+// kernel took 361 us where both of these and the tiles take a tenth (333 x 515 x 2563).
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_mm_pack(const T* __restrict__ src, int64_t rows, int64_t cols, int64_t ld, int64_t group_rows, int64_t sg, T* __restrict__ dst) {
+  const int64_t vr = (cols + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * vr) return;
+  const int64_t row = i / vr, c = i % vr * 8;
+  const T* s = src + (row / group_rows) * sg + (row % group_rows) * ld + c;
+  typename Vec8<T>::V v;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? s[e] : (T)0.f;
+  *reinterpret_cast<typename Vec8<T>::V*>(dst + (row * vr * 8 + c)) = v;
 }
 
 // ---- few rows --------------------------------------------------------------------------------------------
@@ -806,8 +881,75 @@ hipError_t allow_lds(const void* fn, int bytes, std::atomic<uint64_t>* done) {
   return err;
 }
 
+// ---- which kernel ----------------------------------------------------------------------------------------
+
+constexpr double kBigStep = 1.63, kMidStep = 1.16, kLowStep = 0.8;
+enum { KIND_ANY, KIND_FEW1, KIND_FEW2, KIND_BIG, KIND_MID, KIND_LOW };
+typedef TileCfg<256, 256, 2, 4, 64, 2, true> Big;
+typedef TileCfg<128, 128, 2, 2, 64, 2, false> Mid;
+typedef TileCfg<64, 128, 1, 4, 64, 3, false> Low;
+
+struct Plan {
+  int kind, splits;
+  int64_t pack_x, pack_w, part;  // workspace bytes of each (multiples of 256)
+};
+
+int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+int64_t w_rows(const MmArgs& a) { return a.act == EFF_ACT_SWIGLU ? 2 * a.N : a.N; }
+// rows and contiguous values of an operand in memory
+int64_t x_rows(const MmArgs& a) { return a.xk ? a.M : a.K; }
+int64_t x_cols(const MmArgs& a) { return a.xk ? a.K : a.M; }
+int64_t w_mem_rows(const MmArgs& a) { return (a.mode == MM_ROW_GROUPS ? a.groups : 1) * (a.wk ? w_rows(a) : a.K); }
+int64_t w_cols(const MmArgs& a) { return a.wk ? a.K : a.N; }
+
+// From sizes and strides alone (pointers that are not 16-byte aligned are the launch's business).
+Plan plan_matmul(const MmArgs& a) {
+  Plan p = {KIND_ANY, 1, 0, 0, 0};
+  if (a.M == 0 || a.K == 0) return p;   // zeros: any kernel writes them
+  const bool glu = a.act == EFF_ACT_SWIGLU;
+  const int64_t groups = std::max(1, a.groups);
+  // Rows of whole 16-byte vectors, or padded with zeros up to one: an x row may then be read past K against rows of w
+  // that are padded too, or (w contiguous along n) masked.
+  const bool x_ok = (a.xk ? a.sxm : a.sxk) % 8 == 0 && (x_cols(a) % 8 == 0 || a.x_padded);
+  const bool w_ok = (a.wk ? a.swn : a.swk) % 8 == 0 && a.swg % 8 == 0 && (w_cols(a) % 8 == 0 || a.w_padded);
+  if (!x_ok) p.pack_x = up(x_rows(a) * up(x_cols(a), 8) * 2, 256);
+  if (!w_ok) p.pack_w = up(w_mem_rows(a) * up(w_cols(a), 8) * 2, 256);
+  // all groups' weights are only worth copying if most of them are used by several rows
+  if (p.pack_w && a.mode == MM_ROW_GROUPS && a.M < 16 * groups) return Plan{KIND_ANY, 1, 0, 0, 0};
+  const int64_t n = w_rows(a);
+  const int64_t rows = a.mode == MM_ROW_GROUPS ? a.M / std::max<int64_t>(1, std::min(groups, a.M)) : a.M;
+  if (a.xk && a.wk) {
+    // the tiles' waves share x, the split of k over waves fills the chip when there are few tiles
+    const bool fill = row_tiles(a, Low::BM) * ceil_div(n, Low::BN) >= 512;
+    if (rows <= 16 && !fill) return p.kind = KIND_FEW1, p;
+    if (rows <= 32 && !fill) return p.kind = KIND_FEW2, p;
+  }
+  // Tiles and splits of k by an estimate of the time: rounds of workgroups (256 CUs, `occ` each) of `steps` 64-k steps,
+  // each workgroup's start and epilogue, and a split's sums written, read and joined (measured constants, us).
+  struct Tile { int kind; int64_t bm, bn; int occ; double step, fixed; };
+  const Tile tiles[] = {{KIND_BIG, Big::BM, Big::BN, 1, kBigStep, 10}, {KIND_MID, Mid::BM, Mid::BN, 2, kMidStep, 7}, {KIND_LOW, Low::BM, Low::BN, 2, kLowStep, 6}};
+  const int64_t k = a.mode == MM_K_GROUPS ? std::max<int64_t>(1, a.K / groups) : a.K, steps = ceil_div(k, 64);
+  double best = 0;
+  for (const Tile& t : tiles) {
+    double count = (double)ceil_div(n, t.bn);
+    if (a.mode == MM_ROW_GROUPS) count *= std::max<double>((double)ceil_div(rows, t.bm) * std::min(groups, a.M), a.M / (double)t.bm);
+    else count *= (double)ceil_div(a.M, t.bm) * (a.mode == MM_K_GROUPS ? groups : 1);
+    for (int64_t s = 1; s <= 16 && (s == 1 || (a.mode == MM_DENSE && s * 4 <= steps)); ++s) {
+      const double rounds = std::max(1.0, std::ceil(count * s / (256.0 * t.occ)));
+      double us = rounds * (t.step * ceil_div(steps, s) + t.fixed);
+      if (s > 1) us += 5 + s * (double)a.M * n * 8 / 4e6;
+      if (best == 0 || us < best) best = us, p.kind = t.kind, p.splits = (int)s;
+    }
+  }
+  if (p.splits > 1) {
+    p.splits = (int)ceil_div(steps, ceil_div(steps, p.splits));  // none empty
+    p.part = up((int64_t)p.splits * a.M * (glu ? 2 : 1) * up(a.N, 8) * 4, 256);
+  }
+  return p;
+}
+
 template <typename T, class C, bool XK, bool WK, bool GLU>
-hipError_t launch_tile_c(MmArgs a, hipStream_t s) {
+hipError_t launch_tile_c(const MmArgs& a, int splits, hipStream_t s) {
   const int64_t tiles = ceil_div(a.N, GLU ? C::BN / 2 : C::BN) * row_tiles(a, C::BM);
   if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
   constexpr int lds = C::S * (C::BM + C::BN) * C::BK * 2;
@@ -815,63 +957,91 @@ hipError_t launch_tile_c(MmArgs a, hipStream_t s) {
   static std::atomic<uint64_t> done{0};
   const hipError_t set = allow_lds(reinterpret_cast<const void*>(fn), lds, &done);
   if (set != hipSuccess) return set;
-  hipLaunchKernelGGL(fn, dim3((unsigned)tiles, a.mode == MM_K_GROUPS ? (unsigned)a.groups : 1u), dim3(C::TH), lds, s, a);
+  hipLaunchKernelGGL(fn, dim3((unsigned)tiles, a.mode == MM_K_GROUPS ? (unsigned)a.groups : (unsigned)splits), dim3(C::TH), lds, s, a);
+  if (splits > 1)
+    hipLaunchKernelGGL((k_mm_join<T, GLU>), dim3((unsigned)ceil_div(a.M * ceil_div(a.N, 8), 256)), dim3(256), 0, s, a, splits);
   return hipGetLastError();
 }
 
 template <typename T, int MT, bool GLU>
-hipError_t launch_few(MmArgs a, hipStream_t s) {
+hipError_t launch_few(const MmArgs& a, hipStream_t s) {
   const int64_t slices = ceil_div(a.N, GLU ? 8 : 16), jobs = slices * row_tiles(a, 16 * MT);
   if (jobs > kMaxTiles) return hipErrorInvalidConfiguration;
   // waves per workgroup: about 16 per CU over the launch, each with at least two chunks of k
   int waves = 16;
   while (waves > 1 && (jobs * waves > 8192 || waves * 128 > a.K + 127)) waves /= 2;
-  hipLaunchKernelGGL((k_mm_few<T, MT, GLU>), dim3((unsigned)jobs), dim3(64 * waves), std::max(waves * MT * 1024, 1024), s, a, (int)slices);
+  hipLaunchKernelGGL((k_mm_few<T, MT, GLU>), dim3((unsigned)jobs), dim3(64 * waves), waves * MT * 1024, s, a, (int)slices);
   return hipGetLastError();
 }
 
 template <typename T, bool XK, bool WK, bool GLU>
-hipError_t launch_tile(const MmArgs& a, hipStream_t s) {
-  typedef TileCfg<256, 256, 2, 4, 64, 2, true> Big;
-  typedef TileCfg<128, 128, 2, 2, 64, 2, false> Mid;
-  typedef TileCfg<64, 128, 1, 4, 64, 3, false> Low;
-  const int64_t z = a.mode == MM_K_GROUPS ? a.groups : 1, n = GLU ? 2 * a.N : a.N;
-  const int64_t rows = a.mode == MM_ROW_GROUPS ? a.M / std::max<int64_t>(1, std::min<int64_t>(a.groups, a.M)) : a.M;
+hipError_t launch_kind(const MmArgs& a, const Plan& p, hipStream_t s) {
   if constexpr (XK && WK) {
-    // the tiles' waves share x, the split of k fills the chip when there are few tiles
-    const bool fill = row_tiles(a, 64) * ceil_div(n, 128) >= 512;
-    if (rows <= 16 && !fill) return launch_few<T, 1, GLU>(a, s);
-    if (rows <= 32 && !fill) return launch_few<T, 2, GLU>(a, s);
+    if (p.kind == KIND_FEW1) return launch_few<T, 1, GLU>(a, s);
+    if (p.kind == KIND_FEW2) return launch_few<T, 2, GLU>(a, s);
   }
-  if (rows > 128 && ceil_div(rows, 256) * ceil_div(n, 256) * z >= 200) return launch_tile_c<T, Big, XK, WK, GLU>(a, s);
-  if (rows > 64) return launch_tile_c<T, Mid, XK, WK, GLU>(a, s);
-  return launch_tile_c<T, Low, XK, WK, GLU>(a, s);
+  if (p.kind == KIND_BIG) return launch_tile_c<T, Big, XK, WK, GLU>(a, p.splits, s);
+  if (p.kind == KIND_MID) return launch_tile_c<T, Mid, XK, WK, GLU>(a, p.splits, s);
+  return launch_tile_c<T, Low, XK, WK, GLU>(a, p.splits, s);
 }
 
-}  // namespace
+template <typename T>
+hipError_t launch_pack(const void* src, int64_t rows, int64_t cols, int64_t ld, int64_t group_rows, int64_t sg, void* dst, hipStream_t s) {
+  const int64_t blocks = ceil_div(rows * ceil_div(cols, 8), 256);
+  if (blocks > kMaxTiles * 2) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((k_mm_pack<T>), dim3((unsigned)blocks), dim3(256), 0, s, (const T*)src, rows, cols, ld, group_rows, sg, (T*)dst);
+  return hipGetLastError();
+}
 
-hipError_t launch_matmul(const MmArgs& in, hipStream_t s) {
-  MmArgs a = in;
-  const bool glu = a.act == EFF_ACT_SWIGLU, xk = a.sxk == 1, wk = a.swk == 1;
-  // 16-byte copies: aligned matrices whose contiguous side is whole vectors
-  const bool direct = aligned16({a.x, a.w}, {xk ? a.sxm : a.sxk, wk ? a.swn : a.swk, a.swg, xk && !(a.x_padded && !wk) ? a.K : 0, xk || a.x_padded ? 0 : a.M, wk ? 0 : a.N}, 2) &&
-                      (xk || !wk);
-  a.vec = aligned16({a.y, a.bias, a.residual, a.pre}, {a.N, a.ldy, a.syg, a.residual ? a.ldr : 0, a.pre ? a.ldp : 0}, 2);
-  auto go = [&](auto t) -> hipError_t {
-    typedef decltype(t) T;
-    if (direct) {
-      if (xk && wk) return glu ? launch_tile<T, true, true, true>(a, s) : launch_tile<T, true, true, false>(a, s);
-      if (xk) return launch_tile<T, true, false, false>(a, s);
-      return launch_tile<T, false, false, false>(a, s);
-    }
+template <typename T>
+hipError_t launch_typed(MmArgs a, Plan p, char* ws, hipStream_t s) {
+  const bool glu = a.act == EFF_ACT_SWIGLU;
+  if ((!p.pack_x && (uintptr_t)a.x % 16) || (!p.pack_w && (uintptr_t)a.w % 16)) p.kind = KIND_ANY;
+  if (p.kind == KIND_ANY) {
     const int64_t tiles = ceil_div(a.N, glu ? kAnyBN / 2 : kAnyBN) * row_tiles(a, kAnyBM);
     if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)tiles, a.mode == MM_K_GROUPS ? (unsigned)a.groups : 1u);
     if (glu) hipLaunchKernelGGL((k_mm_any<T, true>), g, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_mm_any<T, false>), g, dim3(256), 0, s, a);
     return hipGetLastError();
-  };
-  return a.dtype == EFF_DT_BF16 ? go(bf16_t{}) : go(f16_t{});
+  }
+  if (p.pack_x) {
+    const int64_t ld = up(x_cols(a), 8);
+    const hipError_t err = launch_pack<T>(a.x, x_rows(a), x_cols(a), a.xk ? a.sxm : a.sxk, x_rows(a), 0, ws, s);
+    if (err != hipSuccess) return err;
+    a.x = ws, a.x_padded = 1;
+    (a.xk ? a.sxm : a.sxk) = ld;
+  }
+  if (p.pack_w) {
+    const int64_t ld = up(w_cols(a), 8), rows = a.wk ? w_rows(a) : a.K;
+    const hipError_t err = launch_pack<T>(a.w, w_mem_rows(a), w_cols(a), a.wk ? a.swn : a.swk, rows, a.swg, ws + p.pack_x, s);
+    if (err != hipSuccess) return err;
+    a.w = ws + p.pack_x, a.w_padded = 1;
+    (a.wk ? a.swn : a.swk) = ld;
+    a.swg = rows * ld;
+  }
+  if (p.splits > 1) {
+    a.part = reinterpret_cast<float*>(ws + p.pack_x + p.pack_w);
+    a.ldpart = (glu ? 2 : 1) * up(a.N, 8);
+    a.split_steps = (int)ceil_div(ceil_div(a.K, 64), p.splits);
+  }
+  if (a.xk && a.wk) return glu ? launch_kind<T, true, true, true>(a, p, s) : launch_kind<T, true, true, false>(a, p, s);
+  return a.xk ? launch_kind<T, true, false, false>(a, p, s) : launch_kind<T, false, false, false>(a, p, s);
+}
+
+}  // namespace
+
+int64_t matmul_workspace(const MmArgs& a) {
+  const Plan p = plan_matmul(a);
+  return p.pack_x + p.pack_w + p.part;
+}
+
+hipError_t launch_matmul(const MmArgs& in, void* workspace, hipStream_t s) {
+  MmArgs a = in;
+  a.vec = aligned16({a.y, a.bias, a.residual, a.pre}, {a.N, a.ldy, a.syg, a.residual ? a.ldr : 0, a.pre ? a.ldp : 0}, 2);
+  const Plan p = plan_matmul(a);
+  char* ws = static_cast<char*>(workspace);
+  return a.dtype == EFF_DT_BF16 ? launch_typed<bf16_t>(a, p, ws, s) : launch_typed<f16_t>(a, p, ws, s);
 }
 
 // row tiles of the pass over dz, and of its partial sums

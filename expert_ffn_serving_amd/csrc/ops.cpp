@@ -51,11 +51,46 @@ const char* check_desc(const eff_matmul_desc* d) {
 int64_t w_rows(const eff_matmul_desc* d) { return d->act == EFF_ACT_SWIGLU ? 2 * d->n : d->n; }
 bool inputs_ld_bad(int64_t ld) { return ld < 0; }
 
-// the backward pass materialises dz unless it is dy itself
-bool needs_dz(const eff_matmul_desc* d) { return d->act != EFF_ACT_NONE || d->out_dtype != d->dtype; }
+// The products of a description: the forward one, and the two of the backward pass (pointers unset).
+MmArgs forward_args(const eff_matmul_desc* d) {
+  MmArgs a = {};
+  a.dtype = d->dtype, a.y_f32 = d->out_dtype == EFF_DT_F32, a.act = d->act, a.groups = d->groups;
+  a.mode = d->groups ? MM_ROW_GROUPS : MM_DENSE;
+  a.xk = 1, a.sxm = d->ld_x, a.sxk = 1;
+  a.wk = 1, a.swn = d->ld_w, a.swk = 1, a.swg = d->groups ? d->stride_w : 0;
+  a.M = d->m, a.N = d->n, a.K = d->k;
+  a.ldr = d->ld_residual, a.ldy = d->ld_y, a.ldp = d->ld_pre;
+  return a;
+}
+// The backward pass materialises dz unless it is dy itself, in rows that can be read as 16-byte vectors.
 int64_t dz_ld(const eff_matmul_desc* d) { return (w_rows(d) + 7) / 8 * 8; }
+bool needs_dz(const eff_matmul_desc* d) {
+  return d->act != EFF_ACT_NONE || d->out_dtype != d->dtype || d->n % 8 || d->ld_y % 8;
+}
 int64_t dz_bytes(const eff_matmul_desc* d) { return needs_dz(d) ? align256(d->m * dz_ld(d) * 2) : 0; }
 int64_t part_bytes(const eff_matmul_desc* d) { return align256(matmul_dz_tiles(d->m, d->groups) * w_rows(d) * 4); }
+// dx[m,k] = sum over W's rows n of dz[m,n] w[n,k]
+MmArgs dx_args(const eff_matmul_desc* d) {
+  MmArgs a = {};
+  a.dtype = d->dtype, a.groups = d->groups;
+  a.mode = d->groups ? MM_ROW_GROUPS : MM_DENSE;
+  a.xk = 1, a.sxm = needs_dz(d) ? dz_ld(d) : d->ld_y, a.sxk = 1, a.x_padded = needs_dz(d);
+  a.swn = 1, a.swk = d->ld_w, a.swg = d->groups ? d->stride_w : 0;
+  a.M = d->m, a.N = d->k, a.K = w_rows(d);
+  a.ldy = d->ld_dx;
+  return a;
+}
+// dw[n,k] = sum over rows m of dz[m,n] x[m,k]
+MmArgs dw_args(const eff_matmul_desc* d) {
+  MmArgs a = {};
+  a.dtype = d->dtype, a.groups = d->groups;
+  a.mode = d->groups ? MM_K_GROUPS : MM_DENSE;
+  a.sxm = 1, a.sxk = needs_dz(d) ? dz_ld(d) : d->ld_y, a.x_padded = needs_dz(d);
+  a.swn = 1, a.swk = d->ld_x;
+  a.M = w_rows(d), a.N = d->k, a.K = d->m;
+  a.ldy = d->ld_dw, a.syg = d->groups ? d->stride_dw : 0;
+  return a;
+}
 
 int check_ws(const char* fn, int64_t need, const void* ws, size_t bytes) {
   if (need <= 0) return EFF_OK;
@@ -77,7 +112,9 @@ extern "C" {
 
 int64_t eff_matmul_workspace(const eff_matmul_desc* d, int backward) {
   if (const char* why = check_desc(d)) return bad("eff_matmul_workspace", why);
-  return backward ? dz_bytes(d) + part_bytes(d) : 0;
+  if (d->m == 0) return 0;
+  if (!backward) return align256(matmul_workspace(forward_args(d)));
+  return dz_bytes(d) + part_bytes(d) + align256(std::max(matmul_workspace(dx_args(d)), matmul_workspace(dw_args(d))));
 }
 
 int eff_matmul(const eff_matmul_desc* d, const void* x, const void* w, const void* bias, const void* residual,
@@ -91,18 +128,9 @@ int eff_matmul(const eff_matmul_desc* d, const void* x, const void* w, const voi
   if (inputs_ld_bad(d->ld_x) || inputs_ld_bad(d->ld_w) || inputs_ld_bad(d->ld_residual) || d->stride_w < 0) return bad(fn, "negative stride");
   if (d->m > 1 && (d->ld_y < d->n || (pre && d->ld_pre < nw))) return bad(fn, "rows of an output overlap");
   if (int rc = check_ws(fn, eff_matmul_workspace(d, 0), workspace, workspace_bytes)) return rc;
-  MmArgs a = {};
-  a.dtype = d->dtype;
-  a.mode = d->groups ? MM_ROW_GROUPS : MM_DENSE;
-  a.groups = d->groups;
-  a.offsets = offsets;
-  a.x = x, a.sxm = d->ld_x, a.sxk = 1;
-  a.w = w, a.swn = d->ld_w, a.swk = 1, a.swg = d->stride_w;
-  a.M = d->m, a.N = d->n, a.K = d->k;
-  a.bias = bias, a.residual = residual, a.ldr = d->ld_residual;
-  a.y = y, a.ldy = d->ld_y, a.y_f32 = d->out_dtype == EFF_DT_F32;
-  a.pre = pre, a.ldp = d->ld_pre, a.act = d->act;
-  return launched(fn, launch_matmul(a, (hipStream_t)stream));
+  MmArgs a = forward_args(d);
+  a.x = x, a.w = w, a.offsets = offsets, a.bias = bias, a.residual = residual, a.y = y, a.pre = pre;
+  return launched(fn, launch_matmul(a, workspace, (hipStream_t)stream));
 }
 
 int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x, const void* w, const void* pre,
@@ -129,33 +157,21 @@ int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x,
   g.offsets = offsets, g.groups = d->groups;
   g.dbias = dbias;
   const void* dz = dy;
-  int64_t lddz = d->ld_y;
-  if (needs_dz(d) && (dx || dw)) {
-    g.dz = workspace, g.lddz = dz_ld(d);
-    dz = workspace, lddz = g.lddz;
-  }
-  if (dbias) g.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + dz_bytes(d));
+  char* ws = static_cast<char*>(workspace);
+  if (needs_dz(d) && (dx || dw)) dz = g.dz = ws, g.lddz = dz_ld(d);
+  if (dbias) g.part = reinterpret_cast<float*>(ws + dz_bytes(d));
   if (g.dz || dbias)
     if (int rc = launched(fn, launch_matmul_dz(g, s))) return rc;
-  MmArgs a = {};
-  a.dtype = d->dtype;
-  a.groups = d->groups;
-  a.offsets = offsets;
-  if (dx && rows) {  // dx[m,k] = sum over W's rows n of dz[m,n] w[n,k]
-    a.mode = d->groups ? MM_ROW_GROUPS : MM_DENSE;
-    a.x = dz, a.sxm = lddz, a.sxk = 1, a.x_padded = g.dz != nullptr;
-    a.w = w, a.swn = 1, a.swk = d->ld_w, a.swg = d->stride_w;
-    a.M = d->m, a.N = d->k, a.K = nw;
-    a.y = dx, a.ldy = d->ld_dx;
-    if (int rc = launched(fn, launch_matmul(a, s))) return rc;
+  if (ws) ws += dz_bytes(d) + part_bytes(d);
+  if (dx && rows) {
+    MmArgs a = dx_args(d);
+    a.x = dz, a.w = w, a.y = dx, a.offsets = offsets;
+    if (int rc = launched(fn, launch_matmul(a, ws, s))) return rc;
   }
-  if (dw) {  // dw[n,k] = sum over rows m of dz[m,n] x[m,k]
-    a.mode = d->groups ? MM_K_GROUPS : MM_DENSE;
-    a.x = dz, a.sxm = 1, a.sxk = lddz, a.x_padded = g.dz != nullptr;
-    a.w = x, a.swn = 1, a.swk = d->ld_x, a.swg = 0;
-    a.M = nw, a.N = d->k, a.K = d->m;
-    a.y = dw, a.ldy = d->ld_dw, a.syg = d->stride_dw;
-    if (int rc = launched(fn, launch_matmul(a, s))) return rc;
+  if (dw) {
+    MmArgs a = dw_args(d);
+    a.x = dz, a.w = x, a.y = dw, a.offsets = offsets;
+    if (int rc = launched(fn, launch_matmul(a, ws, s))) return rc;
   }
   return EFF_OK;
 }
