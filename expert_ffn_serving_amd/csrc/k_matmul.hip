@@ -331,11 +331,11 @@ __device__ inline int swz_rows(int row) {
 // operand contiguous along its index, LDS row = k: pairs of chunks (32 bytes) move
 __device__ inline int swz_k(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
 
-// BM x BN tile, WM x WN waves, BK k per step, S steps in LDS; PP: two groups of 4 waves take turns (below)
-template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_, bool PP_>
+// BM x BN tile, WM x WN waves, BK k per step, S steps in LDS; AHEAD: operands are read half a step ahead (below)
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_, bool AHEAD_>
 struct TileCfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_, TH = 64 * WM_ * WN_;
-  static constexpr bool PP = PP_;
+  static constexpr bool AHEAD = AHEAD_;
 };
 
 // subtiles of 16 rows per wave that the epilogue's LDS holds at once
@@ -371,8 +371,12 @@ k_mm_tile(MmArgs a) {
     nt_i = blockIdx.x % nt;
     if (!find_tile<BM>(a.offsets, a.groups, a.M, mt_i, reinterpret_cast<int*>(s_tile), &g, &m0, &m1)) return;
   } else {
-    mt_i = blockIdx.x / nt;
-    nt_i = blockIdx.x % nt;
+    // Workgroups go to the 8 XCDs in turn, each with its own L2: an XCD takes a contiguous part of the tiles, in bands of
+    // 8 row tiles walked column by column, so that the tiles it has in flight share rows of x and of W.
+    const int all = gridDim.x, xcd = blockIdx.x & 7, id = xcd * (all >> 3) + min(xcd, all & 7) + (blockIdx.x >> 3);
+    const int mts = all / nt, band = id / (8 * nt), in_band = id - band * 8 * nt, height = min(8, mts - band * 8);
+    mt_i = band * 8 + in_band % height;
+    nt_i = in_band / height;
     m0 = (int64_t)mt_i * BM;
     m1 = min(a.M, m0 + BM);
     if (a.mode == MM_K_GROUPS) {
@@ -385,12 +389,14 @@ k_mm_tile(MmArgs a) {
   }
   const int64_t n0 = (int64_t)nt_i * BNH;
 
-  // this thread's copies: source of step 0 and bytes between steps
+  // this thread's copies: byte offsets from a uniform address that advances with the steps (the host keeps them < 2^31)
   const T* x = reinterpret_cast<const T*>(a.x);
   const T* w = reinterpret_cast<const T*>(a.w) + (a.mode == MM_ROW_GROUPS ? g * a.swg : 0);
   const int64_t xcols = a.x_padded ? (a.M + 7) & ~(int64_t)7 : a.M;  // x contiguous along m
   const int64_t wcols = a.w_padded ? (a.N + 7) & ~(int64_t)7 : a.N;  // w contiguous along n
-  const char *px[SX], *pw[SW];
+  const char* bx = reinterpret_cast<const char*>(XK ? x + m0 * a.sxm + k0 : x + k0 * a.sxk + m0);
+  const char* bw = reinterpret_cast<const char*>(WK ? w + n0 * a.swn + k0 : w + k0 * a.swk + n0);
+  uint32_t ox[SX], ow[SW];
   int kx[SX], kw[SW];  // the copy's first k inside a step
 #pragma unroll
   for (int i = 0; i < SX; ++i) {
@@ -398,12 +404,12 @@ k_mm_tile(MmArgs a) {
     if (XK) {
       const int row = idx / CK, c = (idx % CK) ^ swz_rows<BK, 1>(row);
       kx[i] = c * 8;
-      px[i] = reinterpret_cast<const char*>(x + min(m0 + row, m1 - 1) * a.sxm + k0 + c * 8);
+      ox[i] = (uint32_t)((min((int64_t)row, m1 - 1 - m0) * a.sxm + c * 8) * 2);
     } else {
       constexpr int CH = BM / 8;
       const int k = idx / CH, p = idx % CH, c = ((((p >> 1) ^ swz_k(k)) << 1) | (p & 1)) % CH;
       kx[i] = k;
-      px[i] = reinterpret_cast<const char*>(x + (k0 + k) * a.sxk + min(m0 + c * 8, xcols - 8));
+      ox[i] = (uint32_t)((k * a.sxk + min((int64_t)c * 8, xcols - 8 - m0)) * 2);
     }
   }
 #pragma unroll
@@ -412,17 +418,17 @@ k_mm_tile(MmArgs a) {
     if (WK) {
       const int row = idx / CK, c = (idx % CK) ^ swz_rows<BK, RUN>(row);
       const int col = (row / TN) * TNH + (row % TNH);
-      const int64_t wr = min(n0 + col, a.N - 1) + (GLU && (row % TN) >= TNH ? a.N : 0);
       kw[i] = c * 8;
-      pw[i] = reinterpret_cast<const char*>(w + wr * a.swn + k0 + c * 8);
+      ow[i] = (uint32_t)((min((int64_t)col, a.N - 1 - n0) * a.swn + c * 8) * 2);
     } else {
       constexpr int CH = BN / 8;
       const int k = idx / CH, p = idx % CH, c = ((((p >> 1) ^ swz_k(k)) << 1) | (p & 1)) % CH;
       kw[i] = k;
-      pw[i] = reinterpret_cast<const char*>(w + (k0 + k) * a.swk + min(n0 + c * 8, wcols - 8));
+      ow[i] = (uint32_t)((k * a.swk + min((int64_t)c * 8, wcols - 8 - n0)) * 2);
     }
   }
   const int64_t stepx = XK ? BK * 2 : a.sxk * (BK * 2), stepw = WK ? BK * 2 : a.swk * (BK * 2);
+  const int64_t up_rows = GLU ? a.N * a.swn * 2 : 0;  // bytes from gate to up rows
   const uint32_t lds0 = lds_address(s_tile);
   const int64_t klen = k1 - k0;
   const int steps = (int)((klen + BK - 1) / BK);
@@ -430,22 +436,21 @@ k_mm_tile(MmArgs a) {
   auto issue = [&](int t) {
     const uint32_t base = lds0 + (t % S) * STEP + wave * 1024;
     const int left = (int)min((int64_t)BK, klen - (int64_t)t * BK);
+    const char *sx = bx + t * stepx, *sw = bw + t * stepw;
+    // a wave copies whole rows, on one side of a tile's gate and up rows
+    auto side = [&](int i) { return GLU && ((i * TH + wave * 64) / CK) % TN >= TNH ? sw + up_rows : sw; };
     if (left == BK) {
 #pragma unroll
-      for (int i = 0; i < SX; ++i) lds_copy16(px[i], base + i * (TH * 16));
+      for (int i = 0; i < SX; ++i) lds_copy16(sx, ox[i], base + i * (TH * 16));
 #pragma unroll
-      for (int i = 0; i < SW; ++i) lds_copy16(pw[i], base + XB + i * (TH * 16));
+      for (int i = 0; i < SW; ++i) lds_copy16(side(i), ow[i], base + XB + i * (TH * 16));
     } else {
       const char* zero = reinterpret_cast<const char*>(g_zero16);
 #pragma unroll
-      for (int i = 0; i < SX; ++i) lds_copy16(kx[i] < left ? px[i] : zero, base + i * (TH * 16));
+      for (int i = 0; i < SX; ++i) lds_copy16(kx[i] < left ? sx + ox[i] : zero, base + i * (TH * 16));
 #pragma unroll
-      for (int i = 0; i < SW; ++i) lds_copy16(kw[i] < left ? pw[i] : zero, base + XB + i * (TH * 16));
+      for (int i = 0; i < SW; ++i) lds_copy16(kw[i] < left ? side(i) + ow[i] : zero, base + XB + i * (TH * 16));
     }
-#pragma unroll
-    for (int i = 0; i < SX; ++i) px[i] += stepx;
-#pragma unroll
-    for (int i = 0; i < SW; ++i) pw[i] += stepw;
   };
 
   f32x4_t acc[MT][NT];
@@ -482,53 +487,69 @@ k_mm_tile(MmArgs a) {
     }
   };
 
-  V8 fw[NT], fx[MT];
-  auto read = [&](int t, int ks) {
-    const uint8_t* b = s_tile + (t % S) * STEP;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) fw[j] = frag_w(b, j, ks);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) fx[i] = frag_x(b, i, ks);
-  };
-  auto multiply = [&] {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = mfma(fw[j], fx[i], acc[i][j]);
-  };
   // this wave's copies of every step up to the last CP * N issued ones are in LDS
   auto arrived = [&](bool all) {
     if (all) vm_wait<0>();
     else vm_wait<(S - 2) * CP>();
   };
+  auto buffer = [&](int t) { return s_tile + (t % S) * STEP; };
 
 #pragma unroll
   for (int t = 0; t < S - 1; ++t)
     if (t < steps) issue(t);
-  if constexpr (C::PP) {
-    // Two groups of 4 waves, one of each on every SIMD, half a step apart: while one group multiplies (at raised
-    // priority) the other reads its next operands from LDS and issues copies.  A barrier ends each half.
-    static_assert(TH == 512, "two groups of 4 waves");
-    const bool second = wave >= 4;
-    arrived(S - 1 > steps);
-    meet();
-    if (second) meet();
-    for (int t = 0; t < steps; ++t) {
-      const bool tail = t + S - 1 >= steps;
+  if constexpr (C::AHEAD) {
+    // One wave's products hide its LDS reads: an x operand is read again for the next half step as soon as its products
+    // are issued, the w operands are read one half step ahead into a second set.  The barrier of a step stands inside the
+    // last half's products, when the reads before it have long returned.
+    static_assert(KS == 2 && S == 2, "two halves, two buffers");
+    V8 fw[2][NT], fx[MT];
+    auto products = [&](int from, int i) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if (ks == 0 && !tail) issue(t + S - 1);
-        read(t, ks);
-        if (ks == KS - 1 && second) arrived(tail);
-        meet();
-        __builtin_amdgcn_s_setprio(1);
-        multiply();
-        __builtin_amdgcn_s_setprio(0);
-        if (ks == KS - 1 && !second) arrived(tail);
-        meet();
+      for (int j = 0; j < NT; ++j) acc[i][j] = mfma(fw[from][j], fx[i], acc[i][j]);
+    };
+    auto read_w = [&](int into, const uint8_t* b, int ks) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fw[into][j] = frag_w(b, j, ks);
+    };
+    if (steps > 0) {
+      arrived(true);
+      meet();
+      if (steps > 1) issue(1);
+      read_w(0, buffer(0), 0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fx[i] = frag_x(buffer(0), i, 0);
+      for (int t = 0; t < steps - 1; ++t) {
+        const uint8_t *b = buffer(t), *next = buffer(t + 1);
+        read_w(1, b, 1);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          products(0, i);
+          fx[i] = frag_x(b, i, 1);
+        }
+        products(1, 0);
+        products(1, 1);
+        arrived(true);
+        meet();                      // step t + 1 is in LDS and step t in registers
+        if (t + 2 < steps) issue(t + 2);
+        read_w(0, next, 0);
+        fx[0] = frag_x(next, 0, 0);
+        fx[1] = frag_x(next, 1, 0);
+#pragma unroll
+        for (int i = 2; i < MT; ++i) {
+          products(1, i);
+          fx[i] = frag_x(next, i, 0);
+        }
       }
+      const uint8_t* b = buffer(steps - 1);
+      read_w(1, b, 1);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        products(0, i);
+        fx[i] = frag_x(b, i, 1);
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) products(1, i);
     }
-    if (!second) meet();
   } else {
     for (int t = 0; t < steps; ++t) {
       arrived(t + S - 1 > steps);
@@ -536,8 +557,15 @@ k_mm_tile(MmArgs a) {
       if (t + S - 1 < steps) issue(t + S - 1);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        read(t, ks);
-        multiply();
+        V8 fw[NT], fx[MT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fw[j] = frag_w(buffer(t), j, ks);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) fx[i] = frag_x(buffer(t), i, ks);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[i][j] = mfma(fw[j], fx[i], acc[i][j]);
       }
     }
   }
@@ -883,7 +911,6 @@ hipError_t allow_lds(const void* fn, int bytes, std::atomic<uint64_t>* done) {
 
 // ---- which kernel ----------------------------------------------------------------------------------------
 
-constexpr double kBigStep = 1.63, kMidStep = 1.16, kLowStep = 0.8;
 enum { KIND_ANY, KIND_FEW1, KIND_FEW2, KIND_BIG, KIND_MID, KIND_LOW };
 typedef TileCfg<256, 256, 2, 4, 64, 2, true> Big;
 typedef TileCfg<128, 128, 2, 2, 64, 2, false> Mid;
@@ -894,6 +921,7 @@ struct Plan {
   int64_t pack_x, pack_w, part;  // workspace bytes of each (multiples of 256)
 };
 
+constexpr int64_t kMaxStride = (int64_t)1 << 22;
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 int64_t w_rows(const MmArgs& a) { return a.act == EFF_ACT_SWIGLU ? 2 * a.N : a.N; }
 // rows and contiguous values of an operand in memory
@@ -910,8 +938,10 @@ Plan plan_matmul(const MmArgs& a) {
   const int64_t groups = std::max(1, a.groups);
   // Rows of whole 16-byte vectors, or padded with zeros up to one: an x row may then be read past K against rows of w
   // that are padded too, or (w contiguous along n) masked.
-  const bool x_ok = (a.xk ? a.sxm : a.sxk) % 8 == 0 && (x_cols(a) % 8 == 0 || a.x_padded);
-  const bool w_ok = (a.wk ? a.swn : a.swk) % 8 == 0 && a.swg % 8 == 0 && (w_cols(a) % 8 == 0 || a.w_padded);
+  // The tiles' byte offsets are 32 bits: 256 rows of less than 2^22 values.
+  const int64_t ldx = a.xk ? a.sxm : a.sxk, ldw = a.wk ? a.swn : a.swk;
+  const bool x_ok = ldx % 8 == 0 && ldx < kMaxStride && (x_cols(a) % 8 == 0 || a.x_padded);
+  const bool w_ok = ldw % 8 == 0 && ldw < kMaxStride && a.swg % 8 == 0 && (w_cols(a) % 8 == 0 || a.w_padded);
   if (!x_ok) p.pack_x = up(x_rows(a) * up(x_cols(a), 8) * 2, 256);
   if (!w_ok) p.pack_w = up(w_mem_rows(a) * up(w_cols(a), 8) * 2, 256);
   // all groups' weights are only worth copying if most of them are used by several rows
@@ -924,10 +954,13 @@ Plan plan_matmul(const MmArgs& a) {
     if (rows <= 16 && !fill) return p.kind = KIND_FEW1, p;
     if (rows <= 32 && !fill) return p.kind = KIND_FEW2, p;
   }
-  // Tiles and splits of k by an estimate of the time: rounds of workgroups (256 CUs, `occ` each) of `steps` 64-k steps,
-  // each workgroup's start and epilogue, and a split's sums written, read and joined (measured constants, us).
-  struct Tile { int kind; int64_t bm, bn; int occ; double step, fixed; };
-  const Tile tiles[] = {{KIND_BIG, Big::BM, Big::BN, 1, kBigStep, 10}, {KIND_MID, Mid::BM, Mid::BN, 2, kMidStep, 7}, {KIND_LOW, Low::BM, Low::BN, 2, kLowStep, 6}};
+  // Tiles and splits of k by an estimate of the time: rounds of workgroups over 256 CUs (`occ` on each; with one on each
+  // a step is faster), 64-k steps, a workgroup's start and epilogue, and a split's sums written, read and joined.  The
+  // constants (us) fit 4096^3, 8192 x 4096 x {512, 2048}, 2048^3 and 333 x 512 x 2560 to 15 %.
+  struct Tile { int kind; int64_t bm, bn; int occ; double alone, step, fixed; };
+  const Tile tiles[] = {{KIND_BIG, Big::BM, Big::BN, 1, 1.55, 1.55, 14},
+                        {KIND_MID, Mid::BM, Mid::BN, 2, 0.75, 1.0, 7},
+                        {KIND_LOW, Low::BM, Low::BN, 2, 0.42, 0.64, 6}};
   const int64_t k = a.mode == MM_K_GROUPS ? std::max<int64_t>(1, a.K / groups) : a.K, steps = ceil_div(k, 64);
   double best = 0;
   for (const Tile& t : tiles) {
@@ -935,9 +968,10 @@ Plan plan_matmul(const MmArgs& a) {
     if (a.mode == MM_ROW_GROUPS) count *= std::max<double>((double)ceil_div(rows, t.bm) * std::min(groups, a.M), a.M / (double)t.bm);
     else count *= (double)ceil_div(a.M, t.bm) * (a.mode == MM_K_GROUPS ? groups : 1);
     for (int64_t s = 1; s <= 16 && (s == 1 || (a.mode == MM_DENSE && s * 4 <= steps)); ++s) {
-      const double rounds = std::max(1.0, std::ceil(count * s / (256.0 * t.occ)));
-      double us = rounds * (t.step * ceil_div(steps, s) + t.fixed);
-      if (s > 1) us += 5 + s * (double)a.M * n * 8 / 4e6;
+      const double each = (double)ceil_div(steps, s), full = std::floor(count * s / (256.0 * t.occ)), rest = count * s - full * 256 * t.occ;
+      double us = full * (t.step * each + t.fixed);
+      if (rest > 0) us += (rest <= 256 ? t.alone : t.step) * each + t.fixed;
+      if (s > 1) us += 5 + s * (double)a.M * n * 8 / 8e6;
       if (best == 0 || us < best) best = us, p.kind = t.kind, p.splits = (int)s;
     }
   }

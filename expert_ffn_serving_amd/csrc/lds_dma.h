@@ -21,6 +21,11 @@ __device__ inline void lds_copy16(const void* src, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(src) : "memory", "m0");
 }
 
+// the same from base + off: a uniform address and the lane's own byte offset (unsigned)
+__device__ inline void lds_copy16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+
 // waits until at most N vector memory operations of this wave are outstanding.  Loads complete in the
 // order they were issued, so once N is the number of loads issued after a given LDS copy, that copy
 // is complete (stores issued meanwhile only make the wait stricter).
