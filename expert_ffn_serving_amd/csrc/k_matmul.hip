@@ -35,8 +35,16 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f;
 constexpr float kGeluCubic = 0.044715f;
 
-__device__ inline float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
-__device__ inline float act_silu(float z) { return z / (1.0f + expf(-z)); }
+// e^x to about 2 units in the last place for any x that is not NaN: 2^(x log2 e), the product's rounding error put back.
+// (expf and an IEEE division took two thirds of the time of the pass over dz.)
+__device__ inline float exp_f32(float x) {
+  x = fminf(fmaxf(x, -104.f), 89.f);  // past both ends the result is 0 or infinity anyway
+  const float t = x * 1.44269504088896341f, lo = fmaf(x, 1.44269504088896341f, -t) + x * 1.92596299e-8f;
+  return __builtin_amdgcn_exp2f(t) * fmaf(lo, 0.693147180559945309f, 1.0f);
+}
+// 1 / (1 + e^-z), v_rcp_f32 being good to one unit in the last place; NaN stays NaN through its factor z
+__device__ inline float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-z)); }
+__device__ inline float act_silu(float z) { return z * sigmoid(z); }
 __device__ inline float act_one(int act, float z) {
   switch (act) {
     case EFF_ACT_SILU: return act_silu(z);
@@ -45,21 +53,21 @@ __device__ inline float act_one(int act, float z) {
     default: return z;
   }
 }
-// d silu / dz = s + z s (1 - s).  Where s (1 - s) is 0 its product with a large z is 0 too.
-__device__ inline float dact_silu(float z) {
-  const float s = sigmoid(z), t = s * (1.0f - s);
-  return t > 0.f ? fmaf(z, t, s) : s;
+// d silu / dz = s + z s (1 - s), s the sigmoid.  Where s (1 - s) is 0 its product with a large z is 0 too.
+__device__ inline float dact_silu(float z, float s) {
+  const float t = s * (1.0f - s);
+  return t > 0.f ? fmaf(z, t, s) : z == z ? s : z;
 }
 __device__ inline float dact_one(int act, float z) {
   switch (act) {
-    case EFF_ACT_SILU: return dact_silu(z);
+    case EFF_ACT_SILU: return dact_silu(z, sigmoid(z));
     case EFF_ACT_GELU: {
       const float g = expf(-0.5f * z * z) * kInvSqrt2Pi, p = 0.5f * erfcf(-z * kInvSqrt2);
       return g > 0.f ? fmaf(z, g, p) : p;
     }
     case EFF_ACT_GELU_TANH: {
       const float s = sigmoid(2.0f * kSqrt2OverPi * (z + kGeluCubic * z * z * z)), t = s * (1.0f - s);
-      return t > 0.f ? fmaf(z * t, 2.0f * kSqrt2OverPi * fmaf(3.0f * kGeluCubic * z, z, 1.0f), s) : s;
+      return t > 0.f ? fmaf(z * t, 2.0f * kSqrt2OverPi * fmaf(3.0f * kGeluCubic * z, z, 1.0f), s) : z == z ? s : z;
     }
     default: return 1.0f;
   }
@@ -754,22 +762,32 @@ k_mm_few(MmArgs a, int slices) {
 
 // ---- dz and dbias --------------------------------------------------------------------------------------
 //
-// One pass over dy and pre: a workgroup takes 64 rows of one group and 64 VEC columns, each of its 4 waves every
+// One pass over dy and pre: a workgroup takes 32 rows of one group and 64 VEC columns, each of its 4 waves every
 // fourth row.  It writes dz rounded to T (the operand that dx and dw multiply; columns up to lddz are zeroed, so that
 // dz's rows are whole 16-byte vectors) and the columns' fp32 sums over its rows, which a second kernel adds up in row
 // order.  Bound by HBM: every value is read once and written once.
-constexpr int kDzRows = 64;
+constexpr int kDzRows = 32;
 
 template <typename T, int VEC>
-__device__ inline void load_row(const void* p, int64_t i, float* o) {
+struct Piece {
+  typedef T V __attribute__((ext_vector_type(VEC)));
+};
+template <typename T>
+struct Piece<T, 1> {
+  typedef T V;
+};
+template <typename T, int VEC>
+__device__ inline void widen(const typename Piece<T, VEC>::V& v, float* o) {
   if constexpr (VEC == 1) {
-    o[0] = (float)reinterpret_cast<const T*>(p)[i];
+    o[0] = (float)v;
   } else {
-    typedef T V __attribute__((ext_vector_type(VEC)));
-    const V v = *reinterpret_cast<const V*>(reinterpret_cast<const T*>(p) + i);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) o[e] = (float)v[e];
   }
+}
+template <typename T, int VEC>
+__device__ inline typename Piece<T, VEC>::V piece(const void* p, int64_t i) {
+  return *reinterpret_cast<const typename Piece<T, VEC>::V*>(reinterpret_cast<const T*>(p) + i);
 }
 template <typename T, int VEC>
 __device__ inline void store_row(void* p, int64_t i, const float* v) {
@@ -799,31 +817,41 @@ k_mm_dz(MmGrad a, int cols) {
   float sum[VEC], sup[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) sum[e] = sup[e] = 0.f;
-  if (n < a.N)
+  if (n < a.N && m0 + wave < m1) {
+    // a row is in flight while the one before it is used; past the end the last row again (not used)
+    typename Piece<D, VEC>::V dn;
+    typename Piece<T, VEC>::V zn, un;
+    auto fetch = [&](int64_t m) {
+      m = min(m, m1 - 1);
+      dn = piece<D, VEC>(a.dy, m * a.ldy + n);
+      if (a.act != EFF_ACT_NONE) zn = piece<T, VEC>(a.pre, m * a.ldp + n);
+      if (glu) un = piece<T, VEC>(a.pre, m * a.ldp + a.N + n);
+    };
+    fetch(m0 + wave);
     for (int64_t m = m0 + wave; m < m1; m += 4) {
       float d[VEC], z[VEC], u[VEC];
-      load_row<D, VEC>(a.dy, m * a.ldy + n, d);
-      if (a.act != EFF_ACT_NONE) {
-        load_row<T, VEC>(a.pre, m * a.ldp + n, z);
-        if (glu) {
-          load_row<T, VEC>(a.pre, m * a.ldp + a.N + n, u);
+      widen<D, VEC>(dn, d);
+      if (a.act != EFF_ACT_NONE) widen<T, VEC>(zn, z);
+      if (glu) widen<T, VEC>(un, u);
+      fetch(m + 4);
+      if (glu) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float up = d[e] * act_silu(z[e]);
-            d[e] = d[e] * u[e] * dact_silu(z[e]);
-            u[e] = up;
-            sup[e] += up;
-          }
-          if (a.dz) store_row<T, VEC>(a.dz, m * a.lddz + a.N + n, u);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) d[e] *= dact_one(a.act, z[e]);
+        for (int e = 0; e < VEC; ++e) {
+          const float sg = sigmoid(z[e]), up = d[e] * z[e] * sg;
+          d[e] = d[e] * u[e] * dact_silu(z[e], sg);
+          u[e] = up;
+          sup[e] += up;
         }
+        if (a.dz) store_row<T, VEC>(a.dz, m * a.lddz + a.N + n, u);
+      } else if (a.act != EFF_ACT_NONE) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) d[e] *= dact_one(a.act, z[e]);
       }
       if (a.dz) store_row<T, VEC>(a.dz, m * a.lddz + n, d);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) sum[e] += d[e];
     }
+  }
   // the zeros behind a row
   if (a.dz && blockIdx.x % cols == 0 && nw + lane < a.lddz)
     for (int64_t m = m0 + wave; m < m1; m += 4) reinterpret_cast<T*>(a.dz)[m * a.lddz + nw + lane] = (T)0.f;
@@ -871,6 +899,7 @@ k_mm_dbias(MmGrad a) {
   const int64_t count = (hi - lo + kDzRows - 1) / kDzRows, last = min(first + count, a.tiles);
   float sum = 0.f;
   if (n < nw)
+#pragma unroll 8
     for (int64_t t = first + wave; t < last; t += 4) sum += a.part[t * nw + n];
   s_sum[wave][lane] = sum;
   __syncthreads();
@@ -911,8 +940,9 @@ hipError_t allow_lds(const void* fn, int bytes, std::atomic<uint64_t>* done) {
 
 // ---- which kernel ----------------------------------------------------------------------------------------
 
-enum { KIND_ANY, KIND_FEW1, KIND_FEW2, KIND_BIG, KIND_MID, KIND_LOW };
+enum { KIND_ANY, KIND_FEW1, KIND_FEW2, KIND_BIG, KIND_WIDE, KIND_MID, KIND_LOW };
 typedef TileCfg<256, 256, 2, 4, 64, 2, true> Big;
+typedef TileCfg<128, 256, 2, 4, 32, 3, false> Wide;
 typedef TileCfg<128, 128, 2, 2, 64, 2, false> Mid;
 typedef TileCfg<64, 128, 1, 4, 64, 3, false> Low;
 
@@ -959,6 +989,7 @@ Plan plan_matmul(const MmArgs& a) {
   // constants (us) fit 4096^3, 8192 x 4096 x {512, 2048}, 2048^3 and 333 x 512 x 2560 to 15 %.
   struct Tile { int kind; int64_t bm, bn; int occ; double alone, step, fixed; };
   const Tile tiles[] = {{KIND_BIG, Big::BM, Big::BN, 1, 1.55, 1.55, 14},
+                        {KIND_WIDE, Wide::BM, Wide::BN, 2, 1.05, 2.05, 8},
                         {KIND_MID, Mid::BM, Mid::BN, 2, 0.75, 1.0, 7},
                         {KIND_LOW, Low::BM, Low::BN, 2, 0.42, 0.64, 6}};
   const int64_t k = a.mode == MM_K_GROUPS ? std::max<int64_t>(1, a.K / groups) : a.K, steps = ceil_div(k, 64);
@@ -1015,6 +1046,7 @@ hipError_t launch_kind(const MmArgs& a, const Plan& p, hipStream_t s) {
     if (p.kind == KIND_FEW2) return launch_few<T, 2, GLU>(a, s);
   }
   if (p.kind == KIND_BIG) return launch_tile_c<T, Big, XK, WK, GLU>(a, p.splits, s);
+  if (p.kind == KIND_WIDE) return launch_tile_c<T, Wide, XK, WK, GLU>(a, p.splits, s);
   if (p.kind == KIND_MID) return launch_tile_c<T, Mid, XK, WK, GLU>(a, p.splits, s);
   return launch_tile_c<T, Low, XK, WK, GLU>(a, p.splits, s);
 }
