@@ -643,7 +643,7 @@ k_mm_join(MmArgs a, int splits) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) z[e] = u[e] = 0.f;
   const float* p = a.part + m * a.ldpart + n;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < splits; ++s, p += a.M * a.ldpart)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -660,36 +660,45 @@ k_mm_join(MmArgs a, int splits) {
 }
 
 // ---- operands that cannot be copied 16 bytes at a time ---------------------------------------------------
-// rows x cols values with any stride into rows of ldp (a multiple of 8) values, zeros behind cols; rows = groups *
-// group_rows.  A thread writes 16 bytes.  Reading and writing the matrix once more is what this costs; the general
-// kernel took 361 us where both of these and the tiles take a tenth (333 x 515 x 2563).
+// rows x cols values with any stride into rows of ceil(cols / 8) * 8 values, zeros behind cols (rows = groups *
+// group_rows), for both operands in one launch.  A thread writes 16 bytes.  Reading and writing the matrix once more
+// is what this costs; the general kernel took 361 us where this and the tiles take 24 (333 x 515 x 2563).
+struct PackJob {
+  const void* src;
+  void* dst;
+  int64_t rows, cols, ld, group_rows, sg, blocks;
+};
+
 template <typename T>
 __global__ void __launch_bounds__(256)
-k_mm_pack(const T* __restrict__ src, int64_t rows, int64_t cols, int64_t ld, int64_t group_rows, int64_t sg, T* __restrict__ dst) {
-  const int64_t vr = (cols + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * vr) return;
+k_mm_pack(PackJob a, PackJob b) {
+  const bool first = blockIdx.x < a.blocks;
+  const PackJob& p = first ? a : b;
+  const int64_t vr = (p.cols + 7) / 8, i = (int64_t)(blockIdx.x - (first ? 0 : a.blocks)) * 256 + threadIdx.x;
+  if (i >= p.rows * vr) return;
   const int64_t row = i / vr, c = i % vr * 8;
-  const T* s = src + (row / group_rows) * sg + (row % group_rows) * ld + c;
+  const T* s = reinterpret_cast<const T*>(p.src) + (row / p.group_rows) * p.sg + (row % p.group_rows) * p.ld + c;
   typename Vec8<T>::V v;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = c + e < cols ? s[e] : (T)0.f;
-  *reinterpret_cast<typename Vec8<T>::V*>(dst + (row * vr * 8 + c)) = v;
+  for (int e = 0; e < 8; ++e) v[e] = c + e < p.cols ? s[e] : (T)0.f;
+  *reinterpret_cast<typename Vec8<T>::V*>(reinterpret_cast<T*>(p.dst) + (row * vr * 8 + c)) = v;
 }
 
 // ---- few rows --------------------------------------------------------------------------------------------
 //
 // Up to 16 MT rows of x against 16 rows of W per workgroup (SwiGLU: 8 gate and 8 up rows), the k split over its waves:
-// bound by the stream of W, so every wave keeps kFewU chunks of 64 k (2 KiB of W each) in flight in registers and nothing
+// bound by the stream of W, so every wave keeps U chunks of 64 k (2 KiB of W each) in flight in registers and nothing
 // waits for a barrier before the end, where the waves' sums meet in LDS in wave order.  The lane of W row r and k group
 // q takes 32 consecutive bytes of a chunk: k = 16 q .. 16 q + 15 (the order of k inside a product is free as long as
 // both operands share it), so a chunk is one 128-byte line of every row.
-constexpr int kFewU = 2;
+template <int MT>
+constexpr int few_unroll() { return MT == 1 ? 4 : 2; }
 
 template <typename T, int MT, bool GLU>
 __global__ void __launch_bounds__(1024)
 k_mm_few(MmArgs a, int slices) {
   typedef typename Vec8<T>::V V8;
-  constexpr int U = kFewU, BM = 16 * MT;
+  constexpr int U = few_unroll<MT>(), BM = 16 * MT;
   extern __shared__ __attribute__((aligned(16))) uint8_t s_few[];
   f32x4_t* s_acc = reinterpret_cast<f32x4_t*>(s_few);                       // [waves][MT][64]
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
@@ -735,13 +744,16 @@ k_mm_few(MmArgs a, int slices) {
   };
 #pragma unroll
   for (int s = 0; s < U; ++s) load(wave + s * waves, s);
-  for (int c = wave; c < chunks; c += U * waves) {
+  int c = wave;
+  for (; c + U * waves < chunks; c += U * waves) {
 #pragma unroll
     for (int s = 0; s < U; ++s) {
       use(c + s * waves, s);
       load(c + (s + U) * waves, s);
     }
   }
+#pragma unroll
+  for (int s = 0; s < U; ++s) use(c + s * waves, s);
 #pragma unroll
   for (int i = 0; i < MT; ++i) s_acc[(wave * MT + i) * 64 + lane] = acc[i];
   __syncthreads();
@@ -1052,14 +1064,6 @@ hipError_t launch_kind(const MmArgs& a, const Plan& p, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t launch_pack(const void* src, int64_t rows, int64_t cols, int64_t ld, int64_t group_rows, int64_t sg, void* dst, hipStream_t s) {
-  const int64_t blocks = ceil_div(rows * ceil_div(cols, 8), 256);
-  if (blocks > kMaxTiles * 2) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((k_mm_pack<T>), dim3((unsigned)blocks), dim3(256), 0, s, (const T*)src, rows, cols, ld, group_rows, sg, (T*)dst);
-  return hipGetLastError();
-}
-
-template <typename T>
 hipError_t launch_typed(MmArgs a, Plan p, char* ws, hipStream_t s) {
   const bool glu = a.act == EFF_ACT_SWIGLU;
   if ((!p.pack_x && (uintptr_t)a.x % 16) || (!p.pack_w && (uintptr_t)a.w % 16)) p.kind = KIND_ANY;
@@ -1071,20 +1075,23 @@ hipError_t launch_typed(MmArgs a, Plan p, char* ws, hipStream_t s) {
     else hipLaunchKernelGGL((k_mm_any<T, false>), g, dim3(256), 0, s, a);
     return hipGetLastError();
   }
-  if (p.pack_x) {
-    const int64_t ld = up(x_cols(a), 8);
-    const hipError_t err = launch_pack<T>(a.x, x_rows(a), x_cols(a), a.xk ? a.sxm : a.sxk, x_rows(a), 0, ws, s);
-    if (err != hipSuccess) return err;
-    a.x = ws, a.x_padded = 1;
-    (a.xk ? a.sxm : a.sxk) = ld;
-  }
-  if (p.pack_w) {
-    const int64_t ld = up(w_cols(a), 8), rows = a.wk ? w_rows(a) : a.K;
-    const hipError_t err = launch_pack<T>(a.w, w_mem_rows(a), w_cols(a), a.wk ? a.swn : a.swk, rows, a.swg, ws + p.pack_x, s);
-    if (err != hipSuccess) return err;
-    a.w = ws + p.pack_x, a.w_padded = 1;
-    (a.wk ? a.swn : a.swk) = ld;
-    a.swg = rows * ld;
+  if (p.pack_x || p.pack_w) {
+    PackJob jobs[2] = {};
+    if (p.pack_x) {
+      int64_t* ld = a.xk ? &a.sxm : &a.sxk;
+      jobs[0] = {a.x, ws, x_rows(a), x_cols(a), *ld, x_rows(a), 0, ceil_div(x_rows(a) * ceil_div(x_cols(a), 8), 256)};
+      a.x = ws, a.x_padded = 1, *ld = up(x_cols(a), 8);
+    }
+    if (p.pack_w) {
+      int64_t* ld = a.wk ? &a.swn : &a.swk;
+      const int64_t rows = a.wk ? w_rows(a) : a.K;
+      jobs[1] = {a.w, ws + p.pack_x, w_mem_rows(a), w_cols(a), *ld, rows, a.swg, ceil_div(w_mem_rows(a) * ceil_div(w_cols(a), 8), 256)};
+      a.w = ws + p.pack_x, a.w_padded = 1, *ld = up(w_cols(a), 8);
+      a.swg = rows * *ld;
+    }
+    const int64_t blocks = jobs[0].blocks + jobs[1].blocks;
+    if (blocks > 2 * kMaxTiles) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((k_mm_pack<T>), dim3((unsigned)blocks), dim3(256), 0, s, jobs[0], jobs[1]);
   }
   if (p.splits > 1) {
     a.part = reinterpret_cast<float*>(ws + p.pack_x + p.pack_w);

@@ -121,6 +121,7 @@ k_sort_place(const int32_t* __restrict__ ids, int64_t n, int E, int bits, int64_
     int total = 0, before = 0;
     if (e < E) {
       if (hist) {
+#pragma unroll 16
         for (int p = 0; p < parts; ++p) {
           const int c = hist[(int64_t)p * E + e];
           total += c;
@@ -211,6 +212,8 @@ k_dispatch(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ pos
   }
 }
 
+constexpr int kAhead = 4;
+
 // grid: (ceil(H / (256 VEC)), T).  out = residual + sum_k w * ys[pos], k ascending in fp32; w null: weights of 1.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
@@ -225,14 +228,31 @@ k_combine_rows(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int32
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
   }
-  for (int k = 0; k < K; ++k) {
-    const int64_t p = pos[t * K + k];
-    if (p < 0 || p >= rows) continue;
-    const float wk = w ? w[t * K + k] : 1.f;
-    float v[VEC];
-    load_f32<T, VEC>(ys + p * ldys + h, v);
+  // kAhead pairs' rows are loaded before the first is added; a pair without a row loads nothing
+  for (int k0 = 0; k0 < K; k0 += kAhead) {
+    typename Pack<T, VEC>::V v[kAhead];
+    float wk[kAhead];
+    bool ok[kAhead];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = fmaf(wk, v[i], acc[i]);
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t at = t * K + min(k0 + i, K - 1);
+      const int64_t p = pos[at];
+      ok[i] = k0 + i < K && p >= 0 && p < rows;
+      if (ok[i]) {
+        wk[i] = w ? w[at] : 1.f;
+        v[i] = *reinterpret_cast<const typename Pack<T, VEC>::V*>(ys + p * ldys + h);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (!ok[i]) continue;
+      if constexpr (VEC == 1) {
+        acc[0] = fmaf(wk[i], (float)v[i], acc[0]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[e] = fmaf(wk[i], (float)v[i][e], acc[e]);
+      }
+    }
   }
   store_f32<T, VEC>(out + t * ldo + h, acc);
 }
