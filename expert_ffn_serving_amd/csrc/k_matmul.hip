@@ -145,6 +145,9 @@ __device__ inline void get_cl(const void* p, int64_t i, int left, bool vec, floa
     const V v = *reinterpret_cast<const V*>(s);
 #pragma unroll
     for (int e = 0; e < CL; ++e) o[e] = (float)v[e];
+  } else if (left == CL) {  // no branch between the loads
+#pragma unroll
+    for (int e = 0; e < CL; ++e) o[e] = (float)s[e];
   } else {
 #pragma unroll
     for (int e = 0; e < CL; ++e) o[e] = e < left ? (float)s[e] : 0.f;
@@ -679,8 +682,13 @@ k_mm_pack(PackJob a, PackJob b) {
   const int64_t row = i / vr, c = i % vr * 8;
   const T* s = reinterpret_cast<const T*>(p.src) + (row / p.group_rows) * p.sg + (row % p.group_rows) * p.ld + c;
   typename Vec8<T>::V v;
+  if (c + 8 <= p.cols) {  // no branch between the loads
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = c + e < p.cols ? s[e] : (T)0.f;
+    for (int e = 0; e < 8; ++e) v[e] = s[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < p.cols ? s[e] : (T)0.f;
+  }
   *reinterpret_cast<typename Vec8<T>::V*>(reinterpret_cast<T*>(p.dst) + (row * vr * 8 + c)) = v;
 }
 

@@ -79,9 +79,11 @@ __device__ inline void place_pairs(const int32_t* ids, int64_t b0, int64_t b1, i
   if (wave >= nw) return;
   int64_t lo, hi;
   wave_part(b0, b1, nw, wave, &lo, &hi);
+  int next = lo + lane < hi ? ids[lo + lane] : -1;
   for (int64_t c = lo; c < hi; c += 64) {
     const int64_t i = c + lane;
-    const int id = i < hi ? ids[i] : -1;
+    const int id = next;
+    next = i + 64 < hi ? ids[i + 64] : -1;  // in flight while this chunk is ranked
     const bool ok = id >= 0 && id < E;
     uint64_t same = __ballot(ok);
     for (int b = 0; b < bits; ++b) {
@@ -121,7 +123,7 @@ k_sort_place(const int32_t* __restrict__ ids, int64_t n, int E, int bits, int64_
     int total = 0, before = 0;
     if (e < E) {
       if (hist) {
-#pragma unroll 16
+#pragma unroll 32
         for (int p = 0; p < parts; ++p) {
           const int c = hist[(int64_t)p * E + e];
           total += c;
@@ -318,11 +320,12 @@ constexpr int64_t kGridY = 65535;  // tokens per launch of the two-dimensional g
 
 // Pairs of one workgroup.  Up to kSortOne pairs one workgroup does the whole sort (one launch).
 constexpr int64_t kSortOne = 8192;
-constexpr int64_t kSortParts = 64;
+constexpr int64_t kSortParts = 128;  // at most; up to 256K pairs 32, whose counts are read in one go
+int64_t sort_parts(int64_t n) { return n <= (int64_t)1 << 18 ? 32 : kSortParts; }
 
 int64_t sort_workspace(int64_t n, int E) {
   if (n <= kSortOne) return 0;
-  return (kSortParts * (int64_t)E * 4 + 255) / 256 * 256;
+  return (sort_parts(n) * E * 4 + 255) / 256 * 256;
 }
 
 hipError_t launch_sort_tokens(const int32_t* ids, int64_t n, int E, int32_t* offsets, int32_t* order, int32_t* pos,
@@ -334,7 +337,7 @@ hipError_t launch_sort_tokens(const int32_t* ids, int64_t n, int E, int32_t* off
     hipLaunchKernelGGL(k_sort_place, dim3(1), dim3(kSortThreads), lds, s, ids, n, E, bits, n, nullptr, offsets, order, pos);
     return hipGetLastError();
   }
-  const int64_t part = ((n + kSortParts - 1) / kSortParts + 63) / 64 * 64;
+  const int64_t want = sort_parts(n), part = ((n + want - 1) / want + 63) / 64 * 64;
   const int parts = (int)((n + part - 1) / part);
   hipLaunchKernelGGL(k_sort_count, dim3(parts), dim3(kSortThreads), lds, s, ids, n, E, part, hist);
   hipLaunchKernelGGL(k_sort_place, dim3(parts), dim3(kSortThreads), lds, s, ids, n, E, bits, part, hist, offsets, order, pos);
