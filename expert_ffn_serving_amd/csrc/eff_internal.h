@@ -357,6 +357,7 @@ struct MmArgs {
   int xk, wk;              // whether x and w are contiguous along k (sxk, swk = 1) or along their own index (sxm, swn = 1)
   int x_padded, w_padded;  // every row in memory is zero up to a multiple of 8 values
   // set by launch_matmul
+  int simple;   // nothing but the activation of SwiGLU and the residual, in whole vectors
   int plain;    // nothing but the sums is stored, in whole vectors
   int stream;   // an output larger than the caches, stored past them
   int vec;      // the epilogue's rows are whole 16-byte vectors

@@ -610,8 +610,18 @@ k_mm_tile(MmArgs a) {
   float* s_c = reinterpret_cast<float*>(s_tile);
   const int64_t nb = (int64_t)g * (GLU ? 2 * a.N : a.N);
   const int64_t n = n0 + (tid % VR) * 8;
+  constexpr int NR = RP / ROUND;
+  auto row_of = [&](int p, int rr) { return m0 + (rr / (16 * IP)) * TM + p * (16 * IP) + rr % (16 * IP); };
 #pragma unroll
   for (int p = 0; p < MT / IP; ++p) {
+    V8 res[NR];
+    if (a.simple && a.residual) {  // on its way while the sums go through LDS
+#pragma unroll
+      for (int h = 0; h < NR; ++h) {
+        const int64_t m = row_of(p, tid / VR + h * ROUND);
+        if (m < m1 && n < a.N) res[h] = *reinterpret_cast<const V8*>(reinterpret_cast<const T*>(a.residual) + m * a.ldr + n);
+      }
+    }
     meet();
 #pragma unroll
     for (int i = 0; i < IP; ++i)
@@ -621,9 +631,30 @@ k_mm_tile(MmArgs a) {
         *reinterpret_cast<f32x4_t*>(s_c + ((wm * IP + i) * 16 + r) * LDC + col) = acc[p * IP + i][j];
       }
     meet();
+    if (a.simple) {  // whole vectors, no bias, nothing saved, no other activation: every round's accesses at once
+#pragma unroll
+      for (int h = 0; h < NR; ++h) {
+        const int64_t m = row_of(p, tid / VR + h * ROUND);
+        const float* c = s_c + (tid / VR + h * ROUND) * LDC + (tid % VR) * 8;
+        V8 o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float z = c[e];
+          if (GLU) z = act_silu(z) * c[BNH + e];
+          if (a.residual) z += (float)res[h][e];
+          o[e] = (T)z;
+        }
+        if (m < m1 && n < a.N) {
+          V8* d = reinterpret_cast<V8*>(reinterpret_cast<T*>(a.y) + yo + m * a.ldy + n);
+          if (a.stream) __builtin_nontemporal_store(o, d);
+          else *d = o;
+        }
+      }
+      continue;
+    }
 #pragma unroll 1
     for (int rr = tid / VR; rr < RP; rr += ROUND) {
-      const int64_t m = m0 + (rr / (16 * IP)) * TM + p * (16 * IP) + rr % (16 * IP);
+      const int64_t m = row_of(p, rr);
       if (m >= m1) continue;
       const float* c = s_c + rr * LDC + (tid % VR) * 8;
       float z[8], u[8];
@@ -1122,7 +1153,7 @@ hipError_t launch_typed(MmArgs a, Plan p, char* ws, hipStream_t s) {
   }
   if (p.splits > 1) {
     a.part = reinterpret_cast<float*>(ws + p.pack_x + p.pack_w);
-    a.ldpart = (glu ? 2 : 1) * up(a.N, 8), a.plain = 0;
+    a.ldpart = (glu ? 2 : 1) * up(a.N, 8), a.plain = a.simple = 0;
     a.split_steps = (int)ceil_div(ceil_div(a.K, 64), p.splits);
   }
   if (a.xk && a.wk) return glu ? launch_kind<T, true, true, true>(a, p, s) : launch_kind<T, true, true, false>(a, p, s);
@@ -1143,6 +1174,7 @@ hipError_t launch_matmul(const MmArgs& in, void* workspace, hipStream_t s) {
   // experts, 1 GiB of dw: 794 -> 760 us).
   a.stream = a.M * a.N * (a.mode == MM_K_GROUPS ? a.groups : 1) * (a.y_f32 ? 4 : 2) > (int64_t)256 << 20;
   a.plain = a.vec && !a.stream && !a.bias && !a.residual && !a.pre && !a.y_f32 && a.act == EFF_ACT_NONE;
+  a.simple = a.vec && !a.bias && !a.pre && !a.y_f32 && (a.act == EFF_ACT_NONE || a.act == EFF_ACT_SWIGLU);
   const Plan p = plan_matmul(a);
   char* ws = static_cast<char*>(workspace);
   return a.dtype == EFF_DT_BF16 ? launch_typed<bf16_t>(a, p, ws, s) : launch_typed<f16_t>(a, p, ws, s);
