@@ -1,4 +1,4 @@
-"""64-bit definitions of the operators without an engine, on the CPU, with the error each output may have.
+"""64-bit definitions of the operators without an engine, on the device of their inputs, with the error each output may have.
 
 Bounds.  A product of two 16-bit values is exact in fp32.  An fp32 sum of n terms, in any order and with one
 rounding (or truncation) of at most 2^-23 per step, is off by at most (n + 8) 2^-23 times the sum of their
@@ -72,7 +72,7 @@ def matmul64(x, w, bias, act, residual, offsets, n):
     m, k = x.shape
     nw = w.shape[-2]
     x, w = x.double(), w.double()
-    z, ze = torch.zeros(m, nw, dtype=torch.float64), torch.zeros(m, nw, dtype=torch.float64)
+    z, ze = (torch.zeros(m, nw, dtype=torch.float64, device=x.device) for _ in range(2))
     for e, rows in groups_of(offsets, m):
         we = w if e is None else w[e]
         z[rows] = x[rows] @ we.t()
@@ -98,7 +98,7 @@ def matmul64(x, w, bias, act, residual, offsets, n):
 def assert_within(got, ref, err, what):
     """got (any type) against ref with err, plus the rounding of got's own type."""
     t = got.dtype
-    g = got.detach().cpu().double()
+    g, ref, err = got.detach().cpu().double(), ref.cpu(), err.cpu()
     assert g.shape == ref.shape, what
     lim = (err + half_ulp(t) * (ref.abs() + err) + tiny(t)) if t != torch.float32 else err + STEP * ref.abs() + 1e-38
     off = (g - ref).abs()

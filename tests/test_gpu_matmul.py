@@ -32,6 +32,11 @@ def offsets_of(counts, before=0):
     return torch.tensor([before] + [before + sum(counts[:i + 1]) for i in range(len(counts))], dtype=torch.int32)
 
 
+def to(t, work):
+    """Large references are computed on the GPU, in 64 bits all the same."""
+    return t if t is None or work < 10 ** 8 else t.cuda()
+
+
 def run_forward(eff, m, n, k, dtype=BF, out=None, act=R.NONE, bias=False, residual=False, pre=False, counts=None, pad=0, seed=0,
                 before=0):
     g = torch.Generator().manual_seed(seed * 1000003 + m * 7919 + n * 31 + k)
@@ -52,7 +57,7 @@ def run_forward(eff, m, n, k, dtype=BF, out=None, act=R.NONE, bias=False, residu
         eff.grouped_matmul(strided(x, pad), strided(w, pad), off.cuda(), y, **args)
     torch.cuda.synchronize()
     x = torch.where(inside[:, None], x.float(), 0.0).to(dtype)
-    ry, ye, rz, ze = R.matmul64(x, w, b, act, r, off, n)
+    ry, ye, rz, ze = (t.cpu() for t in R.matmul64(*(to(t, m * nw * k) for t in (x, w, b)), act, to(r, m * nw * k), off, n))
     what = "m%d n%d k%d %s act%d" % (m, n, k, dtype, act)
     assert (y[~inside.cuda()] == 7).all(), "rows in no group changed"
     R.assert_within(y[inside.cuda()], ry[inside], ye[inside], what + " y")
@@ -232,6 +237,7 @@ def run_backward(eff, m, n, k, dtype=BF, act=R.NONE, counts=None, pad=0, dy32=Fa
     ref = {"dx": torch.zeros(m, k, dtype=torch.float64), "dw": torch.zeros(lead + (nw, k), dtype=torch.float64),
            "dbias": torch.zeros(lead + (nw,), dtype=torch.float64)}
     err = {o: torch.zeros_like(v) for o, v in ref.items()}
+    xd, wd, dz, dze, func = (to(t, m * nw * k) for t in (xd, wd, dz, dze, func))
     for e, rows in R.groups_of(off, m):
         z, ze, xr = dz[rows], dze[rows], xd[rows]
         we = wd if e is None else wd[e]
@@ -323,6 +329,53 @@ def test_gradients_against_differences(eff, act):
             num.view(-1)[j] = (loss(*[up if a is v else a for a in args]) - loss(*[dn if a is v else a for a in args])) / (2 * h)
         lim = (R.half_ulp(HF) + 2e-6) * (mags[i] + num.abs()) + 64 * h * h + R.tiny(HF)
         assert ((got.cpu().double() - num).abs() <= lim).all(), i
+
+
+# Sizes at which every tile (256 x 256, 128 x 256, 128 x 128, 64 x 128) is taken, whole and with its k split, in each
+# layout of the operands; none is a multiple of its tile.
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("shape", [(2051, 4104, 1032), (2051, 2056, 4104), (2051, 1032, 4104), (1030, 1032, 4104), (2051, 2056, 136),
+                                   (2051, 4104, 136)])
+def test_every_tile(eff, shape, dtype):
+    m, n, k = shape
+    run_forward(eff, m, n, k, dtype=dtype, residual=True)
+    run_forward(eff, m, n // 2, k, dtype=dtype, act=R.SWIGLU, bias=True, pre=True)
+
+
+@pytest.mark.parametrize("act", [R.NONE, R.SWIGLU])
+@pytest.mark.parametrize("shape", [(1030, 2056, 4104), (4101, 2056, 2056), (3077, 4104, 136), (1030, 4872, 4104), (2051, 1032, 4104),
+                                   (4900, 1032, 4104), (4101, 3080, 136)])
+def test_every_tile_of_the_gradients(eff, shape, act):
+    m, n, k = shape
+    run_backward(eff, m, n if act == R.NONE else n // 2, k, act=act)
+
+
+@pytest.mark.parametrize("m,n,k,groups", [(4101, 2056, 1032, 2), (500, 2056, 136, 40), (2051, 2056, 136, 2), (4101, 1032, 2056, 2),
+                                          (20000, 520, 136, 2), (4101, 520, 2056, 2)])
+def test_every_tile_of_the_groups(eff, m, n, k, groups):
+    g = torch.Generator().manual_seed(m)
+    cut = sorted(torch.randint(0, m - 4, (groups - 1,), generator=g).tolist())
+    counts = [b - a for a, b in zip([0] + cut, cut + [m - 5])]
+    run_forward(eff, m, n, k, counts=counts, bias=True)
+    run_forward(eff, m, n // 2, k, counts=counts, act=R.SWIGLU, dtype=HF)
+    run_backward(eff, m, n, k, counts=counts)
+    run_backward(eff, m, n // 2, k, counts=counts, act=R.SWIGLU, want=("dx", "dw"))
+
+
+@pytest.mark.parametrize("shape", [(2050, 2051, 133), (40, 515, 2563), (1, 512, 2561), (20, 33, 1001)])
+def test_odd_sizes(eff, shape):
+    """Rows that are no whole vectors: the operands are packed first."""
+    run_forward(eff, *shape, act=R.SILU, bias=True, residual=True, pre=True)
+    run_backward(eff, *shape, act=R.GELU)
+    run_backward(eff, *shape)
+    m, n, k = shape
+    run_forward(eff, m * 3, n, k, counts=[m, 2 * m], act=R.SWIGLU)
+
+
+def test_outputs_larger_than_the_caches(eff):
+    """Stored past them: 256 MiB and more of y and of dw."""
+    run_forward(eff, 16400, 8200, 40, residual=True)
+    run_backward(eff, 300, 1040, 2072, counts=[30] * 8 + [0] * 60, want=("dw",))
 
 
 # ---- how it is used
