@@ -367,6 +367,8 @@ struct MmArgs {
 };
 // workspace that launch_matmul needs, from the sizes and strides alone
 int64_t matmul_workspace(const MmArgs& a);
+// whether its launches hold the problem (a grid's threads stay below 2^32)
+bool matmul_fits(const MmArgs& a);
 hipError_t launch_matmul(const MmArgs& a, void* workspace, hipStream_t s);
 
 // dz = dy * act'(pre) [M, N or 2N] rounded to dtype (dz null: not written), its rows zeroed up to lddz, and its column
@@ -385,6 +387,7 @@ struct MmGrad {
   int dtype, dy_f32, act, groups;
 };
 int64_t matmul_dz_tiles(int64_t M, int groups);
+bool matmul_dz_fits(int64_t M, int64_t N, int groups);
 hipError_t launch_matmul_dz(const MmGrad& a, hipStream_t s);
 
 int64_t sort_workspace(int64_t n, int E);

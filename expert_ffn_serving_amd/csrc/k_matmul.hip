@@ -949,18 +949,18 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 k_mm_dbias(MmGrad a) {
   __shared__ float s_sum[4][64];
-  __shared__ int s_before[4];
+  __shared__ int64_t s_before[4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.y;
   const int64_t nw = a.act == EFF_ACT_SWIGLU ? 2 * a.N : a.N, n = (int64_t)blockIdx.x * 64 + lane;
   int64_t lo = 0, hi = a.M, first = 0;
   if (a.offsets) {  // tiles of the groups before this one
-    int before = 0;
+    int64_t before = 0;
     for (int i = threadIdx.x; i < e; i += 256) {
       group_rows(a.offsets, i, a.M, &lo, &hi);
-      before += (int)((hi - lo + kDzRows - 1) / kDzRows);
+      before += (hi - lo + kDzRows - 1) / kDzRows;
     }
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) before += __shfl_xor(before, o);
+    for (int o = 32; o >= 1; o >>= 1) before += __shfl_xor((long long)before, o);
     if (lane == 0) s_before[wave] = before;
     __syncthreads();
     first = s_before[0] + s_before[1] + s_before[2] + s_before[3];
@@ -985,8 +985,8 @@ int64_t row_tiles(const MmArgs& a, int64_t BM) {
   return a.mode == MM_ROW_GROUPS ? group_tiles(a.M, a.groups, BM) : ceil_div(a.M, BM);
 }
 
-// workgroups of one launch: their threads stay below 2^32
-constexpr int64_t kMaxTiles = (int64_t)1 << 22;
+// whether one launch holds so many workgroups: its threads stay below 2^32
+bool fits(int64_t workgroups, int threads) { return workgroups * threads < (int64_t)1 << 32; }
 
 bool aligned16(std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> sizes, int bytes) {
   for (const void* p : ptrs)
@@ -1086,7 +1086,6 @@ Plan plan_matmul(const MmArgs& a) {
 template <typename T, class C, bool XK, bool WK, bool GLU>
 hipError_t launch_tile_c(const MmArgs& a, int splits, hipStream_t s) {
   const int64_t tiles = ceil_div(a.N, GLU ? C::BN / 2 : C::BN) * row_tiles(a, C::BM);
-  if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
   constexpr int lds = C::S * (C::BM + C::BN) * C::BK * 2;
   auto* fn = &k_mm_tile<T, C, XK, WK, GLU>;
   static std::atomic<uint64_t> done{0};
@@ -1101,7 +1100,6 @@ hipError_t launch_tile_c(const MmArgs& a, int splits, hipStream_t s) {
 template <typename T, int MT, bool GLU>
 hipError_t launch_few(const MmArgs& a, hipStream_t s) {
   const int64_t slices = ceil_div(a.N, GLU ? 8 : 16), jobs = slices * row_tiles(a, 16 * MT);
-  if (jobs > kMaxTiles) return hipErrorInvalidConfiguration;
   // waves per workgroup: about 16 per CU over the launch, each with at least two chunks of k
   int waves = 16;
   while (waves > 1 && (jobs * waves > 8192 || waves * 128 > a.K + 127)) waves /= 2;
@@ -1127,7 +1125,6 @@ hipError_t launch_typed(MmArgs a, Plan p, char* ws, hipStream_t s) {
   if ((!p.pack_x && (uintptr_t)a.x % 16) || (!p.pack_w && (uintptr_t)a.w % 16)) p.kind = KIND_ANY;
   if (p.kind == KIND_ANY) {
     const int64_t tiles = ceil_div(a.N, glu ? kAnyBN / 2 : kAnyBN) * row_tiles(a, kAnyBM);
-    if (tiles > kMaxTiles) return hipErrorInvalidConfiguration;
     const dim3 g((unsigned)tiles, a.mode == MM_K_GROUPS ? (unsigned)a.groups : 1u);
     if (glu) hipLaunchKernelGGL((k_mm_any<T, true>), g, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((k_mm_any<T, false>), g, dim3(256), 0, s, a);
@@ -1148,7 +1145,6 @@ hipError_t launch_typed(MmArgs a, Plan p, char* ws, hipStream_t s) {
       a.swg = rows * *ld;
     }
     const int64_t blocks = jobs[0].blocks + jobs[1].blocks;
-    if (blocks > 2 * kMaxTiles) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((k_mm_pack<T>), dim3((unsigned)blocks), dim3(256), 0, s, jobs[0], jobs[1]);
   }
   if (p.splits > 1) {
@@ -1161,6 +1157,21 @@ hipError_t launch_typed(MmArgs a, Plan p, char* ws, hipStream_t s) {
 }
 
 }  // namespace
+
+bool matmul_fits(const MmArgs& a) {
+  if (a.M == 0) return true;
+  const Plan p = plan_matmul(a);
+  const int64_t n = w_rows(a);
+  // the general kernel too, which takes over where pointers are not aligned
+  bool ok = fits(ceil_div(n, kAnyBN) * row_tiles(a, kAnyBM), 256);
+  ok = ok && fits(ceil_div(p.pack_x, 4096) + ceil_div(p.pack_w, 4096) + 2, 256);
+  if (p.kind == KIND_FEW1 || p.kind == KIND_FEW2) ok = ok && fits(ceil_div(n, 16) * row_tiles(a, 16), 1024);
+  return ok;
+}
+
+bool matmul_dz_fits(int64_t M, int64_t N, int groups) {
+  return fits(ceil_div(N, 64) * matmul_dz_tiles(M, groups), 256) && fits(ceil_div(2 * N, 64), 256);
+}
 
 int64_t matmul_workspace(const MmArgs& a) {
   const Plan p = plan_matmul(a);
@@ -1191,7 +1202,6 @@ hipError_t launch_matmul_dz(const MmGrad& in, hipStream_t s) {
   const int64_t nw = a.act == EFF_ACT_SWIGLU ? 2 * a.N : a.N;
   const bool vec = aligned16({a.dy, a.act ? a.pre : nullptr, a.dz}, {a.N, a.ldy, a.act ? a.ldp : 0, a.lddz}, 2);
   const int64_t cols = ceil_div(a.N, vec ? 512 : 64);
-  if (cols * a.tiles > kMaxTiles || ceil_div(nw, 64) > kMaxTiles) return hipErrorInvalidConfiguration;
   auto go = [&](auto t, auto d) {
     typedef decltype(t) T;
     typedef decltype(d) D;

@@ -314,6 +314,7 @@ hipError_t with_type(int dtype, bool v, F f) {
   }
 }
 
+constexpr int64_t kGridX = 1 << 23;  // workgroups of 256 threads: a grid's threads stay below 2^32
 constexpr int64_t kGridY = 65535;  // tokens per launch of the two-dimensional grids
 
 }  // namespace
@@ -383,8 +384,10 @@ hipError_t launch_combine_tokens_grad(int dtype, const void* dout, int64_t ldd, 
   return with_type(dtype, v, [&](auto t, auto vec) {
     typedef decltype(t) E;
     constexpr int V = decltype(vec)::value;
-    hipLaunchKernelGGL((k_combine_grad<E, V>), dim3((unsigned)T), dim3(256), 0, s, (const E*)dout, ldd, (const E*)ys, ldys,
-                       rows, pos, w, K, H, (E*)dys, lddys, dw);
+    for (int64_t t0 = 0; t0 < T; t0 += kGridX)
+      hipLaunchKernelGGL((k_combine_grad<E, V>), dim3((unsigned)std::min(kGridX, T - t0)), dim3(256), 0, s,
+                         (const E*)dout + t0 * ldd, ldd, (const E*)ys, ldys, rows, pos + t0 * K, w + t0 * K, K, H, (E*)dys, lddys,
+                         dw ? dw + t0 * K : nullptr);
     return hipGetLastError();
   });
 }

@@ -26,11 +26,8 @@ int setup(const char* fn) {
   return EFF_OK;
 }
 
-// a launch that was refused before it reached the device is the caller's sizes
 int launched(const char* fn, hipError_t err) {
-  if (err == hipSuccess) return EFF_OK;
-  if (err == hipErrorInvalidConfiguration) return fail(EFF_EINVAL, std::string(fn) + ": too many output tiles for one launch");
-  return fail(EFF_EHIP, std::string(fn) + ": " + hipGetErrorString(err));
+  return err == hipSuccess ? EFF_OK : fail(EFF_EHIP, std::string(fn) + ": " + hipGetErrorString(err));
 }
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
@@ -129,6 +126,7 @@ int eff_matmul(const eff_matmul_desc* d, const void* x, const void* w, const voi
   if (d->m > 1 && (d->ld_y < d->n || (pre && d->ld_pre < nw))) return bad(fn, "rows of an output overlap");
   if (int rc = check_ws(fn, eff_matmul_workspace(d, 0), workspace, workspace_bytes)) return rc;
   MmArgs a = forward_args(d);
+  if (!matmul_fits(a)) return bad(fn, "too many output tiles for one launch");
   a.x = x, a.w = w, a.offsets = offsets, a.bias = bias, a.residual = residual, a.y = y, a.pre = pre;
   return launched(fn, launch_matmul(a, workspace, (hipStream_t)stream));
 }
@@ -149,6 +147,8 @@ int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x,
       (dw && d->groups > 1 && d->stride_dw < (nw - 1) * std::max(d->ld_dw, d->k) + d->k))
     return bad(fn, "rows of an output overlap");
   if (int rc = check_ws(fn, eff_matmul_workspace(d, 1), workspace, workspace_bytes)) return rc;
+  if (rows && ((dx && !matmul_fits(dx_args(d))) || (dw && !matmul_fits(dw_args(d))) || !matmul_dz_fits(d->m, d->n, d->groups)))
+    return bad(fn, "too many output tiles for one launch");
   hipStream_t s = (hipStream_t)stream;
   MmGrad g = {};
   g.dtype = d->dtype, g.dy_f32 = d->out_dtype == EFF_DT_F32, g.act = d->act;

@@ -49,6 +49,11 @@ def test_bad_forward_calls(eff):
     for kw in (dict(ld_x=-1), dict(ld_w=-16), dict(ld_residual=-1), dict(stride_w=-1), dict(ld_y=7)):
         assert forward(eff, desc(**kw)) == eff.EFF_EINVAL, kw
     assert forward(eff, desc(ld_pre=7), pre=A) == eff.EFF_EINVAL
+    big = desc(m=1 << 30, n=1 << 20, ld_y=1 << 20, ld_residual=1 << 20, ld_pre=1 << 20)
+    assert forward(eff, big) == eff.EFF_EINVAL                        # more tiles than a grid holds
+    big = desc(m=1 << 30, n=1 << 12, k=1 << 12, ld_x=1 << 12, ld_w=1 << 12, ld_y=1 << 12, ld_dx=1 << 12, ld_dw=1 << 12)
+    ws = eff.lib().eff_matmul_workspace(ctypes.addressof(big), 1)
+    assert backward(eff, big, ws=A, nws=ws) == eff.EFF_EINVAL
     assert forward(eff, desc(m=0), x=None, y=None) == eff.EFF_OK      # no rows: nothing to do
 
 
