@@ -305,16 +305,25 @@ k_mm_any(MmArgs a) {
 
 // ---- aligned operands: tiles through LDS ---------------------------------------------------------------
 //
-// Workgroup = BM rows x BN columns, WM x WN waves of (BM/WM) x (BN/WN), 64 k per step.  Both operands go to LDS by
+// Workgroup = BM rows x BN columns, WM x WN waves of (BM/WM) x (BN/WN), BK k per step.  Both operands go to LDS by
 // direct 16-byte copies (no registers), S steps deep; one barrier per step.  An operand is either k-contiguous
-// (LDS: rows of 64 k) or contiguous along its own index (LDS: 64 k rows of BM or BN values, read back transposed by
+// (LDS: rows of BK k) or contiguous along its own index (LDS: BK rows of BM or BN values, read back transposed by
 // ds_read_b64_tr_b16: lane l of a group of 16 gets value l%4 of the 8 bytes that lanes l/4, 4 + l/4, .. address).
 // A copy writes LDS in lane order, so bank conflicts are avoided by permuting which 16 bytes a lane fetches: chunk c
-// of a row sits at chunk c ^ f(row), f chosen so that the lanes that read together hit different banks.
+// of a row sits at chunk c ^ f(row), f chosen so that the lanes that read together hit different banks (counters: none).
+// k past the end is fetched from 16 zero bytes on both sides; rows and columns past the end repeat the last ones, and
+// their sums are dropped.
 //
 // The weights are the matrix core's first operand, so a lane holds 4 consecutive columns of one row per product;
 // with k-contiguous weights the LDS rows are dealt to the products so that a lane's columns of all of them are
-// consecutive: whole 16-byte stores (and residual loads) in the epilogue.
+// consecutive.
+//
+// Measured: 8192^3 811 us, 1355 TFLOP/s (the library's product 1612), 4096^3 109 us; the three layouts within 6 %.  The
+// matrix cores are busy 66 % of the time at 1.8 GHz (the library's 92 % at 1.5 GHz: both run into the power limit); the
+// rest is the step's barrier and the workgroups' starts and epilogues, 14 us of a 256 x 256 tile's 64 at 2048 k.  Steps
+// of 32 k of 256-row tiles fetch half lines, twice the L2 requests (8192^3 954 us and not 922 at that stage).  256 experts x 48 rows (4096 ->
+// 2 x 2048, SwiGLU) are bound by the 8.6 GB of weights: 1.67 ms, 5.2 TB/s of the 6.4 that a plain read reaches; 32-row,
+// 128-row and 256-column tiles, other depths and steps of 32 or 128 k took 1.69 to 2.6 ms.
 __device__ const uint4 g_zero16[1] = {{0u, 0u, 0u, 0u}};  // what a copy past the last k reads
 
 // this wave's LDS reads are done, then every wave's; nothing moves across
@@ -511,8 +520,9 @@ k_mm_tile(MmArgs a) {
     if (t < steps) issue(t);
   if constexpr (C::AHEAD) {
     // One wave's products hide its LDS reads: an x operand is read again for the next half step as soon as its products
-    // are issued, the w operands are read one half step ahead into a second set.  The barrier of a step stands inside the
-    // last half's products, when the reads before it have long returned.
+    // are issued, the w operands are read one half step ahead into a second set (both in a second set spill).  The barrier
+    // of a step stands inside the last half's products, when the reads before it have long returned.  8192^3: 1355
+    // TFLOP/s; each half's reads before its products 1137, two groups of waves taking turns at LDS and the matrix cores 1312.
     static_assert(KS == 2 && S == 2, "two halves, two buffers");
     V8 fw[2][NT], fx[MT];
     auto products = [&](int from, int i) {
@@ -685,7 +695,7 @@ k_mm_tile(MmArgs a) {
   }
 }
 
-// A split k's sums added in order of k, and the epilogue.  grid: ceil(M * vectors / 256); a thread takes 8 columns.
+// A split k's sums added in order of k, and the epilogue (333 x 515, 8 splits: 6 us, a launch and two trips to memory).  grid: ceil(M * vectors / 256); a thread takes 8 columns.
 template <typename T, bool GLU>
 __global__ void __launch_bounds__(256)
 k_mm_join(MmArgs a, int splits) {
@@ -748,7 +758,8 @@ k_mm_pack(PackJob a, PackJob b) {
 // bound by the stream of W, so every wave keeps U chunks of 64 k (2 KiB of W each) in flight in registers and nothing
 // waits for a barrier before the end, where the waves' sums meet in LDS in wave order.  The lane of W row r and k group
 // q takes 32 consecutive bytes of a chunk: k = 16 q .. 16 q + 15 (the order of k inside a product is free as long as
-// both operands share it), so a chunk is one 128-byte line of every row.
+// both operands share it), so a chunk is one 128-byte line of every row.  16 rows, 4096 -> 2 x 2048 SwiGLU: 10.2 us, 3.3
+// TB/s of W (33 MB: a launch, one trip to memory and the join; two chunks in flight 12.3 us, 64 x 128 tiles 32 us).
 template <int MT>
 constexpr int few_unroll() { return MT == 1 ? 4 : 2; }
 
@@ -835,7 +846,7 @@ k_mm_few(MmArgs a, int slices) {
 // One pass over dy and pre: a workgroup takes 32 rows of one group and 64 VEC columns, each of its 4 waves every
 // fourth row.  It writes dz rounded to T (the operand that dx and dw multiply; columns up to lddz are zeroed, so that
 // dz's rows are whole 16-byte vectors) and the columns' fp32 sums over its rows, which a second kernel adds up in row
-// order.  Bound by HBM: every value is read once and written once.
+// order.  Bound by HBM, every value read and written once: 4096 x 2 x 2048 SwiGLU 21 us, 4.0 TB/s.
 constexpr int kDzRows = 32;
 
 template <typename T, int VEC>
@@ -1054,6 +1065,10 @@ Plan plan_matmul(const MmArgs& a) {
     if (rows <= 16 && !fill) return p.kind = KIND_FEW1, p;
     if (rows <= 32 && !fill) return p.kind = KIND_FEW2, p;
   }
+  // 256 x 256 tiles have the most products per byte (4096^3 118 us, 128 x 256 140); 128 x 256 tiles, two workgroups on
+  // a CU so that one's epilogue runs under the other's products, win where sums are short (8192 x 4096 x 512 46 us, 256 x
+  // 256 53; gradients of 256 experts 790 us, 1000); 128 x 128 and 64 x 128 fill the chip when there are few tiles (2048^3
+  // 25 us with 64 x 128, 30 and 55 with the larger ones) and waste less on experts with few rows.
   // Tiles and splits of k by an estimate of the time: rounds of workgroups over 256 CUs (`occ` on each; with one on each
   // a step is faster), 64-k steps, a workgroup's start and epilogue, and a split's sums written, read and joined.  The
   // constants (us) fit 4096^3, 8192 x 4096 x {512, 2048}, 2048^3 and 333 x 512 x 2560 to 15 %.

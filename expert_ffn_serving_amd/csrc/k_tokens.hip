@@ -105,7 +105,9 @@ __device__ inline void place_pairs(const int32_t* ids, int64_t b0, int64_t b1, i
   }
 }
 
-// One workgroup per part of the pairs.  hist null: the whole sort in one workgroup.  Otherwise hist
+// Counting and placing by waves over contiguous parts keeps the order of equal ids without a sort.  Bound by latency: 160
+// pairs over 512 experts 4.6 us in one workgroup; 49152 over 256 in 32 parts 4 + 10 us (in 64 parts, whose counts come in
+// four trips and not one, 4 + 19).  One workgroup per part of the pairs.  hist null: the whole sort in one workgroup.  Otherwise hist
 // [parts][E] holds every part's counts (k_sort_count), and each workgroup sums the columns it needs.
 __global__ void __launch_bounds__(kSortThreads)
 k_sort_place(const int32_t* __restrict__ ids, int64_t n, int E, int bits, int64_t part, const int32_t* __restrict__ hist,
@@ -200,7 +202,9 @@ __device__ inline void store_f32(T* p, const float* o) {
   *reinterpret_cast<typename Pack<T, VEC>::V*>(p) = v;
 }
 
-// grid: (ceil(H / (256 VEC)), T).  A token's row is read once and written to its K places.
+// grid: (ceil(H / (256 VEC)), T).  A token's row is read once and written to its K places (read once per place, most
+// reads would hit L2, but a token's workgroup needs its positions only once this way).  8192 tokens x 6 x 4096: 430 MB in
+// 84 us, 5.1 TB/s; a plain copy moves 5.0.  Stores past the caches changed nothing.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
 k_dispatch(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ pos, int K, int64_t H, T* __restrict__ xs,
@@ -216,7 +220,8 @@ k_dispatch(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ pos
 
 constexpr int kAhead = 4;
 
-// grid: (ceil(H / (256 VEC)), T).  out = residual + sum_k w * ys[pos], k ascending in fp32; w null: weights of 1.
+// grid: (ceil(H / (256 VEC)), T).  out = residual + sum_k w * ys[pos], k ascending in fp32; w null: weights of 1.  8192
+// tokens x 6 x 4096 with the residual: 497 MB in 95 us, 5.2 TB/s (one pair's row at a time: the same).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
 k_combine_rows(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int32_t* __restrict__ pos,
@@ -260,7 +265,8 @@ k_combine_rows(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int32
 }
 
 // grid: T workgroups of 4 waves; wave w takes the pairs k = w, w+4, ...: dys = w * dout and, with dw, the
-// dot product of dout and ys (64 lane sums in column order, folded pairwise).
+// dot product of dout and ys (64 lane sums in column order, folded pairwise).  dout is read from HBM once, by the other
+// pairs from L2.  4096 tokens x 8 x 2048: 286 MB in 54 us on the same rows again, 66 on others, 4.3 TB/s.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
 k_combine_grad(const T* __restrict__ dout, int64_t ldd, const T* __restrict__ ys, int64_t ldys, int64_t rows,
