@@ -170,20 +170,29 @@ __device__ inline void put_cl(void* p, int64_t i, int left, bool vec, const floa
   }
 }
 
+// what the epilogue reads for CL columns (n < N): bias (SwiGLU: of both halves) and residual; zeros where there is none
+template <int CL>
+struct Extra {
+  float bias[CL], up[CL], residual[CL];
+};
 template <typename T, int CL, bool GLU>
-__device__ inline void mm_finish(const MmArgs& a, int64_t m, int64_t n, int64_t nb, int64_t yo, float* z, float* u) {
-  if (n >= a.N) return;
+__device__ inline void mm_fetch(const MmArgs& a, int64_t m, int64_t n, int64_t nb, Extra<CL>* x) {
+  const int left = (int)min((int64_t)CL, a.N - n);
+  if (a.bias) {
+    get_cl<T, CL>(a.bias, nb + n, left, a.vec, x->bias);
+    if (GLU) get_cl<T, CL>(a.bias, nb + a.N + n, left, a.vec, x->up);
+  }
+  if (a.residual) get_cl<T, CL>(a.residual, m * a.ldr + n, left, a.vec, x->residual);
+}
+template <typename T, int CL, bool GLU>
+__device__ inline void mm_apply(const MmArgs& a, int64_t m, int64_t n, int64_t yo, float* z, float* u, const Extra<CL>& x) {
   const int left = (int)min((int64_t)CL, a.N - n);
   const bool vec = a.vec;
-  float t[CL];
   if (a.bias) {
-    get_cl<T, CL>(a.bias, nb + n, left, vec, t);
 #pragma unroll
-    for (int e = 0; e < CL; ++e) z[e] += t[e];
-    if (GLU) {
-      get_cl<T, CL>(a.bias, nb + a.N + n, left, vec, t);
-#pragma unroll
-      for (int e = 0; e < CL; ++e) u[e] += t[e];
+    for (int e = 0; e < CL; ++e) {
+      z[e] += x.bias[e];
+      if (GLU) u[e] += x.up[e];
     }
   }
   if (a.pre) {
@@ -193,13 +202,19 @@ __device__ inline void mm_finish(const MmArgs& a, int64_t m, int64_t n, int64_t 
 #pragma unroll
   for (int e = 0; e < CL; ++e) z[e] = GLU ? act_silu(z[e]) * u[e] : act_one(a.act, z[e]);
   if (a.residual) {
-    get_cl<T, CL>(a.residual, m * a.ldr + n, left, vec, t);
 #pragma unroll
-    for (int e = 0; e < CL; ++e) z[e] += t[e];
+    for (int e = 0; e < CL; ++e) z[e] += x.residual[e];
   }
   const int64_t o = yo + m * a.ldy + n;
   if (a.y_f32) put_cl<float, CL>(a.y, o, left, vec, z, a.stream);
   else put_cl<T, CL>(a.y, o, left, vec, z, a.stream);
+}
+template <typename T, int CL, bool GLU>
+__device__ inline void mm_finish(const MmArgs& a, int64_t m, int64_t n, int64_t nb, int64_t yo, float* z, float* u) {
+  if (n >= a.N) return;
+  Extra<CL> x;
+  mm_fetch<T, CL, GLU>(a, m, n, nb, &x);
+  mm_apply<T, CL, GLU>(a, m, n, yo, z, u, x);
 }
 
 // ---- any strides, any alignment ------------------------------------------------------------------------
@@ -813,6 +828,11 @@ k_mm_few(MmArgs a, int slices) {
   };
 #pragma unroll
   for (int s = 0; s < U; ++s) load(wave + s * waves, s);
+  // what the finishing wave's epilogue reads is on its way with the operands
+  const int64_t nb = (int64_t)g * (GLU ? 2 * a.N : a.N);
+  Extra<4> extra;
+  if (wave < MT && m0 + wave * 16 + r < m1 && n0 + 4 * q < a.N && (!GLU || q < 2))
+    mm_fetch<T, 4, GLU>(a, m0 + wave * 16 + r, n0 + 4 * q, nb, &extra);
   int c = wave;
   for (; c + U * waves < chunks; c += U * waves) {
 #pragma unroll
@@ -828,6 +848,7 @@ k_mm_few(MmArgs a, int slices) {
   __syncthreads();
   // one wave per 16 rows of x: lane's row m = r, W rows 4 q .. 4 q + 3 of the slice
   for (int i = wave; i < MT; i += waves) {
+    const int64_t m = m0 + i * 16 + r, n = n0 + 4 * q;
     f32x4_t sum = s_acc[i * 64 + lane];
     for (int v = 1; v < waves; ++v) sum += s_acc[(v * MT + i) * 64 + lane];
     float z[4], u[4];
@@ -836,8 +857,10 @@ k_mm_few(MmArgs a, int slices) {
       z[e] = sum[e];
       if (GLU) u[e] = __shfl_down(z[e], 32);
     }
-    const int64_t m = m0 + i * 16 + r;
-    if (m < m1 && (!GLU || q < 2)) mm_finish<T, 4, GLU>(a, m, n0 + 4 * q, (int64_t)g * (GLU ? 2 * a.N : a.N), 0, z, u);
+    if (m < m1 && n < a.N && (!GLU || q < 2)) {
+      if (i != wave) mm_fetch<T, 4, GLU>(a, m, n, nb, &extra);
+      mm_apply<T, 4, GLU>(a, m, n, 0, z, u, extra);
+    }
   }
 }
 

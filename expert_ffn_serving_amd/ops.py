@@ -35,11 +35,16 @@ def _bad(msg: str):
     raise EffError(EFF_EINVAL, msg)
 
 
-# The checks below run in front of calls of a few microseconds: one attribute access each, no torch objects made.
+# The checks below run in front of calls of a few microseconds: few attribute accesses, no torch objects made, and
+# something that is no tensor shows as the AttributeError that _no_tensor turns into an EffError.
+
+def _no_tensor(e: AttributeError):
+    raise EffError(EFF_EINVAL, "an argument is not a tensor (%s)" % e) from e
+
 
 def _matrix(name, t, dtype, rows, cols, dev, out=False):
     """Checks a row-major matrix; returns its address and the elements between rows."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
+    if t.dtype is not dtype or t.shape != (rows, cols):
         _explain(name, t, dtype, (rows, cols))
     if t.get_device() != dev:
         _bad("%s is on %s, the call on GPU %d" % (name, t.device, dev))
@@ -55,7 +60,7 @@ def _matrix(name, t, dtype, rows, cols, dev, out=False):
 
 def _stack(name, t, dtype, groups, rows, cols, dev, out=False):
     """A matrix per group: its address, the elements between rows and between groups."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != (groups, rows, cols):
+    if t.dtype is not dtype or t.shape != (groups, rows, cols):
         _explain(name, t, dtype, (groups, rows, cols))
     if t.get_device() != dev:
         _bad("%s is on %s, the call on GPU %d" % (name, t.device, dev))
@@ -72,7 +77,7 @@ def _stack(name, t, dtype, groups, rows, cols, dev, out=False):
 
 
 def _dense(name, t, dtype, shape, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         _explain(name, t, dtype, shape)
     if t.get_device() != dev:
         _bad("%s is on %s, the call on GPU %d" % (name, t.device, dev))
@@ -123,17 +128,17 @@ def _sizes(x, w, act, grouped):
     """(m, n, k, rows of one W, groups) of a product, from x [m,k] and w ([nw,k] or [E,nw,k])."""
     if x.dtype not in _HALF:
         _bad("x must be bfloat16 or float16, got %s" % x.dtype)
-    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != (3 if grouped else 2):
+    xs, ws = x.shape, w.shape
+    if len(xs) != 2 or len(ws) != (3 if grouped else 2):
         _bad("x must be [m,k] and w %s" % ("[E,n,k]" if grouped else "[n,k]"))
-    m, k = x.shape
-    nw, groups = w.size(-2), w.size(0) if grouped else 0
+    nw, groups = ws[-2], ws[0] if grouped else 0
+    if act == ACT_NONE or act in (1, 2, 3):
+        return xs[0], nw, xs[1], nw, groups
     if act != ACT_SWIGLU:
-        if act not in (0, 1, 2, 3):
-            _bad("unknown activation %r" % (act,))
-        return m, nw, k, nw, groups
+        _bad("unknown activation %r" % (act,))
     if nw % 2:
         _bad("w needs an even number of rows (gate, then up) with ACT_SWIGLU")
-    return m, nw // 2, k, nw, groups
+    return xs[0], nw // 2, xs[1], nw, groups
 
 
 def _weights(w, dt, groups, nw, k, dev, offsets):
@@ -145,30 +150,34 @@ def _weights(w, dt, groups, nw, k, dev, offsets):
 
 
 def _out_type(name, t, dt):
-    if not isinstance(t, torch.Tensor) or (t.dtype is not dt and t.dtype is not _F32):
+    got = t.dtype
+    if got is not dt and got is not _F32:
         _bad("%s must be a tensor of x's type or float32" % name)
-    return t.dtype
+    return got
 
 
 def _forward(x, w, offsets, y, bias, act, residual, pre, stream):
-    dev = _device("x", x)
-    dt = x.dtype
-    m, n, k, nw, groups = _sizes(x, w, act, offsets is not None)
-    yt = _out_type("y", y, dt)
-    px, ldx = _matrix("x", x, dt, m, k, dev)
-    pw, ldw, sw, po = _weights(w, dt, groups, nw, k, dev, offsets)
-    py, ldy = _matrix("y", y, yt, m, n, dev, True)
-    pb = pr = pp = None
-    ldr, ldp = 0, nw
-    if bias is not None:
-        pb = _dense("bias", bias, dt, (nw,) if offsets is None else (groups, nw), dev)
-    if residual is not None:
-        pr, ldr = _matrix("residual", residual, dt, m, n, dev)
-    if pre is not None:
-        pp, ldp = _matrix("pre", pre, dt, m, nw, dev, True)
-    d = _pack_desc(_HALF[dt], _DT[yt], act, groups, m, n, k, ldx, ldw, ldy, ldr, ldp, sw, 0, 0, 0)
-    L = lib()
-    _call(L.eff_matmul, dev, stream, (d, px, pw, pb, pr, po, py, pp), L.eff_matmul_workspace(d, 0))
+    try:
+        dev = _device("x", x)
+        dt = x.dtype
+        m, n, k, nw, groups = _sizes(x, w, act, offsets is not None)
+        yt = _out_type("y", y, dt)
+        px, ldx = _matrix("x", x, dt, m, k, dev)
+        pw, ldw, sw, po = _weights(w, dt, groups, nw, k, dev, offsets)
+        py, ldy = _matrix("y", y, yt, m, n, dev, True)
+        pb = pr = pp = None
+        ldr, ldp = 0, nw
+        if bias is not None:
+            pb = _dense("bias", bias, dt, (nw,) if offsets is None else (groups, nw), dev)
+        if residual is not None:
+            pr, ldr = _matrix("residual", residual, dt, m, n, dev)
+        if pre is not None:
+            pp, ldp = _matrix("pre", pre, dt, m, nw, dev, True)
+        d = _pack_desc(_HALF[dt], _DT[yt], act, groups, m, n, k, ldx, ldw, ldy, ldr, ldp, sw, 0, 0, 0)
+        L = lib()
+        _call(L.eff_matmul, dev, stream, (d, px, pw, pb, pr, po, py, pp), L.eff_matmul_workspace(d, 0))
+    except AttributeError as e:
+        _no_tensor(e)
 
 
 def matmul(x, w, y, bias=None, act=ACT_NONE, residual=None, pre=None, stream=None):
@@ -187,31 +196,34 @@ def grouped_matmul(x, w, offsets, y, bias=None, act=ACT_NONE, residual=None, pre
 
 
 def _backward(dy, x, w, offsets, dx, dw, dbias, act, pre, stream):
-    dev = _device("x", x)
-    dt = x.dtype
-    m, n, k, nw, groups = _sizes(x, w, act, offsets is not None)
-    dyt = _out_type("dy", dy, dt)
-    px, ldx = _matrix("x", x, dt, m, k, dev)
-    pw, ldw, sw, po = _weights(w, dt, groups, nw, k, dev, offsets)
-    pdy, lddy = _matrix("dy", dy, dyt, m, n, dev)
-    pp = pdx = pdw = pdb = None
-    ldp, lddx, lddw, sdw = nw, k, k, 0
-    if pre is not None:
-        pp, ldp = _matrix("pre", pre, dt, m, nw, dev)
-    elif act != ACT_NONE:
-        _bad("pre is needed with an activation")
-    if dx is not None:
-        pdx, lddx = _matrix("dx", dx, dt, m, k, dev, True)
-    if dw is not None:
-        if offsets is None:
-            pdw, lddw = _matrix("dw", dw, dt, nw, k, dev, True)
-        else:
-            pdw, lddw, sdw = _stack("dw", dw, dt, groups, nw, k, dev, True)
-    if dbias is not None:
-        pdb = _dense("dbias", dbias, dt, (nw,) if offsets is None else (groups, nw), dev)
-    d = _pack_desc(_HALF[dt], _DT[dyt], act, groups, m, n, k, ldx, ldw, lddy, 0, ldp, sw, lddx, lddw, sdw)
-    L = lib()
-    _call(L.eff_matmul_backward, dev, stream, (d, pdy, px, pw, pp, po, pdx, pdw, pdb), L.eff_matmul_workspace(d, 1))
+    try:
+        dev = _device("x", x)
+        dt = x.dtype
+        m, n, k, nw, groups = _sizes(x, w, act, offsets is not None)
+        dyt = _out_type("dy", dy, dt)
+        px, ldx = _matrix("x", x, dt, m, k, dev)
+        pw, ldw, sw, po = _weights(w, dt, groups, nw, k, dev, offsets)
+        pdy, lddy = _matrix("dy", dy, dyt, m, n, dev)
+        pp = pdx = pdw = pdb = None
+        ldp, lddx, lddw, sdw = nw, k, k, 0
+        if pre is not None:
+            pp, ldp = _matrix("pre", pre, dt, m, nw, dev)
+        elif act != ACT_NONE:
+            _bad("pre is needed with an activation")
+        if dx is not None:
+            pdx, lddx = _matrix("dx", dx, dt, m, k, dev, True)
+        if dw is not None:
+            if offsets is None:
+                pdw, lddw = _matrix("dw", dw, dt, nw, k, dev, True)
+            else:
+                pdw, lddw, sdw = _stack("dw", dw, dt, groups, nw, k, dev, True)
+        if dbias is not None:
+            pdb = _dense("dbias", dbias, dt, (nw,) if offsets is None else (groups, nw), dev)
+        d = _pack_desc(_HALF[dt], _DT[dyt], act, groups, m, n, k, ldx, ldw, lddy, 0, ldp, sw, lddx, lddw, sdw)
+        L = lib()
+        _call(L.eff_matmul_backward, dev, stream, (d, pdy, px, pw, pp, po, pdx, pdw, pdb), L.eff_matmul_workspace(d, 1))
+    except AttributeError as e:
+        _no_tensor(e)
 
 
 def matmul_backward(dy, x, w, dx=None, dw=None, dbias=None, act=ACT_NONE, pre=None, stream=None):
@@ -233,79 +245,96 @@ def sort_tokens(ids, offsets, order, pos, stream=None):
     """eff_sort_tokens: ids int32 (any shape, contiguous; [T,K] as route writes them) sorted stably by expert.  Writes
     offsets int32 [E+1] (its length says E), order int32 [pairs] (pair at a place, -1 behind the last) and pos int32,
     shaped like ids (place of a pair, -1 for an id outside [0,E))."""
-    dev = _device("ids", ids)
-    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
-        _bad("offsets must be a vector of E+1 values")
-    n, E, shape = ids.numel(), offsets.shape[0] - 1, ids.shape
-    pi = _dense("ids", ids, _I32, shape, dev)
-    po = _dense("offsets", offsets, _I32, (E + 1,), dev)
-    pr = _dense("order", order, _I32, (n,), dev)
-    pp = _dense("pos", pos, _I32, shape, dev)
-    L = lib()
-    _call(L.eff_sort_tokens, dev, stream, (pi, n, E, po, pr, pp), L.eff_sort_tokens_workspace(n, E))
+    try:
+        dev = _device("ids", ids)
+        if offsets.dim() != 1 or offsets.shape[0] < 2:
+            _bad("offsets must be a vector of E+1 values")
+        n, E, shape = ids.numel(), offsets.shape[0] - 1, ids.shape
+        pi = _dense("ids", ids, _I32, shape, dev)
+        po = _dense("offsets", offsets, _I32, (E + 1,), dev)
+        pr = _dense("order", order, _I32, (n,), dev)
+        pp = _dense("pos", pos, _I32, shape, dev)
+        L = lib()
+        _call(L.eff_sort_tokens, dev, stream, (pi, n, E, po, pr, pp), L.eff_sort_tokens_workspace(n, E))
+    except AttributeError as e:
+        _no_tensor(e)
 
 
 def _rows_of(name, t):
     """(rows, H) of a matrix of token or expert rows."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in _DT:
+    shape = t.shape
+    if len(shape) != 2 or t.dtype not in _DT:
         _bad("%s must be a matrix of bfloat16, float16 or float32" % name)
-    return t.shape
+    return shape
 
 
 def _pos(pos, T, dev):
-    if not isinstance(pos, torch.Tensor) or pos.dim() != 2 or pos.shape[0] != T:
+    shape = pos.shape
+    if len(shape) != 2 or shape[0] != T:
         _bad("pos must be [T,K] with T = %d" % T)
-    return _dense("pos", pos, _I32, pos.shape, dev), pos.shape[1]
+    return _dense("pos", pos, _I32, shape, dev), shape[1]
 
 
 def dispatch_tokens(x, pos, xs, stream=None):
     """eff_dispatch_tokens: xs[pos[t,k]] = x[t] for every routed pair; the other rows of xs stay as they were.
     x [T,H], xs [rows,H] (bfloat16, float16 or float32), pos int32 [T,K] from sort_tokens."""
-    dev = _device("x", x)
-    T, H = _rows_of("x", x)
-    R = _rows_of("xs", xs)[0]
-    px, ldx = _matrix("x", x, x.dtype, T, H, dev)
-    ps, lds = _matrix("xs", xs, x.dtype, R, H, dev, True)
-    pp, K = _pos(pos, T, dev)
-    _call(lib().eff_dispatch_tokens, dev, stream, (_DT[x.dtype], px, ldx, pp, T, K, H, ps, lds, R))
+    try:
+        dev = _device("x", x)
+        T, H = _rows_of("x", x)
+        R = _rows_of("xs", xs)[0]
+        px, ldx = _matrix("x", x, x.dtype, T, H, dev)
+        ps, lds = _matrix("xs", xs, x.dtype, R, H, dev, True)
+        pp, K = _pos(pos, T, dev)
+        _call(lib().eff_dispatch_tokens, dev, stream, (_DT[x.dtype], px, ldx, pp, T, K, H, ps, lds, R))
+    except AttributeError as e:
+        _no_tensor(e)
 
 
 def dispatch_tokens_backward(dxs, pos, dx, stream=None):
     """eff_dispatch_tokens_backward: dx[t] = sum over k of dxs[pos[t,k]] over the routed pairs."""
-    dev = _device("dxs", dxs)
-    R, H = _rows_of("dxs", dxs)
-    T = _rows_of("dx", dx)[0]
-    ps, lds = _matrix("dxs", dxs, dxs.dtype, R, H, dev)
-    px, ldx = _matrix("dx", dx, dxs.dtype, T, H, dev, True)
-    pp, K = _pos(pos, T, dev)
-    _call(lib().eff_dispatch_tokens_backward, dev, stream, (_DT[dxs.dtype], ps, lds, R, pp, T, K, H, px, ldx))
+    try:
+        dev = _device("dxs", dxs)
+        R, H = _rows_of("dxs", dxs)
+        T = _rows_of("dx", dx)[0]
+        ps, lds = _matrix("dxs", dxs, dxs.dtype, R, H, dev)
+        px, ldx = _matrix("dx", dx, dxs.dtype, T, H, dev, True)
+        pp, K = _pos(pos, T, dev)
+        _call(lib().eff_dispatch_tokens_backward, dev, stream, (_DT[dxs.dtype], ps, lds, R, pp, T, K, H, px, ldx))
+    except AttributeError as e:
+        _no_tensor(e)
 
 
 def combine_tokens(ys, pos, w, out, residual=None, stream=None):
     """eff_combine_tokens: out[t] = residual[t] + sum over k of w[t,k] * ys[pos[t,k]] over the routed pairs.
     ys [rows,H], out and residual [T,H] of one type, w float32 [T,K].  out may be residual."""
-    dev = _device("ys", ys)
-    R, H = _rows_of("ys", ys)
-    T = _rows_of("out", out)[0]
-    py, ldy = _matrix("ys", ys, ys.dtype, R, H, dev)
-    po, ldo = _matrix("out", out, ys.dtype, T, H, dev, True)
-    pr, ldr = _matrix("residual", residual, ys.dtype, T, H, dev) if residual is not None else (None, 0)
-    pp, K = _pos(pos, T, dev)
-    pw = _dense("w", w, _F32, (T, K), dev)
-    _call(lib().eff_combine_tokens, dev, stream, (_DT[ys.dtype], py, ldy, R, pp, pw, T, K, H, pr, ldr, po, ldo))
+    try:
+        dev = _device("ys", ys)
+        R, H = _rows_of("ys", ys)
+        T = _rows_of("out", out)[0]
+        py, ldy = _matrix("ys", ys, ys.dtype, R, H, dev)
+        po, ldo = _matrix("out", out, ys.dtype, T, H, dev, True)
+        pr, ldr = _matrix("residual", residual, ys.dtype, T, H, dev) if residual is not None else (None, 0)
+        pp, K = _pos(pos, T, dev)
+        pw = _dense("w", w, _F32, (T, K), dev)
+        _call(lib().eff_combine_tokens, dev, stream, (_DT[ys.dtype], py, ldy, R, pp, pw, T, K, H, pr, ldr, po, ldo))
+    except AttributeError as e:
+        _no_tensor(e)
 
 
 def combine_tokens_backward(dout, ys, pos, w, dys, dw=None, stream=None):
     """eff_combine_tokens_backward: dys[pos[t,k]] = w[t,k] * dout[t] (the other rows of dys stay as they were) and, if
     given, dw[t,k] = <dout[t], ys[pos[t,k]]> in float32 (0 for an unrouted pair).  The residual's gradient is dout."""
-    dev = _device("dout", dout)
-    T, H = _rows_of("dout", dout)
-    R = _rows_of("ys", ys)[0]
-    pd, ldd = _matrix("dout", dout, dout.dtype, T, H, dev)
-    py, ldy = _matrix("ys", ys, dout.dtype, R, H, dev)
-    ps, lds = _matrix("dys", dys, dout.dtype, R, H, dev, True)
-    pp, K = _pos(pos, T, dev)
-    pw = _dense("w", w, _F32, (T, K), dev)
-    pg = _dense("dw", dw, _F32, (T, K), dev) if dw is not None else None
-    _call(lib().eff_combine_tokens_backward, dev, stream,
-          (_DT[dout.dtype], pd, ldd, py, ldy, R, pp, pw, T, K, H, ps, lds, pg))
+    try:
+        dev = _device("dout", dout)
+        T, H = _rows_of("dout", dout)
+        R = _rows_of("ys", ys)[0]
+        pd, ldd = _matrix("dout", dout, dout.dtype, T, H, dev)
+        py, ldy = _matrix("ys", ys, dout.dtype, R, H, dev)
+        ps, lds = _matrix("dys", dys, dout.dtype, R, H, dev, True)
+        pp, K = _pos(pos, T, dev)
+        pw = _dense("w", w, _F32, (T, K), dev)
+        pg = _dense("dw", dw, _F32, (T, K), dev) if dw is not None else None
+        _call(lib().eff_combine_tokens_backward, dev, stream,
+              (_DT[dout.dtype], pd, ldd, py, ldy, R, pp, pw, T, K, H, ps, lds, pg))
+    except AttributeError as e:
+        _no_tensor(e)

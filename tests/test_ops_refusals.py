@@ -137,6 +137,9 @@ def test_bad_tensors(eff):
         lambda: eff.grouped_matmul(x, z(2, 8, 16), off.long(), y), lambda: eff.grouped_matmul(x, z(2, 8, 16), off.cpu(), y),
         lambda: eff.grouped_matmul_backward(y, x, z(2, 8, 16), off, dw=z(1, 8, 16).expand(2, 8, 16)),
         lambda: eff.grouped_matmul(x, z(0, 8, 16), z(1, d=torch.int32), y), lambda: eff.grouped_matmul(x, z(2, 8, 32)[..., ::2], off, y),
+        lambda: eff.matmul(x, None, y), lambda: eff.matmul(x, w, None), lambda: eff.matmul(x, w, y, bias=3), lambda: eff.matmul(x, w, y, residual="r"),
+        lambda: eff.matmul(x, w, y, pre=y.cpu().float().numpy()), lambda: eff.matmul_backward(None, x, w), lambda: eff.dispatch_tokens(x, None, x),
+        lambda: eff.sort_tokens(ids, None, ids.view(-1), pos), lambda: eff.combine_tokens(z(8, 16), pos, None, x),
         lambda: eff.sort_tokens(ids.long(), off, ids.view(-1), pos), lambda: eff.sort_tokens(ids, off, z(7, d=torch.int32), pos),
         lambda: eff.sort_tokens(ids, off, ids.view(-1), z(2, 4, d=torch.int32)), lambda: eff.sort_tokens(ids, off[:1], ids.view(-1), pos),
         lambda: eff.sort_tokens(ids, z(4098, d=torch.int32), z(8, d=torch.int32), pos), lambda: eff.sort_tokens(ids.t(), off, z(8, d=torch.int32), pos),
