@@ -333,7 +333,7 @@ k_mm_any(MmArgs a) {
 // with k-contiguous weights the LDS rows are dealt to the products so that a lane's columns of all of them are
 // consecutive.
 //
-// Measured: 8192^3 811 us, 1355 TFLOP/s (the library's product 1612), 4096^3 109 us; the three layouts within 6 %.  The
+// Measured: 8192^3 800 us, 1374 TFLOP/s (the library's product 1612), 4096^3 105 us; the three layouts within 6 %.  The
 // matrix cores are busy 66 % of the time at 1.8 GHz (the library's 92 % at 1.5 GHz: both run into the power limit); the
 // rest is the step's barrier and the workgroups' starts and epilogues, 14 us of a 256 x 256 tile's 64 at 2048 k.  Steps
 // of 32 k of 256-row tiles fetch half lines, twice the L2 requests (8192^3 954 us and not 922 at that stage).  256 experts x 48 rows (4096 ->
@@ -536,9 +536,10 @@ k_mm_tile(MmArgs a) {
   if constexpr (C::AHEAD) {
     // One wave's products hide its LDS reads: an x operand is read again for the next half step as soon as its products
     // are issued, the w operands are read one half step ahead into a second set (both in a second set spill).  The barrier
-    // of a step stands inside the last half's products, when the reads before it have long returned.  8192^3: 1355
-    // TFLOP/s; each half's reads before its products 1137, two groups of waves taking turns at LDS and the matrix cores 1312.
+    // of a step stands inside the last half's products, when the reads before it have long returned.  8192^3: 1374
+    // TFLOP/s (with 1 to 6 operands before the barrier, or raised priority: the same); each half's reads before its products 1137, two groups of waves taking turns at LDS and the matrix cores 1312.
     static_assert(KS == 2 && S == 2, "two halves, two buffers");
+    constexpr int LATE = 2;  // x operands whose products stand before the barrier
     V8 fw[2][NT], fx[MT];
     auto products = [&](int from, int i) {
 #pragma unroll
@@ -563,16 +564,16 @@ k_mm_tile(MmArgs a) {
           products(0, i);
           fx[i] = frag_x(b, i, 1);
         }
-        products(1, 0);
-        products(1, 1);
+#pragma unroll
+        for (int i = 0; i < LATE; ++i) products(1, i);
         arrived(true);
         meet();                      // step t + 1 is in LDS and step t in registers
         if (t + 2 < steps) issue(t + 2);
         read_w(0, next, 0);
-        fx[0] = frag_x(next, 0, 0);
-        fx[1] = frag_x(next, 1, 0);
 #pragma unroll
-        for (int i = 2; i < MT; ++i) {
+        for (int i = 0; i < LATE; ++i) fx[i] = frag_x(next, i, 0);
+#pragma unroll
+        for (int i = LATE; i < MT; ++i) {
           products(1, i);
           fx[i] = frag_x(next, i, 0);
         }

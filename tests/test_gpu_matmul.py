@@ -467,3 +467,40 @@ def test_captured_and_replayed(eff):
             torch.cuda.synchronize()
             for a, c in zip(got, want):
                 assert torch.equal(a, c), (m, i)
+
+
+def test_two_threads(eff):
+    """Calls from two threads at once, each on a stream of its own, give what one thread gives."""
+    import threading
+    g = torch.Generator().manual_seed(7)
+    x, w = rnd(g, 200, 264).cuda(), rnd(g, 528, 264, scale=0.06).cuda()
+
+    def once(stream):
+        y, p = torch.empty(200, 264, dtype=BF, device="cuda"), torch.empty(200, 528, dtype=BF, device="cuda")
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        eff.matmul(x, w, y, act=R.SWIGLU, pre=p, stream=stream)
+        eff.matmul_backward(y, x, w, dx=dx, dw=dw, act=R.SWIGLU, pre=p, stream=stream)
+        return y, p, dx, dw
+
+    want = once(None)
+    torch.cuda.synchronize()
+    got, failed = [], []
+
+    def work():
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                outs = [once(None) for _ in range(20)]
+            s.synchronize()
+            got.extend(outs)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and len(got) == 40
+    for outs in got:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
