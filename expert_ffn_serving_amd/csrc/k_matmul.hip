@@ -325,7 +325,7 @@ k_mm_any(MmArgs a) {
 // (LDS: rows of BK k) or contiguous along its own index (LDS: BK rows of BM or BN values, read back transposed by
 // ds_read_b64_tr_b16: lane l of a group of 16 gets value l%4 of the 8 bytes that lanes l/4, 4 + l/4, .. address).
 // A copy writes LDS in lane order, so bank conflicts are avoided by permuting which 16 bytes a lane fetches: chunk c
-// of a row sits at chunk c ^ f(row), f chosen so that the lanes that read together hit different banks (counters: none).
+// of a row sits at chunk c ^ f(row), f chosen so that the lanes that read together hit different banks (conflicts: 1 % of LDS cycles).
 // k past the end is fetched from 16 zero bytes on both sides; rows and columns past the end repeat the last ones, and
 // their sums are dropped.
 //
@@ -334,7 +334,7 @@ k_mm_any(MmArgs a) {
 // consecutive.
 //
 // Measured: 8192^3 800 us, 1374 TFLOP/s (the library's product 1612), 4096^3 105 us; the three layouts within 6 %.  The
-// matrix cores are busy 66 % of the time at 1.8 GHz (the library's 92 % at 1.5 GHz: both run into the power limit); the
+// matrix cores are busy 68 % of the time at 1.8 GHz (the library's 92 % at 1.5 GHz: both run into the power limit); the
 // rest is the step's barrier and the workgroups' starts and epilogues, 14 us of a 256 x 256 tile's 64 at 2048 k.  Steps
 // of 32 k of 256-row tiles fetch half lines, twice the L2 requests (8192^3 954 us and not 922 at that stage).  256 experts x 48 rows (4096 ->
 // 2 x 2048, SwiGLU) are bound by the 8.6 GB of weights: 1.67 ms, 5.2 TB/s of the 6.4 that a plain read reaches; 32-row,
