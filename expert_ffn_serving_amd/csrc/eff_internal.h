@@ -385,8 +385,9 @@ struct MmGrad {
   const int32_t* offsets;
   int64_t M, N, tiles;
   int dtype, dy_f32, act, groups;
+  int rows;  // set by launch_matmul_dz
 };
-int64_t matmul_dz_tiles(int64_t M, int groups);
+int64_t matmul_dz_tiles(int64_t M, int64_t N, int groups);
 bool matmul_dz_fits(int64_t M, int64_t N, int groups);
 hipError_t launch_matmul_dz(const MmGrad& a, hipStream_t s);
 

@@ -867,11 +867,12 @@ k_mm_few(MmArgs a, int slices) {
 
 // ---- dz and dbias --------------------------------------------------------------------------------------
 //
-// One pass over dy and pre: a workgroup takes 32 rows of one group and 64 VEC columns, each of its 4 waves every
+// One pass over dy and pre: a workgroup takes ROWS rows of one group and 64 VEC columns, each of its 4 waves every
 // fourth row.  It writes dz rounded to T (the operand that dx and dw multiply; columns up to lddz are zeroed, so that
 // dz's rows are whole 16-byte vectors) and the columns' fp32 sums over its rows, which a second kernel adds up in row
 // order.  Bound by HBM, every value read and written once: 4096 x 2 x 2048 SwiGLU 21 us, 4.0 TB/s.
-constexpr int kDzRows = 32;
+// Rows of one workgroup: 32, or 8 where 32 leave most of the chip idle (100 rows x 640, gelu: 21 -> 8 us; with 8 rows
+// everywhere the sums' second pass reads four times as much).
 
 template <typename T, int VEC>
 struct Piece {
@@ -907,7 +908,7 @@ __device__ inline void store_row(void* p, int64_t i, const float* v) {
   }
 }
 
-template <typename T, typename D, int VEC>
+template <typename T, typename D, int VEC, int ROWS>
 __global__ void __launch_bounds__(256)
 k_mm_dz(MmGrad a, int cols) {
   __shared__ float s_sum[2][4][64][VEC];
@@ -915,8 +916,8 @@ k_mm_dz(MmGrad a, int cols) {
   const int tile = blockIdx.x / cols;
   const int64_t n = ((int64_t)(blockIdx.x % cols) * 64 + lane) * VEC;
   int g;
-  int64_t m0 = (int64_t)tile * kDzRows, m1 = min(a.M, m0 + kDzRows);
-  if (a.offsets && !find_tile<kDzRows>(a.offsets, a.groups, a.M, tile, reinterpret_cast<int*>(s_sum), &g, &m0, &m1)) return;
+  int64_t m0 = (int64_t)tile * ROWS, m1 = min(a.M, m0 + ROWS);
+  if (a.offsets && !find_tile<ROWS>(a.offsets, a.groups, a.M, tile, reinterpret_cast<int*>(s_sum), &g, &m0, &m1)) return;
   const bool glu = a.act == EFF_ACT_SWIGLU;
   const int64_t nw = glu ? 2 * a.N : a.N;
   float sum[VEC], sup[VEC];
@@ -992,7 +993,7 @@ k_mm_dbias(MmGrad a) {
     int64_t before = 0;
     for (int i = threadIdx.x; i < e; i += 256) {
       group_rows(a.offsets, i, a.M, &lo, &hi);
-      before += (hi - lo + kDzRows - 1) / kDzRows;
+      before += (hi - lo + a.rows - 1) / a.rows;
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) before += __shfl_xor((long long)before, o);
@@ -1001,7 +1002,7 @@ k_mm_dbias(MmGrad a) {
     first = s_before[0] + s_before[1] + s_before[2] + s_before[3];
     group_rows(a.offsets, e, a.M, &lo, &hi);
   }
-  const int64_t count = (hi - lo + kDzRows - 1) / kDzRows, last = min(first + count, a.tiles);
+  const int64_t count = (hi - lo + a.rows - 1) / a.rows, last = min(first + count, a.tiles);
   float sum = 0.f;
   if (n < nw)
 #pragma unroll 8
@@ -1209,7 +1210,7 @@ bool matmul_fits(const MmArgs& a) {
 }
 
 bool matmul_dz_fits(int64_t M, int64_t N, int groups) {
-  return fits(ceil_div(N, 64) * matmul_dz_tiles(M, groups), 256) && fits(ceil_div(2 * N, 64), 256);
+  return fits(ceil_div(N, 64) * matmul_dz_tiles(M, N, groups), 256) && fits(ceil_div(2 * N, 64), 256);
 }
 
 int64_t matmul_workspace(const MmArgs& a) {
@@ -1230,23 +1231,30 @@ hipError_t launch_matmul(const MmArgs& in, void* workspace, hipStream_t s) {
   return a.dtype == EFF_DT_BF16 ? launch_typed<bf16_t>(a, p, ws, s) : launch_typed<f16_t>(a, p, ws, s);
 }
 
-// row tiles of the pass over dz, and of its partial sums
-int64_t matmul_dz_tiles(int64_t M, int groups) {
-  return groups ? group_tiles(M, groups, kDzRows) : ceil_div(M, kDzRows);
-}
+// rows of a workgroup in the pass over dz, and its row tiles (those of the partial sums)
+static int64_t dz_tiles(int64_t M, int groups, int64_t rows) { return groups ? group_tiles(M, groups, rows) : ceil_div(M, rows); }
+static int dz_rows(int64_t M, int64_t N, int groups) { return ceil_div(N, 512) * dz_tiles(M, groups, 32) < 256 ? 8 : 32; }
+int64_t matmul_dz_tiles(int64_t M, int64_t N, int groups) { return dz_tiles(M, groups, dz_rows(M, N, groups)); }
 
 hipError_t launch_matmul_dz(const MmGrad& in, hipStream_t s) {
   MmGrad a = in;
-  a.tiles = matmul_dz_tiles(a.M, a.offsets ? a.groups : 0);
+  const int groups = a.offsets ? a.groups : 0;
+  a.rows = dz_rows(a.M, a.N, groups);
+  a.tiles = matmul_dz_tiles(a.M, a.N, groups);
   const int64_t nw = a.act == EFF_ACT_SWIGLU ? 2 * a.N : a.N;
   const bool vec = aligned16({a.dy, a.act ? a.pre : nullptr, a.dz}, {a.N, a.ldy, a.act ? a.ldp : 0, a.lddz}, 2);
   const int64_t cols = ceil_div(a.N, vec ? 512 : 64);
   auto go = [&](auto t, auto d) {
     typedef decltype(t) T;
     typedef decltype(d) D;
-    if (a.M > 0) {
-      if (vec) hipLaunchKernelGGL((k_mm_dz<T, D, 8>), dim3((unsigned)(cols * a.tiles)), dim3(256), 0, s, a, (int)cols);
-      else hipLaunchKernelGGL((k_mm_dz<T, D, 1>), dim3((unsigned)(cols * a.tiles)), dim3(256), 0, s, a, (int)cols);
+    const dim3 grid((unsigned)(cols * a.tiles));
+    if (a.M == 0) {
+    } else if (a.rows == 8) {
+      if (vec) hipLaunchKernelGGL((k_mm_dz<T, D, 8, 8>), grid, dim3(256), 0, s, a, (int)cols);
+      else hipLaunchKernelGGL((k_mm_dz<T, D, 1, 8>), grid, dim3(256), 0, s, a, (int)cols);
+    } else {
+      if (vec) hipLaunchKernelGGL((k_mm_dz<T, D, 8, 32>), grid, dim3(256), 0, s, a, (int)cols);
+      else hipLaunchKernelGGL((k_mm_dz<T, D, 1, 32>), grid, dim3(256), 0, s, a, (int)cols);
     }
     if (a.dbias)
       hipLaunchKernelGGL((k_mm_dbias<T>), dim3((unsigned)ceil_div(nw, 64), (unsigned)(a.offsets ? a.groups : 1)), dim3(256), 0, s, a);

@@ -65,7 +65,7 @@ bool needs_dz(const eff_matmul_desc* d) {
   return d->act != EFF_ACT_NONE || d->out_dtype != d->dtype || d->n % 8 || d->ld_y % 8;
 }
 int64_t dz_bytes(const eff_matmul_desc* d) { return needs_dz(d) ? align256(d->m * dz_ld(d) * 2) : 0; }
-int64_t part_bytes(const eff_matmul_desc* d) { return align256(matmul_dz_tiles(d->m, d->groups) * w_rows(d) * 4); }
+int64_t part_bytes(const eff_matmul_desc* d) { return align256(matmul_dz_tiles(d->m, d->n, d->groups) * w_rows(d) * 4); }
 // dx[m,k] = sum over W's rows n of dz[m,n] w[n,k]
 MmArgs dx_args(const eff_matmul_desc* d) {
   MmArgs a = {};
