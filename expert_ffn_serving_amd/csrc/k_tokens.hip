@@ -202,42 +202,61 @@ __device__ inline void store_f32(T* p, const float* o) {
   *reinterpret_cast<typename Pack<T, VEC>::V*>(p) = v;
 }
 
-// grid: (ceil(H / (256 VEC)), T).  A token's row is read once and written to its K places (read once per place, most
+// vectors of one thread, 256 apart: rows that are no whole vectors move value by value, four in flight
+template <int VEC>
+constexpr int columns() { return VEC == 1 ? 4 : 1; }
+
+// grid: (ceil(H / (256 U VEC)), T).  A token's row is read once and written to its K places (read once per place, most
 // reads would hit L2, but a token's workgroup needs its positions only once this way).  8192 tokens x 6 x 4096: 430 MB in
 // 84 us, 5.1 TB/s; a plain copy moves 5.0.  Stores past the caches changed nothing.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
 k_dispatch(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ pos, int K, int64_t H, T* __restrict__ xs,
            int64_t ldxs, int64_t rows) {
-  const int64_t t = blockIdx.y, h = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
-  if (h >= H) return;
-  const typename Pack<T, VEC>::V v = *reinterpret_cast<const typename Pack<T, VEC>::V*>(x + t * ldx + h);
+  constexpr int U = columns<VEC>();
+  typedef typename Pack<T, VEC>::V V;
+  const int64_t t = blockIdx.y, h0 = ((int64_t)blockIdx.x * U * 256 + threadIdx.x) * VEC;
+  if (h0 >= H) return;
+  V v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const V*>(x + t * ldx + min(h0 + u * 256 * VEC, H - VEC));
   for (int k = 0; k < K; ++k) {
     const int64_t p = pos[t * K + k];
-    if (p >= 0 && p < rows) *reinterpret_cast<typename Pack<T, VEC>::V*>(xs + p * ldxs + h) = v;
+    if (p < 0 || p >= rows) continue;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (h0 + u * 256 * VEC < H) *reinterpret_cast<V*>(xs + p * ldxs + h0 + u * 256 * VEC) = v[u];
   }
 }
 
 constexpr int kAhead = 4;
 
-// grid: (ceil(H / (256 VEC)), T).  out = residual + sum_k w * ys[pos], k ascending in fp32; w null: weights of 1.  8192
+// grid: (ceil(H / (256 U VEC)), T).  out = residual + sum_k w * ys[pos], k ascending in fp32; w null: weights of 1.  8192
 // tokens x 6 x 4096 with the residual: 497 MB in 95 us, 5.2 TB/s (one pair's row at a time: the same).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256)
 k_combine_rows(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int32_t* __restrict__ pos,
                const float* __restrict__ w, int K, int64_t H, const T* residual, int64_t ldr, T* out, int64_t ldo) {
-  const int64_t t = blockIdx.y, h = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
-  if (h >= H) return;
-  float acc[VEC];
-  if (residual) {
-    load_f32<T, VEC>(residual + t * ldr + h, acc);
-  } else {
+  constexpr int U = columns<VEC>();
+  typedef typename Pack<T, VEC>::V V;
+  const int64_t t = blockIdx.y, h0 = ((int64_t)blockIdx.x * U * 256 + threadIdx.x) * VEC;
+  if (h0 >= H) return;
+  int64_t h[U];   // past the end the row's last values, which are not stored
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+  for (int u = 0; u < U; ++u) h[u] = min(h0 + u * 256 * VEC, H - VEC);
+  float acc[U][VEC];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (residual) {
+      load_f32<T, VEC>(residual + t * ldr + h[u], acc[u]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[u][i] = 0.f;
+    }
   }
   // kAhead pairs' rows are loaded before the first is added; a pair without a row loads nothing
   for (int k0 = 0; k0 < K; k0 += kAhead) {
-    typename Pack<T, VEC>::V v[kAhead];
+    V v[kAhead][U];
     float wk[kAhead];
     bool ok[kAhead];
 #pragma unroll
@@ -247,21 +266,27 @@ k_combine_rows(const T* __restrict__ ys, int64_t ldys, int64_t rows, const int32
       ok[i] = k0 + i < K && p >= 0 && p < rows;
       if (ok[i]) {
         wk[i] = w ? w[at] : 1.f;
-        v[i] = *reinterpret_cast<const typename Pack<T, VEC>::V*>(ys + p * ldys + h);
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[i][u] = *reinterpret_cast<const V*>(ys + p * ldys + h[u]);
       }
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (!ok[i]) continue;
-      if constexpr (VEC == 1) {
-        acc[0] = fmaf(wk[i], (float)v[i], acc[0]);
-      } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] = fmaf(wk[i], (float)v[i][e], acc[e]);
+      for (int u = 0; u < U; ++u) {
+        if constexpr (VEC == 1) {
+          acc[u][0] = fmaf(wk[i], (float)v[i][u], acc[u][0]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) acc[u][e] = fmaf(wk[i], (float)v[i][u][e], acc[u][e]);
+        }
       }
     }
   }
-  store_f32<T, VEC>(out + t * ldo + h, acc);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (h0 + u * 256 * VEC < H) store_f32<T, VEC>(out + t * ldo + h[u], acc[u]);
 }
 
 // grid: T workgroups of 4 waves; wave w takes the pairs k = w, w+4, ...: dys = w * dout and, with dw, the
@@ -356,9 +381,9 @@ hipError_t launch_dispatch_tokens(int dtype, const void* x, int64_t ldx, const i
   const bool v = vec16(dtype == EFF_DT_F32 ? 4 : 2, H, {x, xs}, {ldx, ldxs});
   return with_type(dtype, v, [&](auto t, auto vec) {
     typedef decltype(t) E;
-    constexpr int V = decltype(vec)::value;
+    constexpr int V = decltype(vec)::value, W = 256 * V * columns<V>();
     for (int64_t t0 = 0; t0 < T; t0 += kGridY) {
-      const dim3 g((unsigned)((H + 256 * V - 1) / (256 * V)), (unsigned)std::min(kGridY, T - t0));
+      const dim3 g((unsigned)((H + W - 1) / W), (unsigned)std::min(kGridY, T - t0));
       hipLaunchKernelGGL((k_dispatch<E, V>), g, dim3(256), 0, s, (const E*)x + t0 * ldx, ldx, pos + t0 * K, K, H, (E*)xs,
                          ldxs, rows);
     }
@@ -372,9 +397,9 @@ hipError_t launch_combine_tokens(int dtype, const void* ys, int64_t ldys, int64_
   const bool v = vec16(dtype == EFF_DT_F32 ? 4 : 2, H, {ys, residual, out}, {ldys, residual ? ldr : 0, ldo});
   return with_type(dtype, v, [&](auto t, auto vec) {
     typedef decltype(t) E;
-    constexpr int V = decltype(vec)::value;
+    constexpr int V = decltype(vec)::value, W = 256 * V * columns<V>();
     for (int64_t t0 = 0; t0 < T; t0 += kGridY) {
-      const dim3 g((unsigned)((H + 256 * V - 1) / (256 * V)), (unsigned)std::min(kGridY, T - t0));
+      const dim3 g((unsigned)((H + W - 1) / W), (unsigned)std::min(kGridY, T - t0));
       hipLaunchKernelGGL((k_combine_rows<E, V>), g, dim3(256), 0, s, (const E*)ys, ldys, rows, pos + t0 * K,
                          w ? w + t0 * K : nullptr, K, H, residual ? (const E*)residual + t0 * ldr : nullptr, ldr,
                          (E*)out + t0 * ldo, ldo);
