@@ -367,6 +367,16 @@ struct MmArgs {
 };
 // workspace that launch_matmul needs, from the sizes and strides alone
 int64_t matmul_workspace(const MmArgs& a);
+// Which kernel a product takes where its pointers are 16-byte aligned, into how many parts its k is split, and the
+// elements between the operands' rows as that kernel reads them (packed or not).
+enum { KIND_ANY, KIND_FEW1, KIND_FEW2, KIND_BIG, KIND_WIDE, KIND_MID, KIND_LOW };
+struct MmChoice {
+  int kind, splits;
+  int64_t ld_x, ld_w;
+};
+MmChoice matmul_choice(const MmArgs& a);
+// of a description's product: 0 forward, 1 dx, 2 dw
+MmChoice matmul_choice(const eff_matmul_desc& d, int product);
 // whether its launches hold the problem (a grid's threads stay below 2^32)
 bool matmul_fits(const MmArgs& a);
 hipError_t launch_matmul(const MmArgs& a, void* workspace, hipStream_t s);

@@ -425,7 +425,7 @@ k_mm_tile(MmArgs a) {
   }
   const int64_t n0 = (int64_t)nt_i * BNH;
 
-  // this thread's copies: byte offsets from a uniform address that advances with the steps (the host keeps them < 2^31)
+  // this thread's copies: byte offsets from a uniform address that advances with the steps (plan_matmul keeps them < 2^32)
   const T* x = reinterpret_cast<const T*>(a.x);
   const T* w = reinterpret_cast<const T*>(a.w) + (a.mode == MM_ROW_GROUPS ? g * a.swg : 0);
   const int64_t xcols = a.x_padded ? (a.M + 7) & ~(int64_t)7 : a.M;  // x contiguous along m
@@ -793,7 +793,7 @@ k_mm_few(MmArgs a, int slices) {
   int64_t m0 = (int64_t)tile * BM, m1 = min(a.M, m0 + BM);
   if (a.mode == MM_ROW_GROUPS && !find_tile<BM>(a.offsets, a.groups, a.M, tile, reinterpret_cast<int*>(s_few), &g, &m0, &m1)) return;
   const T* x = reinterpret_cast<const T*>(a.x);
-  const int K = (int)a.K, chunks = (K + 63) / 64;
+  const int K = (int)a.K, chunks = (int)((a.K + 63) / 64);  // k is below 2^31, the next multiple of 64 need not be
   const int64_t col = min((int64_t)n0 + (GLU ? r & 7 : r), a.N - 1);
   const T* w = reinterpret_cast<const T*>(a.w) + g * a.swg + (col + (GLU && r >= 8 ? a.N : 0)) * a.swn + q * 16;
   const T* xr[MT];
@@ -818,7 +818,7 @@ k_mm_few(MmArgs a, int slices) {
     if (c >= chunks) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (c * 64 + 64 > K && c * 64 + q * 16 + h * 8 >= K) {              // nothing there: zeros on both sides
+      if (c * 64 > K - 64 && c * 64 + q * 16 + h * 8 >= K) {              // nothing there: zeros on both sides
         fw[s][h] = V8{};
 #pragma unroll
         for (int i = 0; i < MT; ++i) fx[s][i][h] = V8{};
@@ -1046,7 +1046,6 @@ hipError_t allow_lds(const void* fn, int bytes, std::atomic<uint64_t>* done) {
 
 // ---- which kernel ----------------------------------------------------------------------------------------
 
-enum { KIND_ANY, KIND_FEW1, KIND_FEW2, KIND_BIG, KIND_WIDE, KIND_MID, KIND_LOW };
 typedef TileCfg<256, 256, 2, 4, 64, 2, true> Big;
 typedef TileCfg<128, 256, 2, 4, 32, 3, false> Wide;
 typedef TileCfg<128, 128, 2, 2, 64, 2, false> Mid;
@@ -1057,7 +1056,7 @@ struct Plan {
   int64_t pack_x, pack_w, part;  // workspace bytes of each (multiples of 256)
 };
 
-constexpr int64_t kMaxStride = (int64_t)1 << 22;
+constexpr int64_t kMaxStride = (int64_t)1 << 22;  // rows further apart are packed (a tile's 256 of them: 2^31 bytes)
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 int64_t w_rows(const MmArgs& a) { return a.act == EFF_ACT_SWIGLU ? 2 * a.N : a.N; }
 // rows and contiguous values of an operand in memory
@@ -1074,7 +1073,6 @@ Plan plan_matmul(const MmArgs& a) {
   const int64_t groups = std::max(1, a.groups);
   // Rows of whole 16-byte vectors, or padded with zeros up to one: an x row may then be read past K against rows of w
   // that are padded too, or (w contiguous along n) masked.
-  // The tiles' byte offsets are 32 bits: 256 rows of less than 2^22 values.
   const int64_t ldx = a.xk ? a.sxm : a.sxk, ldw = a.wk ? a.swn : a.swk;
   const bool x_ok = ldx % 8 == 0 && ldx < kMaxStride && (x_cols(a) % 8 == 0 || a.x_padded);
   const bool w_ok = ldw % 8 == 0 && ldw < kMaxStride && a.swg % 8 == 0 && (w_cols(a) % 8 == 0 || a.w_padded);
@@ -1097,14 +1095,24 @@ Plan plan_matmul(const MmArgs& a) {
   // Tiles and splits of k by an estimate of the time: rounds of workgroups over 256 CUs (`occ` on each; with one on each
   // a step is faster), 64-k steps, a workgroup's start and epilogue, and a split's sums written, read and joined.  The
   // constants (us) fit 4096^3, 8192 x 4096 x {512, 2048}, 2048^3 and 333 x 512 x 2560 to 15 %.
-  struct Tile { int kind; int64_t bm, bn; int occ; double alone, step, fixed; };
-  const Tile tiles[] = {{KIND_BIG, Big::BM, Big::BN, 1, 1.55, 1.55, 14},
-                        {KIND_WIDE, Wide::BM, Wide::BN, 2, 1.05, 2.05, 8},
-                        {KIND_MID, Mid::BM, Mid::BN, 2, 0.75, 1.0, 7},
-                        {KIND_LOW, Low::BM, Low::BN, 2, 0.42, 0.64, 6}};
+  struct Tile { int kind; int64_t bm, bn, bk; int occ; double alone, step, fixed; };
+  const Tile tiles[] = {{KIND_BIG, Big::BM, Big::BN, Big::BK, 1, 1.55, 1.55, 14},
+                        {KIND_WIDE, Wide::BM, Wide::BN, Wide::BK, 2, 1.05, 2.05, 8},
+                        {KIND_MID, Mid::BM, Mid::BN, Mid::BK, 2, 0.75, 1.0, 7},
+                        {KIND_LOW, Low::BM, Low::BN, Low::BK, 2, 0.42, 0.64, 6}};
+  // A tile's lanes hold unsigned 32-bit byte offsets from its first element.  Packing does not shorten a row that is long
+  // itself (2^23 values and 256 of them, say): such rows go to a tile of fewer, or to the general kernel.
+  const int64_t ld_x = p.pack_x ? up(x_cols(a), 8) : ldx, ld_w = p.pack_w ? up(w_cols(a), 8) : ldw;
+  auto reaches = [&](const Tile& t) {
+    const int64_t wide = std::min(glu ? t.bn / 2 : t.bn, a.N);
+    const int64_t x = a.xk ? (std::min(t.bm, a.M) - 1) * ld_x + t.bk : (t.bk - 1) * ld_x + t.bm;
+    const int64_t w = a.wk ? (wide - 1) * ld_w + t.bk : (t.bk - 1) * ld_w + t.bn;
+    return std::max(x, w) * 2 < (int64_t)1 << 32;
+  };
   const int64_t k = a.mode == MM_K_GROUPS ? std::max<int64_t>(1, a.K / groups) : a.K, steps = ceil_div(k, 64);
   double best = 0;
   for (const Tile& t : tiles) {
+    if (!reaches(t)) continue;
     double count = (double)ceil_div(n, t.bn);
     if (a.mode == MM_ROW_GROUPS) count *= std::max<double>((double)ceil_div(rows, t.bm) * std::min(groups, a.M), a.M / (double)t.bm);
     else count *= (double)ceil_div(a.M, t.bm) * (a.mode == MM_K_GROUPS ? groups : 1);
@@ -1116,6 +1124,7 @@ Plan plan_matmul(const MmArgs& a) {
       if (best == 0 || us < best) best = us, p.kind = t.kind, p.splits = (int)s;
     }
   }
+  if (best == 0) return Plan{KIND_ANY, 1, 0, 0, 0};
   if (p.splits > 1) {
     p.splits = (int)ceil_div(steps, ceil_div(steps, p.splits));  // none empty
     p.part = up((int64_t)p.splits * a.M * (glu ? 2 : 1) * up(a.N, 8) * 4, 256);
@@ -1197,6 +1206,11 @@ hipError_t launch_typed(MmArgs a, Plan p, char* ws, hipStream_t s) {
 }
 
 }  // namespace
+
+MmChoice matmul_choice(const MmArgs& a) {
+  const Plan p = plan_matmul(a);
+  return {p.kind, p.splits, p.pack_x ? up(x_cols(a), 8) : a.xk ? a.sxm : a.sxk, p.pack_w ? up(w_cols(a), 8) : a.wk ? a.swn : a.swk};
+}
 
 bool matmul_fits(const MmArgs& a) {
   if (a.M == 0) return true;

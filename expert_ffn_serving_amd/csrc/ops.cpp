@@ -105,6 +105,10 @@ const char* check_rows(int dtype, int64_t T, int K, int64_t H, int64_t rows) {
 
 }  // namespace
 
+MmChoice eff::matmul_choice(const eff_matmul_desc& d, int product) {
+  return matmul_choice(product == 0 ? forward_args(&d) : product == 1 ? dx_args(&d) : dw_args(&d));
+}
+
 extern "C" {
 
 int64_t eff_matmul_workspace(const eff_matmul_desc* d, int backward) {
