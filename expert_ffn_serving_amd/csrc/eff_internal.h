@@ -355,6 +355,7 @@ struct MmArgs {
   int64_t ldp;
   int dtype, y_f32, act, mode, groups;
   int xk, wk;              // whether x and w are contiguous along k (sxk, swk = 1) or along their own index (sxm, swn = 1)
+  const uint32_t* row_max; // fp16: null, or what x is scaled by, per output row (MM_K_GROUPS: of each group)
   int x_padded, w_padded;  // every row in memory is zero up to a multiple of 8 values
   // set by launch_matmul
   int simple;   // nothing but the activation of SwiGLU and the residual, in whole vectors
@@ -382,14 +383,19 @@ bool matmul_fits(const MmArgs& a);
 hipError_t launch_matmul(const MmArgs& a, void* workspace, hipStream_t s);
 
 // dz = dy * act'(pre) [M, N or 2N] rounded to dtype (dz null: not written), its rows zeroed up to lddz, and its column
-// sums per group (part and dbias null: none; part: matmul_dz_tiles rows of fp32)
+// sums per group (part and dbias null: none; part: matmul_dz_tiles rows of fp32).  fp16 may be scaled: row_max [M] gives
+// dz scaled by rows, col_max [groups or 1][N or 2N] dz_cols scaled by columns (both: col_max = row_max + M); written here
+// as bits of the largest magnitudes, for MmArgs::row_max.
 struct MmGrad {
   const void* dy;
   int64_t ldy;
   const void* pre;
   int64_t ldp;
   void* dz;
+  void* dz_cols;
   int64_t lddz;
+  uint32_t* row_max;
+  uint32_t* col_max;
   float* part;
   void* dbias;
   const int32_t* offsets;

@@ -64,7 +64,12 @@ int64_t dz_ld(const eff_matmul_desc* d) { return (w_rows(d) + 7) / 8 * 8; }
 bool needs_dz(const eff_matmul_desc* d) {
   return d->act != EFF_ACT_NONE || d->out_dtype != d->dtype || d->n % 8 || d->ld_y % 8;
 }
-int64_t dz_bytes(const eff_matmul_desc* d) { return needs_dz(d) ? align256(d->m * dz_ld(d) * 2) : 0; }
+// In fp16 dz is scaled into its range where it is rounded, by rows for dx and by columns for dw: a copy for each, and the
+// largest magnitude of every row and of every column of a group.
+bool scales_dz(const eff_matmul_desc* d) { return d->dtype == EFF_DT_F16 && (d->act != EFF_ACT_NONE || d->out_dtype != d->dtype); }
+int64_t dz_bytes(const eff_matmul_desc* d) { return needs_dz(d) ? align256(d->m * dz_ld(d) * 2) : 0; }  // of one copy
+int64_t dz_copies(const eff_matmul_desc* d) { return scales_dz(d) ? 2 : 1; }
+int64_t max_bytes(const eff_matmul_desc* d) { return scales_dz(d) ? align256((d->m + std::max(1, d->groups) * w_rows(d)) * 4) : 0; }
 int64_t part_bytes(const eff_matmul_desc* d) { return align256(matmul_dz_tiles(d->m, d->n, d->groups) * w_rows(d) * 4); }
 // dx[m,k] = sum over W's rows n of dz[m,n] w[n,k]
 MmArgs dx_args(const eff_matmul_desc* d) {
@@ -115,7 +120,7 @@ int64_t eff_matmul_workspace(const eff_matmul_desc* d, int backward) {
   if (const char* why = check_desc(d)) return bad("eff_matmul_workspace", why);
   if (d->m == 0) return 0;
   if (!backward) return align256(matmul_workspace(forward_args(d)));
-  return dz_bytes(d) + part_bytes(d) + align256(std::max(matmul_workspace(dx_args(d)), matmul_workspace(dw_args(d))));
+  return dz_copies(d) * dz_bytes(d) + max_bytes(d) + part_bytes(d) + align256(std::max(matmul_workspace(dx_args(d)), matmul_workspace(dw_args(d))));
 }
 
 int eff_matmul(const eff_matmul_desc* d, const void* x, const void* w, const void* bias, const void* residual,
@@ -160,21 +165,30 @@ int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x,
   g.dy = dy, g.ldy = d->ld_y, g.pre = pre, g.ldp = d->ld_pre;
   g.offsets = offsets, g.groups = d->groups;
   g.dbias = dbias;
-  const void* dz = dy;
+  const void *dz = dy, *dz_w = dy;  // for dx and for dw
   char* ws = static_cast<char*>(workspace);
-  if (needs_dz(d) && (dx || dw)) dz = g.dz = ws, g.lddz = dz_ld(d);
-  if (dbias) g.part = reinterpret_cast<float*>(ws + dz_bytes(d));
-  if (g.dz || dbias)
+  if (needs_dz(d) && (dx || dw)) {
+    dz = dz_w = g.dz = ws, g.lddz = dz_ld(d);
+    if (rows && scales_dz(d)) {
+      uint32_t* largest = reinterpret_cast<uint32_t*>(ws + 2 * dz_bytes(d));
+      if (dx) g.row_max = largest, largest += d->m;
+      else g.dz = nullptr;
+      if (dw) g.col_max = largest, dz_w = g.dz_cols = ws + dz_bytes(d);
+    }
+  }
+  if (ws) ws += dz_copies(d) * dz_bytes(d) + max_bytes(d);
+  if (dbias) g.part = reinterpret_cast<float*>(ws);
+  if (g.dz || g.dz_cols || dbias)
     if (int rc = launched(fn, launch_matmul_dz(g, s))) return rc;
-  if (ws) ws += dz_bytes(d) + part_bytes(d);
+  if (ws) ws += part_bytes(d);
   if (dx && rows) {
     MmArgs a = dx_args(d);
-    a.x = dz, a.w = w, a.y = dx, a.offsets = offsets;
+    a.x = dz, a.w = w, a.y = dx, a.offsets = offsets, a.row_max = g.row_max;
     if (int rc = launched(fn, launch_matmul(a, ws, s))) return rc;
   }
   if (dw) {
     MmArgs a = dw_args(d);
-    a.x = dz, a.w = x, a.y = dw, a.offsets = offsets;
+    a.x = dz_w, a.w = x, a.y = dw, a.offsets = offsets, a.row_max = g.col_max;
     if (int rc = launched(fn, launch_matmul(a, ws, s))) return rc;
   }
   return EFF_OK;

@@ -429,7 +429,9 @@ int eff_matmul(const eff_matmul_desc* d, const void* x, const void* w, const voi
  *   dx [m,k] = dz W;   dw [nw,k] = dz^T x;   dbias [nw] = the sum of dz's rows;   the residual's is dy itself.
  * With groups, each over the group's own rows (a group without rows: zeros); rows of dx in no group are left as
  * they were.  dy has ld_y, pre ld_pre (needed unless EFF_ACT_NONE).  Outputs may be NULL; x is needed for dw, w for
- * dx.  dz is rounded to dtype once where it enters dx and dw (fp32 in dbias).  m = 0 writes zeros to dw and dbias. */
+ * dx.  dz is rounded to dtype's bits once where it enters dx and dw (fp32 in dbias); in fp16 after an exact power of two
+ * per row (dx) or per column of a group (dw), so that its size does not matter: what is below 2^-39 of the largest there
+ * may become 0.  m = 0 writes zeros to dw and dbias. */
 int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x, const void* w, const void* pre,
                         const int32_t* offsets, void* dx, void* dw, void* dbias, void* workspace,
                         size_t workspace_bytes, eff_stream_t stream);
