@@ -36,21 +36,32 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f;
 constexpr float kGeluCubic = 0.044715f;
 
-// e^x to about 2 units in the last place for any x that is not NaN: 2^(x log2 e), the product's rounding error put back.
-// (expf and an IEEE division took two thirds of the time of the pass over dz.)
+// e^x to about 2 units in the last place, and 0 below 2^-126 (v_exp_f32 gives no subnormal numbers), for any x that is not
+// NaN: 2^(x log2 e), the product's rounding error put back.  (expf and an IEEE division took two thirds of the time of the
+// pass over dz.)
 __device__ inline float exp_f32(float x) {
   x = fminf(fmaxf(x, -104.f), 89.f);  // past both ends the result is 0 or infinity anyway
   const float t = x * 1.44269504088896341f, lo = fmaf(x, 1.44269504088896341f, -t) + x * 1.92596299e-8f;
   return __builtin_amdgcn_exp2f(t) * fmaf(lo, 0.693147180559945309f, 1.0f);
 }
-// 1 / (1 + e^-z), v_rcp_f32 being good to one unit in the last place; NaN stays NaN through its factor z
-__device__ inline float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + exp_f32(-z)); }
-__device__ inline float act_silu(float z) { return z * sigmoid(z); }
+// The sigmoid of v from h = e^(-|v|/2): 1 / (1 + h^2), times h^2 where v < 0.  v_rcp_f32, good to one unit in the last place,
+// gets numbers in [1, 2]; 1 / (1 + e^-v) is below 2^-126 for v < -87.3, where it would give 0.
+struct Sigmoid {
+  float h, r;
+  bool pos;
+  __device__ explicit Sigmoid(float v) : h(exp_f32(-0.5f * fabsf(v))), r(__builtin_amdgcn_rcpf(fmaf(h, h, 1.0f))), pos(v >= 0.f) {}
+  __device__ float value() const { return pos ? r : h * h * r; }
+  // z times it, of which z * h * h may still be a normal number where h * h is none
+  __device__ float times(float z) const { return pos ? z * r : z * h * (h * r); }
+};
+// NaN gives 0 (or 1), and stays NaN through the factor z that every use has
+__device__ inline float sigmoid(float z) { return Sigmoid(z).value(); }
+__device__ inline float act_silu(float z) { return Sigmoid(z).times(z); }
 __device__ inline float act_one(int act, float z) {
   switch (act) {
     case EFF_ACT_SILU: return act_silu(z);
     case EFF_ACT_GELU: return 0.5f * z * erfcf(-z * kInvSqrt2);
-    case EFF_ACT_GELU_TANH: return z * sigmoid(2.0f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));  // (1 + tanh u) / 2 = sigmoid(2u)
+    case EFF_ACT_GELU_TANH: return Sigmoid(2.0f * kSqrt2OverPi * (z + kGeluCubic * z * z * z)).times(z);  // (1 + tanh u) / 2 = sigmoid(2u)
     default: return z;
   }
 }
