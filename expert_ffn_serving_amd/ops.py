@@ -5,6 +5,10 @@ Every call enqueues on `stream` (a torch.cuda.Stream, a handle, or None for the 
 tensors' device), writes the outputs it is given and keeps nothing.  Matrices need unit stride inside a row;
 any stride between rows works for inputs (0 broadcasts a row) and any that keeps rows apart for outputs.
 A wrong type, shape, stride or device raises EffError (EFF_EINVAL) before anything is launched.
+
+torch's autograd records none of these calls, whether inputs require grad or not: a training step calls the *_backward
+functions itself.  Outputs count as written in place (their versions go up), so a graph that saved one refuses its
+backward pass, as after a torch operation with out=.
 """
 from __future__ import annotations
 
@@ -18,6 +22,7 @@ from . import ACT_NONE, ACT_SWIGLU, EFF_EINVAL, EffError, lib
 _DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _HALF = {torch.bfloat16: 0, torch.float16: 1}
 _I32, _F32 = torch.int32, torch.float32
+_written = torch._C._increment_version    # takes tensors in a tuple or list; those of inference mode have no version
 
 
 class MatmulDesc(ctypes.Structure):
@@ -176,6 +181,7 @@ def _forward(x, w, offsets, y, bias, act, residual, pre, stream):
         d = _pack_desc(_HALF[dt], _DT[yt], act, groups, m, n, k, ldx, ldw, ldy, ldr, ldp, sw, 0, 0, 0)
         L = lib()
         _call(L.eff_matmul, dev, stream, (d, px, pw, pb, pr, po, py, pp), L.eff_matmul_workspace(d, 0))
+        _written((y,) if pre is None else (y, pre))
     except AttributeError as e:
         _no_tensor(e)
 
@@ -222,6 +228,7 @@ def _backward(dy, x, w, offsets, dx, dw, dbias, act, pre, stream):
         d = _pack_desc(_HALF[dt], _DT[dyt], act, groups, m, n, k, ldx, ldw, lddy, 0, ldp, sw, lddx, lddw, sdw)
         L = lib()
         _call(L.eff_matmul_backward, dev, stream, (d, pdy, px, pw, pp, po, pdx, pdw, pdb), L.eff_matmul_workspace(d, 1))
+        _written([t for t in (dx, dw, dbias) if t is not None])
     except AttributeError as e:
         _no_tensor(e)
 
@@ -256,6 +263,7 @@ def sort_tokens(ids, offsets, order, pos, stream=None):
         pp = _dense("pos", pos, _I32, shape, dev)
         L = lib()
         _call(L.eff_sort_tokens, dev, stream, (pi, n, E, po, pr, pp), L.eff_sort_tokens_workspace(n, E))
+        _written((offsets, order, pos))
     except AttributeError as e:
         _no_tensor(e)
 
@@ -286,6 +294,7 @@ def dispatch_tokens(x, pos, xs, stream=None):
         ps, lds = _matrix("xs", xs, x.dtype, R, H, dev, True)
         pp, K = _pos(pos, T, dev)
         _call(lib().eff_dispatch_tokens, dev, stream, (_DT[x.dtype], px, ldx, pp, T, K, H, ps, lds, R))
+        _written((xs,))
     except AttributeError as e:
         _no_tensor(e)
 
@@ -300,6 +309,7 @@ def dispatch_tokens_backward(dxs, pos, dx, stream=None):
         px, ldx = _matrix("dx", dx, dxs.dtype, T, H, dev, True)
         pp, K = _pos(pos, T, dev)
         _call(lib().eff_dispatch_tokens_backward, dev, stream, (_DT[dxs.dtype], ps, lds, R, pp, T, K, H, px, ldx))
+        _written((dx,))
     except AttributeError as e:
         _no_tensor(e)
 
@@ -317,6 +327,7 @@ def combine_tokens(ys, pos, w, out, residual=None, stream=None):
         pp, K = _pos(pos, T, dev)
         pw = _dense("w", w, _F32, (T, K), dev)
         _call(lib().eff_combine_tokens, dev, stream, (_DT[ys.dtype], py, ldy, R, pp, pw, T, K, H, pr, ldr, po, ldo))
+        _written((out,))
     except AttributeError as e:
         _no_tensor(e)
 
@@ -336,5 +347,6 @@ def combine_tokens_backward(dout, ys, pos, w, dys, dw=None, stream=None):
         pg = _dense("dw", dw, _F32, (T, K), dev) if dw is not None else None
         _call(lib().eff_combine_tokens_backward, dev, stream,
               (_DT[dout.dtype], pd, ldd, py, ldy, R, pp, pw, T, K, H, ps, lds, pg))
+        _written((dys,) if dw is None else (dys, dw))
     except AttributeError as e:
         _no_tensor(e)
