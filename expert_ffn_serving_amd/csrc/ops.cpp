@@ -156,7 +156,8 @@ int eff_matmul_backward(const eff_matmul_desc* d, const void* dy, const void* x,
       (dw && d->groups > 1 && d->stride_dw < (nw - 1) * std::max(d->ld_dw, d->k) + d->k))
     return bad(fn, "rows of an output overlap");
   if (int rc = check_ws(fn, eff_matmul_workspace(d, 1), workspace, workspace_bytes)) return rc;
-  if (rows && ((dx && !matmul_fits(dx_args(d))) || (dw && !matmul_fits(dw_args(d))) || !matmul_dz_fits(d->m, d->n, d->groups)))
+  if ((rows && dx && !matmul_fits(dx_args(d))) || (dw && !matmul_fits(dw_args(d))) ||
+      ((rows || dbias) && !matmul_dz_fits(d->m, d->n, d->groups)))
     return bad(fn, "too many output tiles for one launch");
   hipStream_t s = (hipStream_t)stream;
   MmGrad g = {};
