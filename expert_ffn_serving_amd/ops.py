@@ -22,6 +22,7 @@ from . import ACT_NONE, ACT_SWIGLU, EFF_EINVAL, EffError, lib
 _DT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _HALF = {torch.bfloat16: 0, torch.float16: 1}
 _I32, _F32 = torch.int32, torch.float32
+_MAX_GROUPS, _MAX_TOPK = 4096, 32         # the library's own bounds; its counts are 32-bit
 _written = torch._C._increment_version    # takes tensors in a tuple or list; those of inference mode have no version
 
 
@@ -149,8 +150,8 @@ def _sizes(x, w, act, grouped):
 def _weights(w, dt, groups, nw, k, dev, offsets):
     if offsets is None:
         return _matrix("w", w, dt, nw, k, dev) + (0, None)
-    if groups < 1:
-        _bad("w needs at least one group")
+    if not 1 <= groups <= _MAX_GROUPS:
+        _bad("w needs 1 to %d groups" % _MAX_GROUPS)
     return _stack("w", w, dt, groups, nw, k, dev) + (_dense("offsets", offsets, _I32, (groups + 1,), dev),)
 
 
@@ -254,8 +255,8 @@ def sort_tokens(ids, offsets, order, pos, stream=None):
     shaped like ids (place of a pair, -1 for an id outside [0,E))."""
     try:
         dev = _device("ids", ids)
-        if offsets.dim() != 1 or offsets.shape[0] < 2:
-            _bad("offsets must be a vector of E+1 values")
+        if offsets.dim() != 1 or not 2 <= offsets.shape[0] <= _MAX_GROUPS + 1:
+            _bad("offsets must be a vector of E+1 values, E from 1 to %d" % _MAX_GROUPS)
         n, E, shape = ids.numel(), offsets.shape[0] - 1, ids.shape
         pi = _dense("ids", ids, _I32, shape, dev)
         po = _dense("offsets", offsets, _I32, (E + 1,), dev)
@@ -280,6 +281,8 @@ def _pos(pos, T, dev):
     shape = pos.shape
     if len(shape) != 2 or shape[0] != T:
         _bad("pos must be [T,K] with T = %d" % T)
+    if shape[1] > _MAX_TOPK:
+        _bad("pos has more than %d places a token" % _MAX_TOPK)
     return _dense("pos", pos, _I32, shape, dev), shape[1]
 
 
