@@ -185,6 +185,8 @@ def _forward(x, w, offsets, y, bias, act, residual, pre, stream):
         _written((y,) if pre is None else (y, pre))
     except AttributeError as e:
         _no_tensor(e)
+    except struct.error as e:
+        _bad("act or a size is not an integer that the description holds (%s)" % e)
 
 
 def matmul(x, w, y, bias=None, act=ACT_NONE, residual=None, pre=None, stream=None):
@@ -232,6 +234,8 @@ def _backward(dy, x, w, offsets, dx, dw, dbias, act, pre, stream):
         _written([t for t in (dx, dw, dbias) if t is not None])
     except AttributeError as e:
         _no_tensor(e)
+    except struct.error as e:
+        _bad("act or a size is not an integer that the description holds (%s)" % e)
 
 
 def matmul_backward(dy, x, w, dx=None, dw=None, dbias=None, act=ACT_NONE, pre=None, stream=None):

@@ -1,4 +1,5 @@
-"""Counts that do not fit the library's 32-bit ones are refused by the binding, before it calls the library."""
+"""Arguments that the binding refuses before it calls the library: counts that do not fit the library's 32-bit ones, values of
+the wrong kind."""
 import pytest
 import torch
 
@@ -35,3 +36,12 @@ def test_counts_beyond_32_bits(eff):
     w, y = torch.ones(1, 8, 8, dtype=BF, device="cuda").expand(1 << 32, 8, 8), torch.zeros(1, 8, dtype=BF, device="cuda")
     refused(eff, lambda: eff.grouped_matmul(x, w, offsets, y))
     assert not y.any()
+
+
+def test_values_of_another_kind(eff):
+    x, w, y = (torch.ones(s, dtype=BF, device="cuda") for s in ((4, 16), (8, 16), (4, 8)))
+    for act in (1.0, 4.0, "silu", None):
+        refused(eff, lambda: eff.matmul(x, w, y, act=act))
+        refused(eff, lambda: eff.matmul_backward(y, x, w, dx=torch.empty_like(x), act=act, pre=y))
+    for stream in ("s", 1.5):
+        refused(eff, lambda: eff.matmul(x, w, y, stream=stream))
