@@ -113,8 +113,12 @@ def _call(fn, dev, stream, args, need=None):
             return _call(fn, dev, stream, args, need)
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif isinstance(stream, int):
+        handle = stream
     else:
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        handle = stream.cuda_stream
+        if stream.device_index != dev:
+            _bad("the stream is on GPU %d, the tensors on GPU %d" % (stream.device_index, dev))
     if need is None:
         rc = fn(*args, handle)
     elif need <= 0:      # a negative number is the description's error: the call itself reports it

@@ -1,5 +1,5 @@
 """Arguments that the binding refuses before it calls the library: counts that do not fit the library's 32-bit ones, values of
-the wrong kind."""
+the wrong kind, a stream of another device."""
 import pytest
 import torch
 
@@ -45,3 +45,13 @@ def test_values_of_another_kind(eff):
         refused(eff, lambda: eff.matmul_backward(y, x, w, dx=torch.empty_like(x), act=act, pre=y))
     for stream in ("s", 1.5):
         refused(eff, lambda: eff.matmul(x, w, y, stream=stream))
+
+
+def test_stream_of_another_device(eff):
+    class Stream:
+        cuda_stream, device_index = torch.cuda.current_stream().cuda_stream, 1
+
+    x, w, y = (torch.ones(s, dtype=BF, device="cuda") for s in ((4, 16), (8, 16), (4, 8)))
+    refused(eff, lambda: eff.matmul(x, w, y, stream=Stream()))
+    eff.matmul(x, w, y, stream=torch.cuda.current_stream())
+    assert (y == 16).all()
