@@ -331,8 +331,8 @@ def test_gradients_against_differences(eff, act):
         assert ((got.cpu().double() - num).abs() <= lim).all(), i
 
 
-# Sizes at which every tile (256 x 256, 128 x 256, 128 x 128, 64 x 128) is taken, whole and with its k split, in each
-# layout of the operands; none is a multiple of its tile.
+# Sizes at which each tile (256 x 256, 128 x 256, 128 x 128, 64 x 128) is taken, some with k split; none is a multiple of its
+# tile.  Every tile in every layout, whole and split: matmul_paths.
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("shape", [(2051, 4104, 1032), (2051, 2056, 4104), (2051, 1032, 4104), (1030, 1032, 4104), (2051, 2056, 136),
                                    (2051, 4104, 136)])

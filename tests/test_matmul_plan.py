@@ -1,5 +1,6 @@
 """Which kernel a product takes, asked of the library without a GPU: what a tile's kernel can address is what it is given."""
 import ctypes
+import itertools
 import os
 import random
 import subprocess
@@ -7,6 +8,7 @@ import subprocess
 import pytest
 
 from expert_ffn_serving_amd.ops import MatmulDesc
+from tests.matmul_paths import PATHS
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 ANY, FEW1, FEW2, BIG, WIDE, MID, LOW = range(7)
@@ -86,3 +88,20 @@ def test_rows_that_fit_keep_their_tiles(choice):
     """The tiles are given up only for rows that they cannot address."""
     assert choice(256, 256, (1 << 23) - 8)[0] in TILES and choice(64, 128, (1 << 24) - 64)[0] in TILES
     assert choice(1, 8, (1 << 31) - 1)[0] == FEW1        # W streamed through registers: addresses of 64 bits
+
+
+def test_the_paths_reach_every_tile(choice):
+    reached = set()
+    for product, m, n, k, act, groups in PATHS:
+        for dtype in (0, 1):
+            kind, splits = choice(m, n, k, product, act, groups, dtype=dtype)[:2]
+            reached.add((product, groups > 0, act == 4 and product == FORWARD, kind, splits > 1, dtype))
+    want = set()
+    for product, grouped, glu, kind, split, dtype in itertools.product((FORWARD, DX, DW), (False, True), (False, True), range(FEW1, LOW + 1),
+                                                                       (False, True), (0, 1)):
+        if split and (grouped or kind in (FEW1, FEW2)):     # k is split where there is one product of few tiles
+            continue
+        if product != FORWARD and (glu or kind in (FEW1, FEW2)):
+            continue
+        want.add((product, grouped, glu, kind, split, dtype))
+    assert reached == want
