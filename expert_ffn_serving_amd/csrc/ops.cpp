@@ -133,6 +133,8 @@ int eff_matmul(const eff_matmul_desc* d, const void* x, const void* w, const voi
   const int64_t nw = w_rows(d);
   if (inputs_ld_bad(d->ld_x) || inputs_ld_bad(d->ld_w) || inputs_ld_bad(d->ld_residual) || d->stride_w < 0) return bad(fn, "negative stride");
   if (d->m > 1 && (d->ld_y < d->n || (pre && d->ld_pre < nw))) return bad(fn, "rows of an output overlap");
+  if (residual == y && (d->out_dtype != d->dtype || (d->m > 1 && d->ld_residual != d->ld_y)))
+    return bad(fn, "y may be the residual only with its type and ld");
   if (int rc = check_ws(fn, eff_matmul_workspace(d, 0), workspace, workspace_bytes)) return rc;
   MmArgs a = forward_args(d);
   if (!matmul_fits(a)) return bad(fn, "too many output tiles for one launch");
@@ -240,6 +242,7 @@ int eff_combine_tokens(int dtype, const void* ys, int64_t ld_ys, int64_t rows, c
   if (T == 0) return EFF_OK;
   if ((!ys && rows > 0) || !pos || !w || !out) return bad(fn, "ys, pos, w and out are needed");
   if (ld_ys < 0 || ld_residual < 0 || (T > 1 && ld_out < H)) return bad(fn, "negative stride, or rows of an output overlap");
+  if (residual == out && T > 1 && ld_residual != ld_out) return bad(fn, "out may be the residual only with its ld");
   return launched(fn, launch_combine_tokens(dtype, ys, ld_ys, rows, pos, w, T, K, H, residual, ld_residual, out, ld_out, (hipStream_t)stream));
 }
 

@@ -418,7 +418,7 @@ typedef struct eff_matmul_desc {
 int64_t eff_matmul_workspace(const eff_matmul_desc* d, int backward);
 
 /* y (and pre if not NULL).  Products of the 16-bit values are exact and summed in fp32; bias, activation and
- * residual are fp32; each output is rounded once.  y may be the residual itself (same pointer and ld).
+ * residual are fp32; each output is rounded once.  y may be the residual itself (same pointer, type and ld).
  * bias, residual, pre may be NULL; offsets only with groups; workspace: 256-byte aligned.
  * Errors: EFF_EINVAL (nothing launched), EFF_EHIP. */
 int eff_matmul(const eff_matmul_desc* d, const void* x, const void* w, const void* bias, const void* residual,
@@ -454,7 +454,7 @@ int eff_dispatch_tokens_backward(int dtype, const void* dxs, int64_t ld_dxs, int
                                  int64_t T, int K, int64_t H, void* dx, int64_t ld_dx, eff_stream_t stream);
 
 /* combine: out[t,:] = residual[t,:] + sum over k ascending of w[t,k] * ys[pos[t,k],:], fp32, rounded once.
- * w fp32 [T,K]; residual may be NULL (ld_residual 0: one row for all), and out may be the residual itself.
+ * w fp32 [T,K]; residual may be NULL (ld_residual 0: one row for all), and out may be the residual itself (same ld).
  * Weights and rows of unrouted pairs are not used, whatever they hold.
  * backward: dys[pos[t,k],:] = w[t,k] * dout[t,:] (other rows left as they were) and, if not NULL, dw fp32 [T,K] =
  * <dout[t,:], ys[pos[t,k],:]> in fp32 (0 for an unrouted pair); the residual's gradient is dout itself. */
