@@ -360,10 +360,11 @@ k_mm_any(MmArgs a) {
 // with k-contiguous weights the LDS rows are dealt to the products so that a lane's columns of all of them are
 // consecutive.
 //
-// Measured: 8192^3 800 us, 1374 TFLOP/s (the library's product 1612), 4096^3 105 us; the three layouts within 6 %.  The
+// Measured: 8192^3 814 us, 1350 TFLOP/s (the library's product 1575 in the same run), 4096^3 114 us (103); the three layouts
+// within 7 %.  The
 // matrix cores are busy 68 % of the time at 1.8 GHz (the library's 92 % at 1.5 GHz: both run into the power limit); the
 // rest is the step's barrier and the workgroups' starts and epilogues, 14 us of a 256 x 256 tile's 64 at 2048 k.  Steps
-// of 32 k of 256-row tiles fetch half lines, twice the L2 requests (8192^3 954 us and not 922 at that stage).  256 experts x 48 rows (4096 ->
+// of 32 k of 256-row tiles fetch half lines, twice the L2 requests (8192^3 954 us and not 922 when it was tried).  256 experts x 48 rows (4096 ->
 // 2 x 2048, SwiGLU) are bound by the 8.6 GB of weights: 1.67 ms, 5.2 TB/s of the 6.4 that a plain read reaches; 32-row,
 // 128-row and 256-column tiles, other depths and steps of 32 or 128 k took 1.69 to 2.6 ms.
 __device__ const uint4 g_zero16[1] = {{0u, 0u, 0u, 0u}};  // what a copy past the last k reads
@@ -563,8 +564,8 @@ k_mm_tile(MmArgs a) {
   if constexpr (C::AHEAD) {
     // One wave's products hide its LDS reads: an x operand is read again for the next half step as soon as its products
     // are issued, the w operands are read one half step ahead into a second set (both in a second set spill).  The barrier
-    // of a step stands inside the last half's products, when the reads before it have long returned.  8192^3: 1374
-    // TFLOP/s (with 1 to 6 operands before the barrier, or raised priority: the same); each half's reads before its products 1137, two groups of waves taking turns at LDS and the matrix cores 1312.
+    // of a step stands inside the last half's products, when the reads before it have long returned.  8192^3: 1350 to
+    // 1374 TFLOP/s (with 1 to 6 operands before the barrier, or raised priority: the same); each half's reads before its products 1137, two groups of waves taking turns at LDS and the matrix cores 1312.
     static_assert(KS == 2 && S == 2, "two halves, two buffers");
     constexpr int LATE = 2;  // x operands whose products stand before the barrier
     V8 fw[2][NT], fx[MT];
@@ -686,7 +687,9 @@ k_mm_tile(MmArgs a) {
         *reinterpret_cast<f32x4_t*>(s_c + ((wm * IP + i) * 16 + r) * LDC + col) = acc[p * IP + i][j];
       }
     meet();
-    if (a.simple) {  // whole vectors, no bias, nothing saved, no other activation: every round's accesses at once
+    // Whole vectors, no bias, nothing saved, no other activation: every round's accesses at once.  8192 x 4096 x 2048 by epilogue:
+    // none 125 us, residual 134; the general rounds below: fp32 output 133, silu 142, gelu 168, bias, gelu and pre 175.
+    if (a.simple) {
 #pragma unroll
       for (int h = 0; h < NR; ++h) {
         const int64_t m = row_of(p, tid / VR + h * ROUND);
@@ -744,7 +747,7 @@ k_mm_tile(MmArgs a) {
   }
 }
 
-// A split k's sums added in order of k, and the epilogue (333 x 515, 8 splits: 6 us, a launch and two trips to memory).  grid: ceil(M * vectors / 256); a thread takes 8 columns.
+// A split k's sums added in order of k, and the epilogue (333 x 515, 7 splits: 6 us, a launch and two trips to memory).  grid: ceil(M * vectors / 256); a thread takes 8 columns.
 template <typename T, bool GLU>
 __global__ void __launch_bounds__(256)
 k_mm_join(MmArgs a, int splits) {
@@ -904,8 +907,10 @@ k_mm_few(MmArgs a, int slices) {
 // ---- dz and dbias --------------------------------------------------------------------------------------
 //
 // One pass over dy and pre: a workgroup takes ROWS rows of one group and 64 VEC columns, each of its 4 waves every
-// fourth row.  It writes dz rounded to T (the operand that dx and dw multiply; columns up to lddz are zeroed, so that
-// dz's rows are whole 16-byte vectors) and the columns' fp32 sums over its rows, which a second kernel adds up in row
+// fourth row.  It writes dz rounded to T (the operand that dx and dw multiply: the matrix cores take 16 bits, and a second
+// term for the bits below would double both products, 116 and 123 us of 247 here; the gradients' error in norm is 2.3e-3 in
+// bf16 where their own rounding alone makes 1.7e-3; columns up to lddz are zeroed, so that dz's rows are whole 16-byte
+// vectors) and the columns' fp32 sums over its rows, which a second kernel adds up in row
 // order.  Bound by HBM, every value read and written once: 4096 x 2 x 2048 SwiGLU 21 us, 4.0 TB/s.
 // Rows of one workgroup: 32, or 8 where 32 leave most of the chip idle (100 rows x 640, gelu: 21 -> 8 us; with 8 rows
 // everywhere the sums' second pass reads four times as much).
@@ -1230,20 +1235,29 @@ Plan plan_matmul(const MmArgs& a) {
   const bool w_ok = ldw % 8 == 0 && ldw < kMaxStride && a.swg % 8 == 0 && (w_cols(a) % 8 == 0 || a.w_padded);
   if (!x_ok) p.pack_x = up(x_rows(a) * up(x_cols(a), 8) * 2, 256);
   if (!w_ok) p.pack_w = up(w_mem_rows(a) * up(w_cols(a), 8) * 2, 256);
-  // all groups' weights are only worth copying if most of them are used by several rows
+  // Packing copies the weights of all groups, with rows or without; the general kernel reads what it needs, value by value.
+  // y and dx in us, packed and general: 8 groups of 1024 x 1025, 64 rows 18 and 23, 31 and 33; 512 rows 23 and 25, 38 and 39;
+  // 64 groups, 512 rows 75 and 85, 64 and 69; 4096 rows 92 and 96, 76 and 84; 256 groups of 1024 x 2049, 160 rows 492 and 488,
+  // 216 and 230; 4096 rows 611 and 604, 441 and 454; 512 groups of 640 x 2561, 160 rows 624 and 615, 146 and 119.
   if (p.pack_w && a.mode == MM_ROW_GROUPS && a.M < 16 * groups) return Plan{KIND_ANY, 1, 0, 0, 0};
   const int64_t n = w_rows(a);
   const int64_t rows = a.mode == MM_ROW_GROUPS ? a.M / std::max<int64_t>(1, std::min(groups, a.M)) : a.M;
   if (a.xk && a.wk) {
-    // the tiles' waves share x, the split of k over waves fills the chip when there are few tiles
+    // The tiles' waves share x, the split of k over waves fills the chip when there are few tiles.  In us, streamed and tiles:
+    // 2560 -> 512, 1 row 7.1 and 9.3, 32 rows 10.7 and 10.3; 4096 -> 4096, 1 row 7.9 and 12.4, 16 rows 10.4 and 15.7, 32 rows
+    // 13.9 and 13.9, 33 rows 19.9 and 13.6; 4096 -> 16384, 1 row 22.7 and 25.1, 16 rows 31 and 25, 32 rows 45 and 26; 17 rows of
+    // 4096 -> 4096 16 at a time 15.6, 32 at a time 11.4.  Groups: 8 of 8 rows, 2048 -> 1024 (64 tiles) 11.6 and 18.6; with 512
+    // tiles and more, 64 of 8 rows, 2048 -> 1024 54 and 44, 512 of 16 rows, 1024 -> 512 166 and 103.
     const bool fill = row_tiles(a, Low::BM) * ceil_div(n, Low::BN) >= 512;
     if (rows <= 16 && !fill) return p.kind = KIND_FEW1, p;
     if (rows <= 32 && !fill) return p.kind = KIND_FEW2, p;
   }
-  // 256 x 256 tiles have the most products per byte (4096^3 118 us, 128 x 256 140); 128 x 256 tiles, two workgroups on
-  // a CU so that one's epilogue runs under the other's products, win where sums are short (8192 x 4096 x 512 46 us, 256 x
-  // 256 53; gradients of 256 experts 790 us, 1000); 128 x 128 and 64 x 128 fill the chip when there are few tiles (2048^3
-  // 25 us with 64 x 128, 30 and 55 with the larger ones) and waste less on experts with few rows.
+  // 256 x 256 tiles have the most products per byte; 128 x 256 tiles, two workgroups on a CU so that one's epilogue runs under
+  // the other's products, win where sums are short; 128 x 128 and 64 x 128 fill the chip when there are few tiles and waste
+  // less on experts with few rows.  Each forced everywhere, us (in this order): 4096^3 114, 145, 132, 182; 8192 x 4096 x 2048
+  // 122, 142, 136, 176; 8192 x 4096 x 512 47, 47, 49, 62; 2048^3 44, 40, 29, 26; 1000^3 27, 23, 15, 12; 333 x 512 x 2560 23, 19,
+  // 16, 15; 256 experts of 128 rows, 2048 <-> 1024, dw 453, 435, 515, 607 and dx 332, 275, 289, 327; of 48 rows, 4096 -> 4096
+  // 2089, 1770, 1807, 1737.
   // Tiles and splits of k by an estimate of the time: rounds of workgroups over 256 CUs (`occ` on each; with one on each
   // a step is faster), 64-k steps, a workgroup's start and epilogue, and a split's sums written, read and joined.  The
   // constants (us) fit 4096^3, 8192 x 4096 x {512, 2048}, 2048^3 and 333 x 512 x 2560 to 15 %.
@@ -1301,7 +1315,7 @@ hipError_t launch_tile_c(const MmArgs& a, int splits, hipStream_t s) {
 template <typename T, int MT, bool GLU>
 hipError_t launch_few(const MmArgs& a, hipStream_t s) {
   const int64_t slices = ceil_div(a.N, GLU ? 8 : 16), jobs = slices * row_tiles(a, 16 * MT);
-  // waves per workgroup: about 16 per CU over the launch, each with at least two chunks of k
+  // waves per workgroup: up to 32 per CU over the launch, each with at least two chunks of k
   int waves = 16;
   while (waves > 1 && (jobs * waves > 8192 || waves * 128 > a.K + 127)) waves /= 2;
   hipLaunchKernelGGL((k_mm_few<T, MT, GLU>), dim3((unsigned)jobs), dim3(64 * waves), waves * MT * 1024, s, a, (int)slices);
@@ -1323,6 +1337,8 @@ hipError_t launch_kind(const MmArgs& a, const Plan& p, hipStream_t s) {
 template <typename T>
 hipError_t launch_typed(MmArgs a, Plan p, char* ws, hipStream_t s) {
   const bool glu = a.act == EFF_ACT_SWIGLU;
+  // The workspace is sized without the pointers, so an operand that only begins at an odd place is not packed.  8192 x 4096 x
+  // 2048: 730 us where the tiles take 126 (packed for an odd stride: 132), its gradients 948 where 256.
   if ((!p.pack_x && (uintptr_t)a.x % 16) || (!p.pack_w && (uintptr_t)a.w % 16)) p.kind = KIND_ANY;
   if (p.kind == KIND_ANY) {
     const int64_t tiles = ceil_div(a.N, glu ? kAnyBN / 2 : kAnyBN) * row_tiles(a, kAnyBM);
@@ -1388,7 +1404,7 @@ hipError_t launch_matmul(const MmArgs& in, void* workspace, hipStream_t s) {
   MmArgs a = in;
   a.vec = aligned16({a.y, a.bias, a.residual, a.pre}, {a.N, a.ldy, a.syg, a.residual ? a.ldr : 0, a.pre ? a.ldp : 0}, 2);
   // Outputs that no cache holds (256 MiB) are stored past it: the next kernels find their inputs there (gradients of 256
-  // experts, 1 GiB of dw: 794 -> 760 us).
+  // experts, 1 GiB of dw: 794 -> 760 us when it was tried).
   a.stream = a.M * a.N * (a.mode == MM_K_GROUPS ? a.groups : 1) * (a.y_f32 ? 4 : 2) > (int64_t)256 << 20;
   a.plain = a.vec && !a.stream && !a.bias && !a.residual && !a.pre && !a.y_f32 && a.act == EFF_ACT_NONE;
   a.simple = a.vec && !a.bias && !a.pre && !a.y_f32 && (a.act == EFF_ACT_NONE || a.act == EFF_ACT_SWIGLU);

@@ -359,9 +359,12 @@ constexpr int64_t kGridY = 65535;  // tokens per launch of the two-dimensional g
 
 }  // namespace
 
-// Pairs of one workgroup.  Up to kSortOne pairs one workgroup does the whole sort (one launch).
+// Up to kSortOne pairs one workgroup does the whole sort (one launch): in us, one workgroup and 32 parts, 4096 pairs over 256
+// experts 10.1 and 12.7, over 4096 19 and 30; 8192 14.3 and 12.9, 27 and 30; 16384 22.7 and 13.0, 45 and 31.
 constexpr int64_t kSortOne = 8192;
-constexpr int64_t kSortParts = 128;  // at most; up to 256K pairs 32, whose counts are read in one go
+// Parts beyond: 32, whose counts are read in one go, and 128 above 256K pairs.  32 and 128: 49152 pairs over 256 14.4 and 24.7,
+// 256K 22 and 27, over 4096 51 and 84; 512K 32 and 30, 72 and 91; 1M 52 and 35, 124 and 106; 4M 200 and 80, 426 and 181.
+constexpr int64_t kSortParts = 128;
 int64_t sort_parts(int64_t n) { return n <= (int64_t)1 << 18 ? 32 : kSortParts; }
 
 int64_t sort_workspace(int64_t n, int E) {

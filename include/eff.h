@@ -413,8 +413,11 @@ typedef struct eff_matmul_desc {
   int64_t ld_dx, ld_dw, stride_dw; /* eff_matmul_backward's outputs */
 } eff_matmul_desc;
 
-/* Workspace bytes that eff_matmul (backward = 0) or eff_matmul_backward (1) needs for this problem at most, a
- * multiple of 256, 0 if none; EFF_EINVAL for a bad description. */
+/* Workspace bytes that eff_matmul (backward = 0) or eff_matmul_backward (1) needs for this problem at most, whichever
+ * outputs it is asked for, a multiple of 256, 0 if none; EFF_EINVAL for a bad description.  Operands whose rows are no
+ * whole 16-byte vectors (k or ld_* not a multiple of 8) are copied into it first, of a stack of groups with 16 rows and
+ * more each the weights of all groups; keep such weights padded to spare that.  x and w that do not begin at a
+ * multiple of 16 bytes are not copied and take a general kernel, 4 to 6 times slower at large sizes. */
 int64_t eff_matmul_workspace(const eff_matmul_desc* d, int backward);
 
 /* y (and pre if not NULL).  Products of the 16-bit values are exact and summed in fp32; bias, activation and
