@@ -16,7 +16,7 @@ def eff():
 
 
 def columns(k, count, seed):
-    """Columns of a long row: both ends, the places around each multiple of 2^31 bytes, and others."""
+    """Columns of a long row: both ends, the middle, and others anywhere."""
     g = torch.Generator().manual_seed(seed)
     at = torch.cat([torch.randint(0, k, (count,), generator=g), torch.tensor([0, 1, k - 1, k - 2, k // 2])])
     return at.unique()
