@@ -25,7 +25,7 @@ CFG_TIMING = 1
 CFG_SYNC_HOST = 2
 T_DECODE_GATEUP, T_DECODE_DOWN, T_PREFILL_GATEUP, T_PREFILL_DOWN = 0, 1, 2, 3
 HOST_ISA_SCALAR, HOST_ISA_AVX2, HOST_ISA_AVX512F, HOST_ISA_AVX512_BF16 = 0, 1, 2, 3
-DT_BF16, DT_F16, DT_F32 = 0, 1, 2
+DT_BF16, DT_F16, DT_F32, DT_MX4 = 0, 1, 2, 3
 ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_SWIGLU = 0, 1, 2, 3, 4
 HOST_ISA_NAMES = {0: "scalar", 1: "avx2+fma", 2: "avx512f", 3: "avx512-bf16"}
 
@@ -112,6 +112,19 @@ def lib():
             "eff_dispatch_tokens_backward": (I32, [I32, VP, I64, I64, VP, I64, I32, I64, VP, I64, VP]),
             "eff_combine_tokens": (I32, [I32, VP, I64, I64, VP, VP, I64, I32, I64, VP, I64, VP, I64, VP]),
             "eff_combine_tokens_backward": (I32, [I32, VP, I64, VP, I64, I64, VP, VP, I64, I32, I64, VP, I64, VP, VP]),
+            "eff_layer_norm": (I32, [I32, I32, VP, I64, VP, VP, ctypes.c_float, I64, I64, VP, I64, VP, VP, VP]),
+            "eff_layer_norm_backward_workspace": (I64, [I64, I64]),
+            "eff_layer_norm_backward": (I32, [I32, I32, VP, I64, VP, I64, VP, VP, VP, VP, I64, I64, I64, VP, I64, VP, VP, VP,
+                                              ctypes.c_size_t, VP]),
+            "eff_balance_loss_workspace": (I64, [I64, I32]),
+            "eff_balance_loss": (I32, [I32, VP, I64, VP, VP, I64, I32, I32, VP, VP, VP, VP, ctypes.c_size_t, VP]),
+            "eff_balance_loss_backward": (I32, [I32, VP, I64, VP, VP, VP, VP, VP, VP, I64, I32, I32, VP, I64, VP]),
+            "eff_mx4_code_bytes": (I64, [I64]),
+            "eff_mx4_scale_bytes": (I64, [I64]),
+            "eff_mx4_quantize": (I32, [I32, VP, I64, I64, I64, VP, I64, VP, I64, VP]),
+            "eff_mx4_dequantize": (I32, [I32, VP, I64, VP, I64, I64, I64, VP, I64, VP]),
+            "eff_mx4_matmul_workspace": (I64, [VP]),
+            "eff_mx4_matmul": (I32, [VP] * 11 + [ctypes.c_size_t, VP]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -373,5 +386,7 @@ class Engine:
         return out.value
 
 
-from .ops import (combine_tokens, combine_tokens_backward, dispatch_tokens, dispatch_tokens_backward,  # noqa: E402,F401
-                  grouped_matmul, grouped_matmul_backward, matmul, matmul_backward, sort_tokens)
+from .ops import (balance_loss, balance_loss_backward, combine_tokens, combine_tokens_backward,  # noqa: E402,F401
+                  dispatch_tokens, dispatch_tokens_backward, grouped_matmul, grouped_matmul_backward, grouped_mx4_matmul,
+                  layer_norm, layer_norm_backward, matmul, matmul_backward, mx4_dequantize, mx4_matmul, mx4_quantize,
+                  mx4_row_bytes, sort_tokens)

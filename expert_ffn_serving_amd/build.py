@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libeff.so")
 BUILD = os.path.join(HERE, "_build")
 
-HIP_SOURCES = ["k_cache.hip", "k_route.hip", "k_decode.hip", "k_prefill.hip", "k_matmul.hip", "k_tokens.hip"]
+HIP_SOURCES = ["k_cache.hip", "k_route.hip", "k_decode.hip", "k_prefill.hip", "k_matmul.hip", "k_tokens.hip",
+               "k_norm.hip", "k_balance.hip", "k_mx4.hip"]
 CPP_SOURCES = ["engine.cpp", "host_exec.cpp", "ops.cpp"]
 
 ARCH = "gfx950"

@@ -419,4 +419,85 @@ hipError_t launch_combine_tokens(int dtype, const void* ys, int64_t ldys, int64_
 hipError_t launch_combine_tokens_grad(int dtype, const void* dout, int64_t ldd, const void* ys, int64_t ldys, int64_t rows,
                                       const int32_t* pos, const float* w, int64_t T, int K, int64_t H, void* dys,
                                       int64_t lddys, float* dw, hipStream_t s);
+
+// Layer norm (k_norm.hip): rows of dtype, weights of w_dtype (dtype or fp32); w, b, mean, rstd may be null.
+struct NormArgs {
+  const void* x;
+  const void *w, *b;
+  void* y;
+  float *mean, *rstd;
+  int64_t ldx, ldy, T, H;
+  float eps;
+  int dtype, w_dtype;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+
+// dx null: not written.  part: norm_parts(T) rows of 2 H fp32 where dw or db is wanted, else null.
+struct NormGradArgs {
+  const void *dy, *x, *w, *residual;
+  const float *mean, *rstd;
+  void *dx, *dw, *db;
+  float* part;
+  int64_t lddy, ldx, ldr, lddx, T, H;
+  int dtype, w_dtype;
+};
+int64_t norm_parts(int64_t T);
+hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s);
+
+// The router's losses (k_balance.hip).
+struct BalanceArgs {
+  const void* logits;
+  int64_t ld;
+  const int32_t* ids;
+  const uint8_t* mask;  // null: every token
+  int32_t* counts;      // [E + 1], the last: live tokens
+  float *lse, *losses;
+  int64_t T;
+  int K, E, dtype;
+  // of the workspace, set by launch_balance
+  double* total_p;   // [E + 1], the last: sum of lse^2
+  int32_t* done;
+  float* part_p;     // [parts][E + 1]
+  int32_t* part_c;
+};
+int64_t balance_workspace(int64_t T, int E);
+hipError_t launch_balance(BalanceArgs a, void* workspace, hipStream_t s);
+
+struct BalanceGradArgs {
+  const void* logits;
+  int64_t ld;
+  const int32_t *ids, *counts;
+  const float *lse, *dlosses;  // dlosses null: the weights' part alone
+  const float *w, *dw;         // null: the losses' part alone
+  void* dlogits;
+  int64_t ldd, T;
+  int K, E, dtype;
+};
+hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s);
+
+// Microscaled 4-bit rows (k_mx4.hip): codes of units * 64 bytes, scales of units * 4, units = ceil(k / 128).
+struct Mx4Rows {
+  const void* x;   // quantise: from
+  void* y;         // dequantise: to
+  uint8_t *codes, *scales;
+  int64_t ldx, ldy, ldc, lds, rows, k, units;
+  int dtype;
+  const int32_t* offsets;  // not null: only rows offsets[0] .. offsets[groups] - 1
+  int groups;
+  int64_t row0;            // set by the launch
+};
+int64_t mx4_units(int64_t k);
+hipError_t launch_mx4_quantize(const Mx4Rows& a, hipStream_t s);
+hipError_t launch_mx4_dequantize(const Mx4Rows& a, hipStream_t s);
+
+// Products of such rows: e holds the sizes and the epilogue (its operands are not used).
+struct Mx4Args {
+  MmArgs e;
+  const uint8_t *x, *xs, *w, *ws;
+  int64_t ldx, ldxs, ldw, ldws, sw, sws;  // bytes between rows, and between groups
+  int units;
+};
+bool mx4_matmul_fits(const Mx4Args& a);
+int64_t mx4_matmul_workspace(const Mx4Args& a);
+hipError_t launch_mx4_matmul(const Mx4Args& a, void* workspace, hipStream_t s);
 }  // namespace eff

@@ -1,0 +1,473 @@
+// Layer norm of token rows and its gradients.
+//
+// mu = mean x, v = mean (x - mu)^2, r = 1 / sqrt(v + eps), xh = (x - mu) r, y = xh w + b.  With g = dy w:
+// dx = r (g - mean g - xh mean(g xh)) + residual, dw = sum over rows of dy xh, db = sum over rows of dy.
+//
+// A row stays in the registers of TH threads (NV vectors of VEC values each), so it is read once: the mean, then the
+// deviations from it, whose own mean corrects the rounding of the first (a stream whose offset is far above its spread
+// loses nothing).  All statistics and sums are fp32.
+#include <algorithm>
+#include <type_traits>
+
+#include "eff_internal.h"
+
+namespace eff {
+namespace {
+
+typedef _Float16 f16_t;
+typedef __bf16 bf16_t;
+
+template <typename T, int VEC>
+struct NormVec {
+  typedef T V __attribute__((ext_vector_type(VEC)));
+};
+template <typename T>
+struct NormVec<T, 1> {
+  typedef T V;
+};
+template <typename T, int VEC>
+__device__ inline void norm_widen(const typename NormVec<T, VEC>::V& v, float* o) {
+  if constexpr (VEC == 1) {
+    o[0] = (float)v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) o[i] = (float)v[i];
+  }
+}
+template <typename T, int VEC>
+__device__ inline typename NormVec<T, VEC>::V norm_load(const void* p, int64_t i) {
+  return *reinterpret_cast<const typename NormVec<T, VEC>::V*>(reinterpret_cast<const T*>(p) + i);
+}
+// VEC values of another type than the rows' (weights): as many 16-byte accesses as they take
+template <typename T, int VEC>
+__device__ inline void norm_get(const void* p, int64_t i, float* o) {
+  constexpr int C = VEC * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : VEC;
+#pragma unroll
+  for (int c = 0; c < VEC; c += C) norm_widen<T, C>(norm_load<T, C>(p, i + c), o + c);
+}
+template <typename T, int VEC>
+__device__ inline void norm_store(void* p, int64_t i, const float* v) {
+  typename NormVec<T, VEC>::V o;
+  if constexpr (VEC == 1) {
+    o = (T)v[0];
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = (T)v[e];
+  }
+  *reinterpret_cast<typename NormVec<T, VEC>::V*>(reinterpret_cast<T*>(p) + i) = o;
+}
+
+// sums of N values over the TH threads of a row (TH = 64: the wave; else the wave's sums meet in LDS, s: [TH / 64][N],
+// in wave order).  Every thread of the workgroup takes part.
+template <int TH, int N>
+__device__ inline void row_sum(float* v, float* s) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o);
+  if constexpr (TH > 64) {
+    const int wave = (threadIdx.x % TH) >> 6;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[wave * N + i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = s[i];
+#pragma unroll
+    for (int w = 1; w < TH / 64; ++w)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += s[w * N + i];
+  }
+}
+
+// grid: ceil(T / R) workgroups of R rows, TH threads each
+template <typename T, typename W, int VEC, int TH, int NV, int R>
+__global__ void __launch_bounds__(TH * R)
+k_norm(NormArgs a) {
+  __shared__ float s_sum[R][2][TH / 64 * 2];
+  const int sub = threadIdx.x / TH, tid = threadIdx.x % TH;
+  const int64_t row = (int64_t)blockIdx.x * R + sub;
+  const bool live = row < a.T;
+  const T* x = reinterpret_cast<const T*>(a.x) + (live ? row : a.T - 1) * a.ldx;
+  const float inv = 1.0f / (float)a.H;
+  typename NormVec<T, VEC>::V raw[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t h = (int64_t)(i * TH + tid) * VEC;
+    if (h < a.H) raw[i] = norm_load<T, VEC>(x, h);
+  }
+  float v[NV][VEC], sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if ((int64_t)(i * TH + tid) * VEC < a.H) {
+      norm_widen<T, VEC>(raw[i], v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) sum[0] += v[i][e];
+  }
+  row_sum<TH, 1>(sum, s_sum[sub][0]);
+  const float first = sum[0] * inv;
+  float dev[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if ((int64_t)(i * TH + tid) * VEC < a.H) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        v[i][e] -= first;
+        dev[0] += v[i][e];
+        dev[1] = fmaf(v[i][e], v[i][e], dev[1]);
+      }
+    }
+  row_sum<TH, 2>(dev, s_sum[sub][1]);
+  const float more = dev[0] * inv;
+  const float rstd = 1.0f / sqrtf(fmaxf(dev[1] * inv - more * more, 0.f) + a.eps + 0.f * dev[1]);
+  if (!live) return;
+  if (tid == 0) {
+    if (a.mean) a.mean[row] = first + more;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t h = (int64_t)(i * TH + tid) * VEC;
+    if (h >= a.H) continue;
+    float w[VEC], b[VEC];
+    if (a.w) norm_get<W, VEC>(a.w, h, w);
+    if (a.b) norm_get<W, VEC>(a.b, h, b);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      float y = (v[i][e] - more) * rstd;
+      if (a.w) y *= w[e];
+      if (a.b) y += b[e];
+      v[i][e] = y;
+    }
+    norm_store<T, VEC>(a.y, row * a.ldy + h, v[i]);
+  }
+}
+
+// Rows longer than the registers hold: a workgroup of 1024 threads reads its row three times (the second and third
+// from the caches).  grid: T.
+constexpr int kLongThreads = 1024;
+
+template <typename T, typename W>
+__global__ void __launch_bounds__(kLongThreads)
+k_norm_long(NormArgs a) {
+  __shared__ float s_sum[2][kLongThreads / 64 * 2];
+  const int64_t row = blockIdx.x;
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
+  const float inv = 1.0f / (float)a.H;
+  float sum[2] = {0.f, 0.f}, dev[2] = {0.f, 0.f};
+  for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) sum[0] += (float)x[h];
+  row_sum<kLongThreads, 1>(sum, s_sum[0]);
+  const float first = sum[0] * inv;
+  for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) {
+    const float d = (float)x[h] - first;
+    dev[0] += d;
+    dev[1] = fmaf(d, d, dev[1]);
+  }
+  row_sum<kLongThreads, 2>(dev, s_sum[1]);
+  const float more = dev[0] * inv;
+  const float rstd = 1.0f / sqrtf(fmaxf(dev[1] * inv - more * more, 0.f) + a.eps + 0.f * dev[1]);
+  if (threadIdx.x == 0) {
+    if (a.mean) a.mean[row] = first + more;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+  for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) {
+    float y = ((float)x[h] - first - more) * rstd;
+    if (a.w) y *= (float)reinterpret_cast<const W*>(a.w)[h];
+    if (a.b) y += (float)reinterpret_cast<const W*>(a.b)[h];
+    reinterpret_cast<T*>(a.y)[row * a.ldy + h] = (T)y;
+  }
+}
+
+// ---- gradients -------------------------------------------------------------------------------------------
+
+// grid: parts workgroups, workgroup p takes rows p R + sub, then parts R further.  dx as rows go by; the columns' sums of
+// dy xh and dy stay in the registers of the thread that owns the column, are added over the workgroup's R rows in LDS and
+// written as one row of partial sums [parts][2][H], which k_norm_join adds in order.
+template <typename T, typename W, int VEC, int TH, int NV, int R>
+__global__ void __launch_bounds__(TH * R)
+k_norm_grad(NormGradArgs a) {
+  __shared__ float s_sum[R][2][TH / 64 * 2];
+  extern __shared__ float s_col[];  // [TH * VEC] per vector slot, R > 1
+  const int sub = threadIdx.x / TH, tid = threadIdx.x % TH;
+  const float inv = 1.0f / (float)a.H;
+  const bool cols = a.part != nullptr;
+  float w[NV][VEC], sw[NV][VEC], sb[NV][VEC];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int64_t h = (int64_t)(i * TH + tid) * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) w[i][e] = 1.f, sw[i][e] = sb[i][e] = 0.f;
+    if (a.w && h < a.H) norm_get<W, VEC>(a.w, h, w[i]);
+  }
+  int phase = 0;
+  const int64_t step = (int64_t)gridDim.x * R;
+  for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.T; r0 += step, phase ^= 1) {
+    const int64_t row = r0 + sub;
+    const bool live = row < a.T;
+    float xh[NV][VEC], g[NV][VEC], sum[2] = {0.f, 0.f};
+    const float mean = live ? a.mean[row] : 0.f, rstd = live ? a.rstd[row] : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t h = (int64_t)(i * TH + tid) * VEC;
+      if (live && h < a.H) {
+        norm_widen<T, VEC>(norm_load<T, VEC>(a.x, row * a.ldx + h), xh[i]);
+        norm_widen<T, VEC>(norm_load<T, VEC>(a.dy, row * a.lddy + h), g[i]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          xh[i][e] = (xh[i][e] - mean) * rstd;
+          if (cols) {
+            sw[i][e] = fmaf(g[i][e], xh[i][e], sw[i][e]);
+            sb[i][e] += g[i][e];
+          }
+          g[i][e] *= w[i][e];
+          sum[0] += g[i][e];
+          sum[1] = fmaf(g[i][e], xh[i][e], sum[1]);
+        }
+      }
+    }
+    if (!a.dx) continue;
+    row_sum<TH, 2>(sum, s_sum[sub][phase]);  // two buffers: one barrier a row keeps them apart
+    const float c1 = sum[0] * inv, c2 = sum[1] * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t h = (int64_t)(i * TH + tid) * VEC;
+      if (!live || h >= a.H) continue;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[i][e] = rstd * (g[i][e] - c1 - xh[i][e] * c2);
+      if (a.residual) {
+        float r[VEC];
+        norm_widen<T, VEC>(norm_load<T, VEC>(a.residual, row * a.ldr + h), r);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) g[i][e] += r[e];
+      }
+      norm_store<T, VEC>(a.dx, row * a.lddx + h, g[i]);
+    }
+  }
+  if (!cols) return;
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.H;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t h = (int64_t)(i * TH + tid) * VEC;
+      if constexpr (R > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s_col[(sub * VEC + e) * TH + tid] = k ? sb[i][e] : sw[i][e];
+        __syncthreads();
+        if (sub == 0 && h < a.H) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            float v = s_col[e * TH + tid];
+#pragma unroll
+            for (int r = 1; r < R; ++r) v += s_col[(r * VEC + e) * TH + tid];
+            part[k * a.H + h + e] = v;
+          }
+        }
+      } else if (h < a.H) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) part[k * a.H + h + e] = k ? sb[i][e] : sw[i][e];
+      }
+    }
+}
+
+// dx of rows longer than the registers hold, grid: T
+template <typename T, typename W>
+__global__ void __launch_bounds__(kLongThreads)
+k_norm_grad_long(NormGradArgs a) {
+  __shared__ float s_sum[kLongThreads / 64 * 2];
+  const int64_t row = blockIdx.x;
+  const T *x = reinterpret_cast<const T*>(a.x) + row * a.ldx, *dy = reinterpret_cast<const T*>(a.dy) + row * a.lddy;
+  const W* w = reinterpret_cast<const W*>(a.w);
+  const float mean = a.mean[row], rstd = a.rstd[row], inv = 1.0f / (float)a.H;
+  float sum[2] = {0.f, 0.f};
+  for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) {
+    const float g = w ? (float)dy[h] * (float)w[h] : (float)dy[h];
+    sum[0] += g;
+    sum[1] = fmaf(g, ((float)x[h] - mean) * rstd, sum[1]);
+  }
+  row_sum<kLongThreads, 2>(sum, s_sum);
+  const float c1 = sum[0] * inv, c2 = sum[1] * inv;
+  for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) {
+    const float g = w ? (float)dy[h] * (float)w[h] : (float)dy[h];
+    float d = rstd * (g - c1 - ((float)x[h] - mean) * rstd * c2);
+    if (a.residual) d += (float)reinterpret_cast<const T*>(a.residual)[row * a.ldr + h];
+    reinterpret_cast<T*>(a.dx)[row * a.lddx + h] = (T)d;
+  }
+}
+
+// the columns' sums of such rows over part p's rows, grid: (ceil(H / 256), parts)
+template <typename T>
+__global__ void __launch_bounds__(256)
+k_norm_cols_long(NormGradArgs a) {
+  const int64_t h = (int64_t)blockIdx.x * 256 + threadIdx.x, per = (a.T + gridDim.y - 1) / gridDim.y;
+  if (h >= a.H) return;
+  const int64_t r1 = min(a.T, (blockIdx.y + 1) * per);
+  float sw = 0.f, sb = 0.f;
+  for (int64_t r = blockIdx.y * per; r < r1; ++r) {
+    const float d = (float)reinterpret_cast<const T*>(a.dy)[r * a.lddy + h];
+    sw = fmaf(d, ((float)reinterpret_cast<const T*>(a.x)[r * a.ldx + h] - a.mean[r]) * a.rstd[r], sw);
+    sb += d;
+  }
+  float* part = a.part + (int64_t)blockIdx.y * 2 * a.H;
+  part[h] = sw;
+  part[a.H + h] = sb;
+}
+
+// grid: (ceil(H / 64), 2).  The partial sums of 64 columns of dw (y = 0) or db: 16 waves take every 16th part, their sums
+// are added in wave order.
+template <typename W>
+__global__ void __launch_bounds__(1024)
+k_norm_join(const float* __restrict__ part, int64_t parts, int64_t H, void* dw, void* db) {
+  __shared__ float s_sum[16][64];
+  W* out = reinterpret_cast<W*>(blockIdx.y ? db : dw);
+  if (!out) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t h = (int64_t)blockIdx.x * 64 + lane;
+  const float* p = part + blockIdx.y * H + h;
+  float sum = 0.f;
+  if (h < H) {
+#pragma unroll 8
+    for (int64_t i = wave; i < parts; i += 16) sum += p[i * 2 * H];
+  }
+  s_sum[wave][lane] = sum;
+  __syncthreads();
+  if (wave || h >= H) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) sum += s_sum[i][lane];
+  out[h] = (W)sum;
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool whole_vectors(int bytes, int64_t H, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
+  if (H * bytes % 16) return false;
+  for (const void* p : ptrs)
+    if ((uintptr_t)p % 16) return false;
+  for (int64_t l : lds)
+    if (l * bytes % 16) return false;
+  return true;
+}
+
+template <int TH, int NV, int R>
+struct NormShape {
+  static constexpr int th = TH, nv = NV, r = R;
+};
+
+// calls f with the shape for rows of n vectors, or g where the registers hold no such row
+template <bool VECTORS, typename F, typename G>
+void with_shape(int64_t n, F f, G g) {
+  if constexpr (VECTORS) {
+    if (n <= 64) f(NormShape<64, 1, 4>{});
+    else if (n <= 128) f(NormShape<64, 2, 4>{});
+    else if (n <= 256) f(NormShape<256, 1, 2>{});
+    else if (n <= 512) f(NormShape<256, 2, 2>{});
+    else if (n <= 1024) f(NormShape<256, 4, 2>{});
+    else if (n <= 2048) f(NormShape<1024, 2, 1>{});
+    else g();
+  } else {
+    if (n <= 256) f(NormShape<64, 4, 4>{});
+    else if (n <= 1024) f(NormShape<256, 4, 2>{});
+    else if (n <= 4096) f(NormShape<256, 16, 2>{});
+    else if (n <= 16384) f(NormShape<1024, 16, 1>{});
+    else g();
+  }
+}
+
+// calls f with the rows' and the weights' types
+template <typename F>
+void with_types(int dtype, int w_dtype, F f) {
+  const bool same = dtype == w_dtype;
+  if (dtype == EFF_DT_BF16) same ? f(bf16_t{}, bf16_t{}) : f(bf16_t{}, float{});
+  else if (dtype == EFF_DT_F16) same ? f(f16_t{}, f16_t{}) : f(f16_t{}, float{});
+  else f(float{}, float{});
+}
+
+constexpr int64_t kNormGrid = 1 << 22;  // workgroups of up to 1024 threads: a grid's threads stay below 2^32
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+  const int b = a.dtype == EFF_DT_F32 ? 4 : 2;
+  // the weights' vectors are no larger than 16 bytes: 16-byte aligned is enough
+  const bool vec = whole_vectors(b, a.H, {a.x, a.y, a.w, a.b}, {a.ldx, a.ldy});
+  with_types(a.dtype, a.w_dtype, [&](auto t, auto wt) {
+    typedef decltype(t) T;
+    typedef decltype(wt) W;
+    constexpr int VEC = 16 / (int)sizeof(T);
+    auto rows = [&](auto launch, int64_t per) {  // per: rows of a workgroup
+      for (int64_t t0 = 0; t0 < a.T; t0 += kNormGrid * per) {
+        NormArgs p = a;
+        p.T = std::min(kNormGrid * per, a.T - t0);
+        p.x = reinterpret_cast<const T*>(a.x) + t0 * a.ldx;
+        p.y = reinterpret_cast<T*>(a.y) + t0 * a.ldy;
+        if (a.mean) p.mean = a.mean + t0;
+        if (a.rstd) p.rstd = a.rstd + t0;
+        launch(p, dim3((unsigned)cdiv(p.T, per)));
+      }
+    };
+    auto lengthy = [&] {
+      rows([&](const NormArgs& p, dim3 g) { hipLaunchKernelGGL((k_norm_long<T, W>), g, dim3(kLongThreads), 0, s, p); }, 1);
+    };
+    if (vec)
+      with_shape<true>(a.H / VEC, [&](auto sh) {
+        typedef decltype(sh) S;
+        rows([&](const NormArgs& p, dim3 g) { hipLaunchKernelGGL((k_norm<T, W, VEC, S::th, S::nv, S::r>), g, dim3(S::th * S::r), 0, s, p); }, S::r);
+      }, lengthy);
+    else
+      with_shape<false>(a.H, [&](auto sh) {
+        typedef decltype(sh) S;
+        rows([&](const NormArgs& p, dim3 g) { hipLaunchKernelGGL((k_norm<T, W, 1, S::th, S::nv, S::r>), g, dim3(S::th * S::r), 0, s, p); }, S::r);
+      }, lengthy);
+  });
+  return hipGetLastError();
+}
+
+// Parts of the columns' sums: as many as there are rows, up to 512.
+int64_t norm_parts(int64_t T) { return std::min<int64_t>(T, 512); }
+
+hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
+  const int b = a.dtype == EFF_DT_F32 ? 4 : 2;
+  const bool vec = whole_vectors(b, a.H, {a.x, a.dy, a.dx, a.w, a.residual}, {a.ldx, a.lddy, a.dx ? a.lddx : 0, a.residual ? a.ldr : 0});
+  const int64_t parts = norm_parts(a.T);
+  with_types(a.dtype, a.w_dtype, [&](auto t, auto wt) {
+    typedef decltype(t) T;
+    typedef decltype(wt) W;
+    constexpr int VEC = 16 / (int)sizeof(T);
+    int64_t written = parts;  // rows of partial sums that the pass writes
+    auto lengthy = [&] {
+      for (int64_t t0 = 0; a.dx && t0 < a.T; t0 += kNormGrid) {
+        NormGradArgs p = a;
+        p.T = std::min(kNormGrid, a.T - t0);
+        p.x = reinterpret_cast<const T*>(a.x) + t0 * a.ldx;
+        p.dy = reinterpret_cast<const T*>(a.dy) + t0 * a.lddy;
+        if (a.residual) p.residual = reinterpret_cast<const T*>(a.residual) + t0 * a.ldr;
+        p.mean = a.mean + t0, p.rstd = a.rstd + t0, p.dx = reinterpret_cast<T*>(a.dx) + t0 * a.lddx;
+        hipLaunchKernelGGL((k_norm_grad_long<T, W>), dim3((unsigned)p.T), dim3(kLongThreads), 0, s, p);
+      }
+      if (a.part) hipLaunchKernelGGL((k_norm_cols_long<T>), dim3((unsigned)cdiv(a.H, 256), (unsigned)parts), dim3(256), 0, s, a);
+    };
+    auto go = [&](auto sh, auto vecs) {
+      typedef decltype(sh) S;
+      constexpr int V = decltype(vecs)::value;
+      const int64_t grid = std::min(parts, cdiv(a.T, S::r));
+      written = grid;
+      const int lds = S::r > 1 ? S::r * S::th * V * 4 : 0;
+      hipLaunchKernelGGL((k_norm_grad<T, W, V, S::th, S::nv, S::r>), dim3((unsigned)grid), dim3(S::th * S::r), lds, s, a);
+    };
+    if (a.T > 0) {
+      if (vec) with_shape<true>(a.H / VEC, [&](auto sh) { go(sh, std::integral_constant<int, VEC>{}); }, lengthy);
+      else with_shape<false>(a.H, [&](auto sh) { go(sh, std::integral_constant<int, 1>{}); }, lengthy);
+    }
+    if (a.dw || a.db)
+      hipLaunchKernelGGL((k_norm_join<W>), dim3((unsigned)cdiv(a.H, 64), 2), dim3(1024), 0, s, a.part, a.T > 0 ? written : 0, a.H, a.dw, a.db);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace eff

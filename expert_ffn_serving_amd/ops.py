@@ -1,5 +1,6 @@
 """Operators around the routed-expert step that need no engine: dense products with their epilogue, the
-experts' products on sorted rows, tokens sorted by expert and back, and the gradients of all of them.
+experts' products on sorted rows, tokens sorted by expert and back, layer norm and the router's losses, the gradients
+of all of them, and microscaled 4-bit rows with their products.
 
 Every call enqueues on `stream` (a torch.cuda.Stream, a handle, or None for the current stream of the
 tensors' device), writes the outputs it is given and keeps nothing.  Matrices need unit stride inside a row;
@@ -285,13 +286,13 @@ def _rows_of(name, t):
     return shape
 
 
-def _pos(pos, T, dev):
+def _pos(pos, T, dev, name="pos"):
     shape = pos.shape
     if len(shape) != 2 or shape[0] != T:
-        _bad("pos must be [T,K] with T = %d" % T)
+        _bad("%s must be [T,K] with T = %d" % (name, T))
     if shape[1] > _MAX_TOPK:
-        _bad("pos has more than %d places a token" % _MAX_TOPK)
-    return _dense("pos", pos, _I32, shape, dev), shape[1]
+        _bad("%s has more than %d places a token" % (name, _MAX_TOPK))
+    return _dense(name, pos, _I32, shape, dev), shape[1]
 
 
 def dispatch_tokens(x, pos, xs, stream=None):
@@ -361,3 +362,248 @@ def combine_tokens_backward(dout, ys, pos, w, dys, dw=None, stream=None):
         _written((dys,) if dw is None else (dys, dw))
     except AttributeError as e:
         _no_tensor(e)
+
+# ---- layer norm, the router's losses -----------------------------------------------------------------------
+
+def _norm_weight(w, x_dtype):
+    """The EFF_DT_* of weights: x's type or float32."""
+    t = w.dtype
+    if t is not x_dtype and t is not _F32:
+        _bad("weights must be of x's type or float32, got %s" % t)
+    return t
+
+
+def layer_norm(x, y, weight=None, bias=None, eps=1e-5, mean=None, rstd=None, stream=None):
+    """eff_layer_norm: y = (x - mean) * rstd * weight + bias over each row of x [T,H] (bfloat16, float16 or float32), y of
+    x's type and shape, written.  weight and bias [H], both of x's type or both float32.  mean and rstd, float32 [T], are
+    written if given: the statistics, for layer_norm_backward."""
+    try:
+        dev = _device("x", x)
+        T, H = _rows_of("x", x)
+        dt = x.dtype
+        if not isinstance(eps, (int, float)):
+            _bad("eps must be a number")
+        wt = _norm_weight(weight if weight is not None else bias if bias is not None else x, dt)
+        px, ldx = _matrix("x", x, dt, T, H, dev)
+        py, ldy = _matrix("y", y, dt, T, H, dev, True)
+        pw = _dense("weight", weight, wt, (H,), dev) if weight is not None else None
+        pb = _dense("bias", bias, wt, (H,), dev) if bias is not None else None
+        pm = _dense("mean", mean, _F32, (T,), dev) if mean is not None else None
+        pr = _dense("rstd", rstd, _F32, (T,), dev) if rstd is not None else None
+        _call(lib().eff_layer_norm, dev, stream, (_DT[dt], _DT[wt], px, ldx, pw, pb, eps, T, H, py, ldy, pm, pr))
+        _written([t for t in (y, mean, rstd) if t is not None])
+    except AttributeError as e:
+        _no_tensor(e)
+
+
+def layer_norm_backward(dy, x, mean, rstd, dx=None, dw=None, db=None, weight=None, residual=None, stream=None):
+    """eff_layer_norm_backward: from dy [T,H], the forward's x and weight and the mean and rstd that it saved, writes the
+    gradients that are given: dx [T,H] (x's type), dw and db [H] (the weight's type, or x's or float32 without one).
+    residual [T,H] is added to dx: the gradient that reaches x past the norm."""
+    try:
+        dev = _device("x", x)
+        T, H = _rows_of("x", x)
+        dt = x.dtype
+        wt = _norm_weight(next((t for t in (weight, dw, db) if t is not None), x), dt)
+        pdy, lddy = _matrix("dy", dy, dt, T, H, dev)
+        px, ldx = _matrix("x", x, dt, T, H, dev)
+        pm, pr = _dense("mean", mean, _F32, (T,), dev), _dense("rstd", rstd, _F32, (T,), dev)
+        pw = _dense("weight", weight, wt, (H,), dev) if weight is not None else None
+        pres, ldr = _matrix("residual", residual, dt, T, H, dev) if residual is not None else (None, 0)
+        pdx, lddx = _matrix("dx", dx, dt, T, H, dev, True) if dx is not None else (None, 0)
+        pdw = _dense("dw", dw, wt, (H,), dev) if dw is not None else None
+        pdb = _dense("db", db, wt, (H,), dev) if db is not None else None
+        L = lib()
+        need = L.eff_layer_norm_backward_workspace(T, H) if dw is not None or db is not None else 0
+        _call(L.eff_layer_norm_backward, dev, stream,
+              (_DT[dt], _DT[wt], pdy, lddy, px, ldx, pw, pm, pr, pres, ldr, T, H, pdx, lddx, pdw, pdb), need)
+        _written([t for t in (dx, dw, db) if t is not None])
+    except AttributeError as e:
+        _no_tensor(e)
+
+
+def _router(logits, ids, dev):
+    """(T, E, K) of a router's logits [T,E] and ids [T,K]."""
+    T, E = _rows_of("logits", logits)
+    if not 1 <= E <= _MAX_GROUPS:
+        _bad("logits must have 1 to %d columns" % _MAX_GROUPS)
+    return (T, E) + _pos(ids, T, dev, "ids")
+
+
+def balance_loss(logits, ids, counts, lse, losses, mask=None, stream=None):
+    """eff_balance_loss: the router's losses over tokens with logits [T,E] (float32, bfloat16 or float16) and ids int32
+    [T,K] as route writes them.  Writes losses, float32 [2]: E * sum of f * P (1 for an even load), and the mean of lse^2;
+    counts, int32 [E+1]: the pairs of every expert, then the live tokens; lse, float32 [T], for balance_loss_backward.
+    mask, bool [T]: tokens that count (padding is not read); a token without a logit above -infinity does not count."""
+    try:
+        dev = _device("logits", logits)
+        T, E, pi, K = _router(logits, ids, dev)
+        pl, ld = _matrix("logits", logits, logits.dtype, T, E, dev)
+        pc, ps = _dense("counts", counts, _I32, (E + 1,), dev), _dense("lse", lse, _F32, (T,), dev)
+        po = _dense("losses", losses, _F32, (2,), dev)
+        pm = _dense("mask", mask, torch.bool, (T,), dev) if mask is not None else None
+        L = lib()
+        _call(L.eff_balance_loss, dev, stream, (_DT[logits.dtype], pl, ld, pi, pm, T, K, E, pc, ps, po),
+              L.eff_balance_loss_workspace(T, E))
+        _written((counts, lse, losses))
+    except AttributeError as e:
+        _no_tensor(e)
+
+
+def balance_loss_backward(logits, ids, counts, lse, dlosses, dlogits, w=None, dw=None, stream=None):
+    """eff_balance_loss_backward: dlogits [T,E] (the logits' type), written: the gradient of dlosses[0] * losses[0] +
+    dlosses[1] * losses[1] (dlosses float32 [2], or None) and, with w and dw (float32 [T,K]), of routing weights w =
+    softmax over the selected logits with gradient dw, as combine_tokens_backward writes it."""
+    try:
+        dev = _device("logits", logits)
+        T, E, pi, K = _router(logits, ids, dev)
+        dt = logits.dtype
+        pl, ld = _matrix("logits", logits, dt, T, E, dev)
+        pd, ldd = _matrix("dlogits", dlogits, dt, T, E, dev, True)
+        pc, ps = _dense("counts", counts, _I32, (E + 1,), dev), _dense("lse", lse, _F32, (T,), dev)
+        pg = _dense("dlosses", dlosses, _F32, (2,), dev) if dlosses is not None else None
+        if (w is None) != (dw is None):
+            _bad("w and dw go together")
+        pw = _dense("w", w, _F32, (T, K), dev) if w is not None else None
+        pdw = _dense("dw", dw, _F32, (T, K), dev) if dw is not None else None
+        _call(lib().eff_balance_loss_backward, dev, stream, (_DT[dt], pl, ld, pi, pc, ps, pg, pw, pdw, T, K, E, pd, ldd))
+        _written((dlogits,))
+    except AttributeError as e:
+        _no_tensor(e)
+
+
+# ---- microscaled 4-bit rows and their products -------------------------------------------------------------
+
+_U8 = torch.uint8
+
+
+class Mx4Desc(ctypes.Structure):
+    """eff_mx4_desc"""
+    _fields_ = [(n, ctypes.c_int32) for n in ("x_dtype", "dtype", "out_dtype", "act", "groups", "reserved")] + [
+        (n, ctypes.c_int64) for n in ("m", "n", "k", "ld_x", "ld_xs", "ld_w", "ld_ws", "stride_w", "stride_ws", "ld_y",
+                                      "ld_residual", "ld_pre")]
+
+
+_pack_mx4 = struct.Struct("=6i12q").pack
+
+
+def mx4_row_bytes(k):
+    """Bytes of codes and of scales of a row of k values."""
+    units = (k + 127) // 128
+    return units * 64, units * 4
+
+
+def _flat_rows(name, t):
+    """A matrix, or a stack of them as one matrix."""
+    if t.dim() == 3:
+        try:
+            return t.view(-1, t.shape[2])
+        except RuntimeError:
+            _bad("%s must have one distance between all rows" % name)
+    return t
+
+
+def mx4_quantize(x, codes, scales, stream=None):
+    """eff_mx4_quantize: x [m,k] or [E,n,k] (bfloat16, float16 or float32) to microscaled 4-bit rows: codes and scales,
+    uint8, of x's leading sizes and mx4_row_bytes(k) bytes a row, written.  Rows of codes begin at multiples of 16 bytes."""
+    try:
+        dev = _device("x", x)
+        if x.shape[:-1] != codes.shape[:-1] or x.shape[:-1] != scales.shape[:-1]:
+            _bad("codes and scales must have x's leading sizes")
+        x2 = _flat_rows("x", x)
+        m, k = _rows_of("x", x2)
+        cb, sb = mx4_row_bytes(k)
+        px, ldx = _matrix("x", x2, x.dtype, m, k, dev)
+        pc, ldc = _matrix("codes", _flat_rows("codes", codes), _U8, m, cb, dev, True)
+        ps, lds = _matrix("scales", _flat_rows("scales", scales), _U8, m, sb, dev, True)
+        _call(lib().eff_mx4_quantize, dev, stream, (_DT[x.dtype], px, ldx, m, k, pc, ldc, ps, lds))
+        _written((codes, scales))
+    except AttributeError as e:
+        _no_tensor(e)
+
+
+def mx4_dequantize(codes, scales, y, stream=None):
+    """eff_mx4_dequantize: what codes and scales stand for, into y [m,k] or [E,n,k] (bfloat16, float16 or float32)."""
+    try:
+        dev = _device("y", y)
+        if y.shape[:-1] != codes.shape[:-1] or y.shape[:-1] != scales.shape[:-1]:
+            _bad("codes and scales must have y's leading sizes")
+        y2 = _flat_rows("y", y)
+        m, k = _rows_of("y", y2)
+        cb, sb = mx4_row_bytes(k)
+        py, ldy = _matrix("y", y2, y.dtype, m, k, dev, True)
+        pc, ldc = _matrix("codes", _flat_rows("codes", codes), _U8, m, cb, dev)
+        ps, lds = _matrix("scales", _flat_rows("scales", scales), _U8, m, sb, dev)
+        _call(lib().eff_mx4_dequantize, dev, stream, (_DT[y.dtype], pc, ldc, ps, lds, m, k, py, ldy))
+        _written((y,))
+    except AttributeError as e:
+        _no_tensor(e)
+
+
+def _mx4(x, w, w_scales, offsets, y, x_scales, bias, act, residual, pre, stream):
+    try:
+        dev = _device("x", x)
+        coded = x.dtype is _U8
+        grouped = offsets is not None
+        if coded:
+            # the values' type is that of what the epilogue reads and writes; y alone may be float32
+            dt = next((t.dtype for t in (bias, residual, pre, y) if t is not None and t.dtype is not _F32), torch.bfloat16)
+        else:
+            dt = x.dtype
+        if dt not in _HALF:
+            _bad("x must be bfloat16, float16 or codes (uint8), the other tensors of one 16-bit type")
+        if coded != (x_scales is not None):
+            _bad("x_scales go with codes")
+        ws = w.shape
+        if len(x.shape) != 2 or len(ws) != (3 if grouped else 2):
+            _bad("x must be a matrix and w %s" % ("[E,n,bytes]" if grouped else "[n,bytes]"))
+        m, nw, groups = x.shape[0], ws[-2], ws[0] if grouped else 0
+        k = 2 * x.shape[1] if coded else x.shape[1]
+        cb, sb = mx4_row_bytes(k)
+        if act == ACT_SWIGLU and nw % 2:
+            _bad("w needs an even number of rows (gate, then up) with ACT_SWIGLU")
+        if not (act == ACT_NONE or act in (1, 2, 3, ACT_SWIGLU)):
+            _bad("unknown activation %r" % (act,))
+        n = nw // 2 if act == ACT_SWIGLU else nw
+        yt = _out_type("y", y, dt)
+        px, ldx = _matrix("x", x, x.dtype, m, cb if coded else k, dev)
+        pxs, ldxs = _matrix("x_scales", x_scales, _U8, m, sb, dev) if coded else (None, 0)
+        po, sw, sws = None, 0, 0
+        if grouped:
+            if not 1 <= groups <= _MAX_GROUPS:
+                _bad("w needs 1 to %d groups" % _MAX_GROUPS)
+            pw, ldw, sw = _stack("w", w, _U8, groups, nw, cb, dev)
+            pws, ldws, sws = _stack("w_scales", w_scales, _U8, groups, nw, sb, dev)
+            po = _dense("offsets", offsets, _I32, (groups + 1,), dev)
+        else:
+            pw, ldw = _matrix("w", w, _U8, nw, cb, dev)
+            pws, ldws = _matrix("w_scales", w_scales, _U8, nw, sb, dev)
+        py, ldy = _matrix("y", y, yt, m, n, dev, True)
+        pb = _dense("bias", bias, dt, (groups, nw) if grouped else (nw,), dev) if bias is not None else None
+        pr, ldr = _matrix("residual", residual, dt, m, n, dev) if residual is not None else (None, 0)
+        pp, ldp = _matrix("pre", pre, dt, m, nw, dev, True) if pre is not None else (None, nw)
+        d = _pack_mx4(3 if coded else _HALF[dt], _HALF[dt], _DT[yt], act, groups, 0, m, n, k, ldx, ldxs, ldw, ldws, sw, sws,
+                      ldy, ldr, ldp)
+        L = lib()
+        _call(L.eff_mx4_matmul, dev, stream, (d, px, pxs, pw, pws, pb, pr, po, py, pp), L.eff_mx4_matmul_workspace(d))
+        _written((y,) if pre is None else (y, pre))
+    except AttributeError as e:
+        _no_tensor(e)
+    except struct.error as e:
+        _bad("act or a size is not an integer that the description holds (%s)" % e)
+
+
+def mx4_matmul(x, w, w_scales, y, x_scales=None, bias=None, act=ACT_NONE, residual=None, pre=None, stream=None):
+    """eff_mx4_matmul: y = act(x @ w.T + bias) + residual of microscaled 4-bit operands.  w and w_scales: the codes and scales
+    of [n,k] ([2n,k] with ACT_SWIGLU) as mx4_quantize writes them; x: bfloat16 or float16 [m,k], quantised by the call in
+    the same way, or codes with x_scales.  The rest as for matmul.  Gradients: matmul_backward on the dequantised operands
+    (straight through the rounding)."""
+    _mx4(x, w, w_scales, None, y, x_scales, bias, act, residual, pre, stream)
+
+
+def grouped_mx4_matmul(x, w, w_scales, offsets, y, x_scales=None, bias=None, act=ACT_NONE, residual=None, pre=None, stream=None):
+    """eff_mx4_matmul with groups: rows offsets[e]..offsets[e+1]-1 of x with w[e], as grouped_matmul.  Rows in no group are
+    not read and their rows of y and pre stay as they were."""
+    if offsets is None:
+        _bad("offsets are needed")
+    _mx4(x, w, w_scales, offsets, y, x_scales, bias, act, residual, pre, stream)

@@ -468,6 +468,87 @@ int eff_combine_tokens_backward(int dtype, const void* dout, int64_t ld_dout, co
                                 int64_t rows, const int32_t* pos, const float* w, int64_t T, int K, int64_t H,
                                 void* dys, int64_t ld_dys, float* dw, eff_stream_t stream);
 
+/* ---- Operators of a block around its router and its experts: layer norm, the router's losses, 4-bit rows and their
+ * products.  No engine; the rules of the operators above hold here too. */
+
+/* Layer norm of T rows: y = (x - mean) rstd w + b, mean and 1 / sqrt(variance + eps) of each row of H values in fp32.
+ * dtype: EFF_DT_* of x and y; w_dtype: of w and b [H], dtype or EFF_DT_F32; w, b, mean and rstd may be NULL (1, 0, not
+ * written).  mean and rstd fp32 [T]. */
+int eff_layer_norm(int dtype, int w_dtype, const void* x, int64_t ld_x, const void* w, const void* b, float eps, int64_t T,
+                   int64_t H, void* y, int64_t ld_y, float* mean, float* rstd, eff_stream_t stream);
+
+/* Its gradients from dy (dtype), x, w and the saved mean and rstd, with xh = (x - mean) rstd and g = dy w:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)) + residual;   dw = sum over rows of dy xh;   db = sum over rows of dy.
+ * residual (NULL: none; ld_residual 0: one row for all): the gradient that reaches x past the norm, as by a skip
+ * connection.  dx, dw and db may be NULL; dw, db of w_dtype.  T = 0 writes zeros to dw and db.  The workspace is needed for
+ * dw or db. */
+int64_t eff_layer_norm_backward_workspace(int64_t T, int64_t H);
+int eff_layer_norm_backward(int dtype, int w_dtype, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, const void* w,
+                            const float* mean, const float* rstd, const void* residual, int64_t ld_residual, int64_t T,
+                            int64_t H, void* dx, int64_t ld_dx, void* dw, void* db, void* workspace, size_t workspace_bytes,
+                            eff_stream_t stream);
+
+/* The router's losses over T tokens' logits [T,E] (dtype EFF_DT_*; E <= 4096), p = softmax, lse = log sum exp of a row:
+ *   losses[0] = E sum over e of f[e] P[e]  (balance: 1 where both are even),  losses[1] = mean of lse^2,
+ * f[e] the share of the n K places that id e takes, P[e] the mean of p[t,e], both over the n live tokens.  A token is live
+ * if mask (uint8 [T], NULL: all set) is not 0 and some logit is above -infinity; other tokens' logits under a mask of 0 and
+ * their ids are not read.  ids int32 [T,K] as eff_route writes them, K <= 32; ids outside [0,E) count nowhere.
+ * counts int32 [E+1]: live tokens' pairs of each expert, then n; lse fp32 [T] (-infinity for a token that is not live);
+ * losses fp32 [2] (0 where n = 0).  Logits of +infinity or NaN make both losses NaN. */
+int64_t eff_balance_loss_workspace(int64_t T, int num_experts);
+int eff_balance_loss(int dtype, const void* logits, int64_t ld_logits, const int32_t* ids, const uint8_t* mask, int64_t T, int K,
+                     int num_experts, int32_t* counts, float* lse, float* losses, void* workspace, size_t workspace_bytes,
+                     eff_stream_t stream);
+
+/* The gradient at the logits, dlogits [T,E] of dtype, of dlosses[0] losses[0] + dlosses[1] losses[1] (dlosses: device
+ * fp32 [2]; NULL: 0; the counts have no gradient) and, with w and dw (fp32 [T,K], both or neither), of routing weights w =
+ * softmax over the selected logits whose own gradient is dw (as eff_combine_tokens_backward writes it): the pairs of a
+ * token add w[k] (dw[k] - sum w dw) at their ids, over its routed pairs; w and dw of unrouted pairs are not used.  counts
+ * and lse as eff_balance_loss wrote them; tokens whose lse is -infinity get zeros and are not read. */
+int eff_balance_loss_backward(int dtype, const void* logits, int64_t ld_logits, const int32_t* ids, const int32_t* counts,
+                              const float* lse, const float* dlosses, const float* w, const float* dw, int64_t T, int K,
+                              int num_experts, void* dlogits, int64_t ld_dlogits, eff_stream_t stream);
+
+/* Microscaled 4-bit floats.  A row of k values is padded with zeros to whole units of 128 = 64 bytes of codes and 4 bytes
+ * of scales.  Codes are e2m1 (sign, 0 0.5 1 1.5 2 3 4 6), value 2i in the low bits of byte i; every 32 values share a
+ * power of two 2^(scale - 127), 2^(floor(log2 of the largest magnitude) - 2), at least 2^-127.  Rounding is to nearest, ties to
+ * the even code, 6 beyond 6.  A block with an infinity or a NaN gets scale 255 and stands for NaN.
+ * Rows of codes begin at multiples of 16 bytes and ld_codes is a multiple of 16, rows of scales 4 (EFF_EINVAL otherwise).
+ * dtype: EFF_DT_* of x or y.  Bytes of a row for k values: */
+int64_t eff_mx4_code_bytes(int64_t k);
+int64_t eff_mx4_scale_bytes(int64_t k);
+int eff_mx4_quantize(int dtype, const void* x, int64_t ld_x, int64_t rows, int64_t k, uint8_t* codes, int64_t ld_codes,
+                     uint8_t* scales, int64_t ld_scales, eff_stream_t stream);
+/* y = the values, rounded once to dtype (exact in bf16 and fp32). */
+int eff_mx4_dequantize(int dtype, const uint8_t* codes, int64_t ld_codes, const uint8_t* scales, int64_t ld_scales, int64_t rows,
+                       int64_t k, void* y, int64_t ld_y, eff_stream_t stream);
+
+enum { EFF_DT_MX4 = 3 }; /* of eff_mx4_desc.x_dtype alone */
+
+/* y = act(x W^T + bias) + residual of x and W in 4 bits, dense or in groups of rows, as eff_matmul_desc otherwise.
+ *   x: codes and scales (x_dtype EFF_DT_MX4), or 16-bit values [m,k] that the call quantises as eff_mx4_quantize does.
+ *   W: codes and scales of [nw,k] or [E,nw,k]. */
+typedef struct eff_mx4_desc {
+  int32_t x_dtype;   /* EFF_DT_MX4, or dtype */
+  int32_t dtype;     /* bias, residual, pre: EFF_DT_BF16 or EFF_DT_F16 */
+  int32_t out_dtype; /* y: dtype, or EFF_DT_F32 */
+  int32_t act;       /* EFF_ACT_* */
+  int32_t groups;    /* 0, or 1..4096 */
+  int32_t reserved;  /* 0 */
+  int64_t m, n, k;   /* m >= 0; n, k >= 1; m, nw, k < 2^31 */
+  int64_t ld_x, ld_xs;         /* between rows of x: bytes of codes (x_dtype EFF_DT_MX4) or values, and bytes of scales */
+  int64_t ld_w, ld_ws;         /* bytes between rows of W's codes and scales */
+  int64_t stride_w, stride_ws; /* bytes between two groups' */
+  int64_t ld_y, ld_residual, ld_pre;
+} eff_mx4_desc;
+int64_t eff_mx4_matmul_workspace(const eff_mx4_desc* d);
+/* Products of 4-bit values are exact, their sums fp32; bias, activation and residual are fp32 and each output is rounded
+ * once.  Pointers may be NULL as with eff_matmul; xs is NULL unless x_dtype is EFF_DT_MX4.  Gradients (straight through
+ * the rounding) are eff_matmul_backward's on the dequantised operands. */
+int eff_mx4_matmul(const eff_mx4_desc* d, const void* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, const void* bias,
+                   const void* residual, const int32_t* offsets, void* y, void* pre, void* workspace, size_t workspace_bytes,
+                   eff_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
