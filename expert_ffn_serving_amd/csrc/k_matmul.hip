@@ -17,23 +17,6 @@ namespace {
 
 __device__ inline f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 __device__ inline f32x4_t mfma(f16x8_t a, f16x8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-// ---- fp16 operands scaled by powers of two ---------------------------------------------------------------
-//
-// dz of a backward pass may be far larger or smaller than fp16 holds although the gradients are not (an fp32 dy, dy * up,
-// a mean over many tokens).  In fp16 it enters dx scaled per row and dw per column of its group, by the power of two that
-// brings the largest finite magnitude there into [2^14, 2^15), and the sums are scaled back: both are exact, what is
-// left is the rounding to 11 bits, and 2^-39 of the largest where an element is that small.  bf16 has fp32's range.
-__device__ inline int top_exponent(uint32_t largest) { return max((int)(largest >> 23), 15); }  // both powers stay normal
-__device__ inline float scale_to_fp16(uint32_t largest) { return __uint_as_float((uint32_t)(268 - top_exponent(largest)) << 23); }
-__device__ inline float scale_back(uint32_t largest) { return __uint_as_float((uint32_t)(top_exponent(largest) - 14) << 23); }
-// what the sums of output row m (of group g) are multiplied with
-template <typename T>
-__device__ inline float unscale(const MmArgs& a, int g, int64_t m) {
-  if constexpr (std::is_same<T, f16_t>::value)
-    if (a.row_max) return scale_back(a.row_max[(a.mode == MM_K_GROUPS ? g * a.M : 0) + m]);
-  return 1.0f;
-}
-
 // ---- any strides, any alignment ------------------------------------------------------------------------
 // Workgroup = 64 rows x 64 columns (SwiGLU: 32 gate and 32 up columns), 4 waves of 32 x 32, 32 k at a time
 // staged through registers with every bound checked.
@@ -166,31 +149,8 @@ __device__ inline s16x4_t read_tr(const void* lds) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)lds);
 }
 
-// 16-byte chunk `phys` of LDS row `row` holds the row's chunk phys ^ swizzle
-// (k-contiguous operand of BK k a row, whose rows are read 16 at a time, as 4 rows of each of 4 runs of GRP rows with
-// GRP > 1: 8 lanes hit 8 different 16-byte places of the 128 bytes of all banks)
-template <int BK, int GRP>
-__device__ inline int swz_rows(int row) {
-  if (BK == 32) return GRP == 1 ? (row >> 1) & 3 : ((row >> 1) & 1) | (((row / GRP) & 1) << 1);
-  return GRP == 1 ? row & 7 : (row & 3) | (((row / GRP) & 1) << 2);
-}
 // operand contiguous along its index, LDS row = k: pairs of chunks (32 bytes) move
 __device__ inline int swz_k(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
-
-// BM x BN tile, WM x WN waves, BK k per step, S steps in LDS; AHEAD: operands are read half a step ahead (below)
-template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_, bool AHEAD_>
-struct TileCfg {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_, TH = 64 * WM_ * WN_;
-  static constexpr bool AHEAD = AHEAD_;
-};
-
-// subtiles of 16 rows per wave that the epilogue's LDS holds at once
-template <class C>
-constexpr int rows_fit(int mt) {
-  int ip = mt;
-  while (ip > 1 && C::WM * 16 * ip * (C::BN + 4) * 4 > C::S * (C::BM + C::BN) * C::BK * 2) ip /= 2;
-  return ip;
-}
 
 template <typename T, class C, bool XK, bool WK, bool GLU>
 __global__ void __launch_bounds__(C::TH)
@@ -279,7 +239,7 @@ k_mm_tile(MmArgs a) {
   const int64_t klen = k1 - k0;
   const int steps = (int)((klen + BK - 1) / BK);
 
-  auto issue = [&](int t) {
+  auto issue = [&](int t) __attribute__((always_inline)) {
     const uint32_t base = lds0 + (t % S) * STEP + wave * 1024;
     const int left = (int)min((int64_t)BK, klen - (int64_t)t * BK);
     const char *sx = bx + t * stepx, *sw = bw + t * stepw;
@@ -305,7 +265,7 @@ k_mm_tile(MmArgs a) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  auto frag_x = [&](const uint8_t* b, int i, int ks) -> V8 {
+  auto frag_x = [&](const uint8_t* b, int i, int ks) __attribute__((always_inline)) -> V8 {
     if (XK) {
       const int row = wm * TM + i * 16 + r;
       return *reinterpret_cast<const V8*>(b + row * (BK * 2) + (((ks * 4 + q) ^ swz_rows<BK, 1>(row)) << 4));
@@ -319,7 +279,7 @@ k_mm_tile(MmArgs a) {
       return __builtin_bit_cast(V8, (s16x8_t)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
   };
-  auto frag_w = [&](const uint8_t* b, int j, int ks) -> V8 {
+  auto frag_w = [&](const uint8_t* b, int j, int ks) __attribute__((always_inline)) -> V8 {
     if (WK) {
       const int row = wn * TN + (j / NTH) * TNH + (r >> 2) * RUN + (j % NTH) * 4 + (r & 3);
       return *reinterpret_cast<const V8*>(b + XB + row * (BK * 2) + (((ks * 4 + q) ^ swz_rows<BK, RUN>(row)) << 4));
@@ -418,12 +378,6 @@ k_mm_tile(MmArgs a) {
     }
   }
 
-  // Epilogue through LDS, RP rows at a time: the sums change from the matrix core's layout to whole rows, so that
-  // bias, residual, pre and y move as 16-byte vectors, a row's side by side.
-  constexpr int LDC = BN + 4;
-  constexpr int IP = rows_fit<C>(MT) ;
-  constexpr int RP = C::WM * 16 * IP, VR = BNH / 8, ROUND = TH / VR;
-  static_assert(TH % VR == 0 && RP % ROUND == 0, "rows of a round");
   const int64_t yo = a.mode == MM_K_GROUPS ? g * a.syg : 0;
   if (!WK && a.plain) {
     // nothing to add: straight from the registers, 4 columns of 16 rows at a time (1000^3 13.6 -> 11.8 us)
@@ -445,118 +399,7 @@ k_mm_tile(MmArgs a) {
     }
     return;
   }
-  float* s_c = reinterpret_cast<float*>(s_tile);
-  const int64_t nb = (int64_t)g * (GLU ? 2 * a.N : a.N);
-  const int64_t n = n0 + (tid % VR) * 8;
-  constexpr int NR = RP / ROUND;
-  auto row_of = [&](int p, int rr) { return m0 + (rr / (16 * IP)) * TM + p * (16 * IP) + rr % (16 * IP); };
-#pragma unroll
-  for (int p = 0; p < MT / IP; ++p) {
-    V8 res[NR];
-    if (a.simple && a.residual) {  // on its way while the sums go through LDS
-#pragma unroll
-      for (int h = 0; h < NR; ++h) {
-        const int64_t m = row_of(p, tid / VR + h * ROUND);
-        if (m < m1 && n < a.N) res[h] = *reinterpret_cast<const V8*>(reinterpret_cast<const T*>(a.residual) + m * a.ldr + n);
-      }
-    }
-    meet();
-#pragma unroll
-    for (int i = 0; i < IP; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int col = (j / NTH) * BNH + wn * TNH + (WK ? q * RUN + (j % NTH) * 4 : (j % NTH) * 16 + q * 4);
-        *reinterpret_cast<f32x4_t*>(s_c + ((wm * IP + i) * 16 + r) * LDC + col) = acc[p * IP + i][j];
-      }
-    meet();
-    // Whole vectors, no bias, nothing saved, no other activation: every round's accesses at once.  8192 x 4096 x 2048 by epilogue:
-    // none 125 us, residual 134; the general rounds below: fp32 output 133, silu 142, gelu 168, bias, gelu and pre 175.
-    if (a.simple) {
-#pragma unroll
-      for (int h = 0; h < NR; ++h) {
-        const int64_t m = row_of(p, tid / VR + h * ROUND);
-        const float* c = s_c + (tid / VR + h * ROUND) * LDC + (tid % VR) * 8;
-        const float back = unscale<T>(a, g, min(m, m1 - 1));
-        V8 o;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float z = c[e] * back;
-          if (GLU) z = act_silu(z) * c[BNH + e];
-          if (a.residual) z += (float)res[h][e];
-          o[e] = (T)z;
-        }
-        if (m < m1 && n < a.N) {
-          V8* d = reinterpret_cast<V8*>(reinterpret_cast<T*>(a.y) + yo + m * a.ldy + n);
-          if (a.stream) __builtin_nontemporal_store(o, d);
-          else *d = o;
-        }
-      }
-      continue;
-    }
-#pragma unroll 1
-    for (int rr = tid / VR; rr < RP; rr += ROUND) {
-      const int64_t m = row_of(p, rr);
-      if (m >= m1) continue;
-      const float* c = s_c + rr * LDC + (tid % VR) * 8;
-      float z[8], u[8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(c + 4 * h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[4 * h + e] = v[e];
-        if (GLU) {
-          const f32x4_t v2 = *reinterpret_cast<const f32x4_t*>(c + BNH + 4 * h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) u[4 * h + e] = v2[e];
-        }
-      }
-      if (a.part) {
-        float* o = a.part + ((int64_t)blockIdx.y * a.M + m) * a.ldpart + n;
-        if (n < a.N) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            *reinterpret_cast<f32x4_t*>(o + 4 * h) = f32x4_t{z[4 * h], z[4 * h + 1], z[4 * h + 2], z[4 * h + 3]};
-            if (GLU) *reinterpret_cast<f32x4_t*>(o + a.ldpart / 2 + 4 * h) = f32x4_t{u[4 * h], u[4 * h + 1], u[4 * h + 2], u[4 * h + 3]};
-          }
-        }
-      } else {
-        const float back = unscale<T>(a, g, m);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] *= back;
-        mm_finish<T, 8, GLU>(a, m, n, nb, yo, z, u);
-      }
-    }
-  }
-}
-
-// A split k's sums added in order of k, and the epilogue (333 x 515, 7 splits: 6 us, a launch and two trips to memory).  grid: ceil(M * vectors / 256); a thread takes 8 columns.
-template <typename T, bool GLU>
-__global__ void __launch_bounds__(256)
-k_mm_join(MmArgs a, int splits) {
-  const int64_t vr = (a.N + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.M * vr) return;
-  const int64_t m = i / vr, n = i % vr * 8;
-  float z[8], u[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) z[e] = u[e] = 0.f;
-  const float* p = a.part + m * a.ldpart + n;
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s, p += a.M * a.ldpart)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + 4 * h);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z[4 * h + e] += v[e];
-      if (GLU) {
-        const f32x4_t v2 = *reinterpret_cast<const f32x4_t*>(p + a.ldpart / 2 + 4 * h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[4 * h + e] += v2[e];
-      }
-    }
-  const float back = unscale<T>(a, 0, m);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) z[e] *= back;
-  mm_finish<T, 8, GLU>(a, m, n, 0, 0, z, u);
+  store_tile<T, C, WK, GLU>(a, acc, s_tile, g, m0, m1, n0);
 }
 
 // ---- operands that cannot be copied 16 bytes at a time ---------------------------------------------------

@@ -8,6 +8,7 @@
 // infinity or a NaN gets the scale byte 255 and stands for NaN.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "eff_internal.h"
@@ -111,75 +112,280 @@ k_mx4_dequantize(Mx4Rows a) {
 
 // ---- products --------------------------------------------------------------------------------------------
 
-// 16 W rows against 16 x rows over 128 k: lane (r, q) holds the 32 values of block q of row r and their scale (the low byte).
-// The sums: W rows 4 q .. 4 q + 3 of x row r.
+// 16 W rows against 16 x rows over 128 k: lane (r, q) holds 32 values of row r, the q-th of 4 blocks, and their scale in byte
+// B of sw and sx.  The sums: W rows 4 q .. 4 q + 3 of x row r.
+template <int B>
 __device__ inline f32x4_t mfma4(i32x4_t w, i32x4_t x, f32x4_t c, int sw, int sx) {
   const i32x8_t a = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1), b = __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, sw, 0, sx);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, B, sw, B, sx);
 }
 
-// Workgroup = 64 rows x 64 columns (SwiGLU: 32 gate and 32 up columns), 4 waves of 32 x 32, operands straight from memory.
-constexpr int kMxBM = 64, kMxBN = 64;
+// ---- tiles through LDS ----------------------------------------------------------------------------------
+//
+// Workgroup = BM rows x BN columns, WM x WN waves, steps of 256 k: 128 bytes of codes a row, which go to LDS by direct 16-byte
+// copies as those of 64 16-bit values do (k_mm_tile in k_matmul.hip: the same tiles, chunk places and epilogue; C::BK counts 2-byte
+// units).  A matrix instruction takes 128 k; which 32 of them a lane holds is free as long as x and W agree, so the lane
+// of block pair q takes blocks 2 q and 2 q + 1 of a step, one for each of its two instructions: its two scale bytes
+// lie side by side and are read as one 16-bit value, whose byte the instruction picks.
+//
+// Scales come to LDS for two steps at a time, 16 bytes a row (one line of a row holds those of 16 steps: fetched step by step
+// it would be requested as often as the codes' lines): [buffer][row][16], x rows first.
+template <typename T, class C, bool GLU>
+__global__ void __launch_bounds__(C::TH)
+k_mx4_tile(Mx4Args a) {
+  constexpr int BM = C::BM, BN = C::BN, S = C::S, TH = C::TH, CK = 8, KB = 256;
+  constexpr int TM = BM / C::WM, TN = BN / C::WN, MT = TM / 16, NT = TN / 16;
+  constexpr int HALVES = GLU ? 2 : 1, NTH = NT / HALVES, TNH = TN / HALVES, BNH = BN / HALVES, RUN = NTH * 4;
+  constexpr int XB = BM * 128, WB = BN * 128, STEP = XB + WB, SCALES = (BM + BN) * 16;
+  constexpr int SX = BM * CK / TH, SW = BN * CK / TH, CP = SX + SW;
+  static_assert(C::BK == 64 && BM * CK % TH == 0 && BN * CK % TH == 0 && (BM + BN) * 4 % TH == 0 && NT % HALVES == 0, "tile");
+  extern __shared__ __attribute__((aligned(128))) uint8_t s_tile[];
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % C::WM, wn = wave / C::WM;
+  const MmArgs& e = a.e;
 
-template <typename T, bool GLU>
-__global__ void __launch_bounds__(256)
-k_mx4_any(Mx4Args a) {
-  __shared__ int s_find[20];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, q = lane >> 4, r = lane & 15;
-  constexpr int NC = GLU ? kMxBN / 2 : kMxBN;
-  const MmArgs& m_ = a.e;
-  const int nt = (int)((m_.N + NC - 1) / NC), tile = blockIdx.x / nt;
-  const int64_t n0 = (int64_t)(blockIdx.x % nt) * NC;
-  int g = 0;
-  int64_t m0 = (int64_t)tile * kMxBM, m1 = min(m_.M, m0 + kMxBM);
-  if (m_.mode == MM_ROW_GROUPS && !find_tile<kMxBM>(m_.offsets, m_.groups, m_.M, tile, s_find, &g, &m0, &m1)) return;
-  const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
-  const uint8_t *x[2], *xs[2], *w[2], *ws[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t row = min(m0 + wm + i * 16 + r, m1 - 1);
-    x[i] = a.x + row * a.ldx + q * 16;
-    xs[i] = a.xs + row * a.ldxs + q;
-    // columns of the wave: 32, with SwiGLU 16 gate then 16 up
-    const int64_t c = min(GLU ? n0 + (wn >> 1) + r : n0 + wn + i * 16 + r, m_.N - 1), wr = c + (GLU && i ? m_.N : 0);
-    w[i] = a.w + g * a.sw + wr * a.ldw + q * 16;
-    ws[i] = a.ws + g * a.sws + wr * a.ldws + q;
+  const int nt = (int)((e.N + BNH - 1) / BNH);
+  int g = 0, mt_i, nt_i, u0 = 0, u1 = a.units;  // units of 128 k
+  int64_t m0, m1;
+  if (e.mode == MM_ROW_GROUPS) {
+    mt_i = blockIdx.x / nt;
+    nt_i = blockIdx.x % nt;
+    if (!find_tile<BM>(e.offsets, e.groups, e.M, mt_i, reinterpret_cast<int*>(s_tile), &g, &m0, &m1)) return;
+  } else {
+    // an XCD's workgroups take a contiguous part of the tiles, in bands of 8 row tiles, as in k_mm_tile
+    const int all = gridDim.x, xcd = blockIdx.x & 7, id = xcd * (all >> 3) + min(xcd, all & 7) + (blockIdx.x >> 3);
+    const int mts = all / nt, band = id / (8 * nt), in_band = id - band * 8 * nt, height = min(8, mts - band * 8);
+    mt_i = band * 8 + in_band % height;
+    nt_i = in_band / height;
+    m0 = (int64_t)mt_i * BM;
+    m1 = min(e.M, m0 + BM);
+    if (e.part) {
+      u0 = blockIdx.y * e.split_steps * 2;
+      u1 = min(a.units, u0 + e.split_steps * 2);
+    }
   }
-  f32x4_t acc[2][2];
+  const int64_t n0 = (int64_t)nt_i * BNH;
+
+  // this thread's copies: byte offsets from uniform addresses (plan_mx4 keeps them < 2^32)
+  const uint8_t *bx = a.x + m0 * a.ldx + (int64_t)u0 * 64, *bw = a.w + g * a.sw + n0 * a.ldw + (int64_t)u0 * 64;
+  const int64_t up_codes = GLU ? e.N * a.ldw : 0;
+  const int bytes = (u1 - u0) * 64;
+  uint32_t ox[SX], ow[SW];
+  int kx[SX], kw[SW];  // the copy's first byte inside a step
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < SX; ++i) {
+    const int idx = i * TH + tid, row = idx / CK, c = (idx % CK) ^ swz_rows<64, 1>(row);
+    kx[i] = c * 16;
+    ox[i] = (uint32_t)(min((int64_t)row, m1 - 1 - m0) * a.ldx + c * 16);
+  }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int u = 0; u < a.units; ++u) {
-    i32x4_t fx[2], fw[2];
-    int sx[2], sw[2];
+  for (int i = 0; i < SW; ++i) {
+    const int idx = i * TH + tid, row = idx / CK, c = (idx % CK) ^ swz_rows<64, RUN>(row);
+    const int col = (row / TN) * TNH + (row % TNH);
+    kw[i] = c * 16;
+    ow[i] = (uint32_t)(min((int64_t)col, e.N - 1 - n0) * a.ldw + c * 16);
+  }
+  const uint32_t lds0 = lds_address(s_tile), lds_s = lds0 + S * STEP;
+  const int steps = (u1 - u0 + 1) / 2;
+  const char* zero = reinterpret_cast<const char*>(g_zero16);
+
+  auto issue = [&](int t) __attribute__((always_inline)) {
+    const uint32_t base = lds0 + (t % S) * STEP + wave * 1024;
+    const int left = min(128, bytes - t * 128);
+    const uint8_t *sx = bx + (int64_t)t * 128, *sw = bw + (int64_t)t * 128;
+    auto side = [&](int i) { return GLU && ((i * TH + wave * 64) / CK) % TN >= TNH ? sw + up_codes : sw; };
+    if (left == 128) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      fx[i] = *reinterpret_cast<const i32x4_t*>(x[i] + (int64_t)u * 64);
-      fw[i] = *reinterpret_cast<const i32x4_t*>(w[i] + (int64_t)u * 64);
-      sx[i] = xs[i][(int64_t)u * 4];
-      sw[i] = ws[i][(int64_t)u * 4];
+      for (int i = 0; i < SX; ++i) lds_copy16(sx, ox[i], base + i * (TH * 16));
+#pragma unroll
+      for (int i = 0; i < SW; ++i) lds_copy16(side(i), ow[i], base + XB + i * (TH * 16));
+    } else {
+#pragma unroll
+      for (int i = 0; i < SX; ++i) lds_copy16(kx[i] < left ? (const char*)sx + ox[i] : zero, base + i * (TH * 16));
+#pragma unroll
+      for (int i = 0; i < SW; ++i) lds_copy16(kw[i] < left ? (const char*)side(i) + ow[i] : zero, base + XB + i * (TH * 16));
+    }
+    if (t % 2 == 0) {  // the scales of steps t and t + 1, 4 units
+      const uint32_t at = lds_s + (t / 2 % 2) * SCALES;
+      const int u = u0 + t * 2, n = min(4, u1 - u);
+#pragma unroll
+      for (int c = 0; c < (BM + BN) * 4 / TH; ++c) {  // a wave's copy: 16 rows of 4 bytes x 4
+        const int i = c * (TH / 4) + wave * 16, row = i + (lane >> 2), unit = lane & 3;
+        const uint8_t* p;
+        if (row < BM) {
+          p = a.xs + (m0 + min((int64_t)row, m1 - 1 - m0)) * a.ldxs;
+        } else {
+          const int w = row - BM, col = (w / TN) * TNH + (w % TNH);
+          p = a.ws + g * a.sws + ((w % TN >= TNH ? e.N : 0) + n0 + min((int64_t)col, e.N - 1 - n0)) * a.ldws;
+        }
+        lds_copy4(unit < n ? (const char*)p + (u + unit) * 4 : zero, at + i * 16);
+      }
+    }
+  };
+
+  f32x4_t acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  auto x_row = [&](int i) { return wm * TM + i * 16 + r; };
+  auto w_row = [&](int j) { return wn * TN + (j / NTH) * TNH + (r >> 2) * RUN + (j % NTH) * 4 + (r & 3); };
+  auto frag_x = [&](const uint8_t* b, int i, int ks) __attribute__((always_inline)) {
+    const int row = x_row(i);
+    return *reinterpret_cast<const i32x4_t*>(b + row * 128 + (((2 * q + ks) ^ swz_rows<64, 1>(row)) << 4));
+  };
+  auto frag_w = [&](const uint8_t* b, int j, int ks) __attribute__((always_inline)) {
+    const int row = w_row(j);
+    return *reinterpret_cast<const i32x4_t*>(b + XB + row * 128 + (((2 * q + ks) ^ swz_rows<64, RUN>(row)) << 4));
+  };
+  auto scale_of = [&](int t, int row) -> int {
+    return *reinterpret_cast<const uint16_t*>(s_tile + S * STEP + (t / 2 % 2) * SCALES + row * 16 + (t & 1) * 8 + q * 2);
+  };
+  auto buffer = [&](int t) { return s_tile + (t % S) * STEP; };
+
+#pragma unroll
+  for (int t = 0; t < S - 1; ++t)
+    if (t < steps) issue(t);
+  for (int t = 0; t < steps; ++t) {
+    // copies issued after step t's: at least CP for every later step (scales beside, which only makes the wait stricter)
+    if (t + S - 1 > steps) vm_wait<0>();
+    else vm_wait<(S - 2) * CP>();
+    meet();
+    if (t + S - 1 < steps) issue(t + S - 1);
+    int sx[MT], sw[NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sx[i] = scale_of(t, x_row(i));
+#pragma unroll
+    for (int j = 0; j < NT; ++j) sw[j] = scale_of(t, BM + w_row(j));
+    {
+      i32x4_t fw[NT], fx[MT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fw[j] = frag_w(buffer(t), j, 0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fx[i] = frag_x(buffer(t), i, 0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = mfma4<0>(fw[j], fx[i], acc[i][j], sw[j], sx[i]);
+    }
+    {
+      i32x4_t fw[NT], fx[MT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fw[j] = frag_w(buffer(t), j, 1);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fx[i] = frag_x(buffer(t), i, 1);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = mfma4<1>(fw[j], fx[i], acc[i][j], sw[j], sx[i]);
+    }
+  }
+  store_tile<T, C, true, GLU>(e, acc, s_tile, g, m0, m1, n0);
+}
+
+// ---- few rows --------------------------------------------------------------------------------------------
+//
+// Up to 16 MT rows of x against 16 rows of W per workgroup (SwiGLU: 8 gate and 8 up rows), the k split over its waves, as
+// k_mm_few does for 16 bits: every wave keeps U chunks of 256 k (2 KiB of W each) in flight in registers, nothing waits for a
+// barrier before the end, where the waves' sums meet in LDS in wave order.
+template <int MT>
+constexpr int mx4_unroll() { return MT == 1 ? 4 : 2; }
+
+template <typename T, int MT, bool GLU>
+__global__ void __launch_bounds__(1024)
+k_mx4_few(Mx4Args a, int slices) {
+  constexpr int U = mx4_unroll<MT>(), BM = 16 * MT;
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_few[];
+  f32x4_t* s_acc = reinterpret_cast<f32x4_t*>(s_few);  // [waves][MT][64]
+  const MmArgs& e = a.e;
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+  const int64_t tile = blockIdx.x / slices, n0 = (int64_t)(blockIdx.x % slices) * (GLU ? 8 : 16);
+  int g = 0;
+  int64_t m0 = tile * BM, m1 = min(e.M, m0 + BM);
+  if (e.mode == MM_ROW_GROUPS && !find_tile<BM>(e.offsets, e.groups, e.M, (int)tile, reinterpret_cast<int*>(s_few), &g, &m0, &m1)) return;
+  const int chunks = (a.units + 1) / 2;
+  const int64_t col = min(n0 + (GLU ? r & 7 : r), e.N - 1), wr = col + (GLU && r >= 8 ? e.N : 0);
+  const uint8_t *w = a.w + g * a.sw + wr * a.ldw + q * 32, *ws = a.ws + g * a.sws + wr * a.ldws + q * 2;
+  const uint8_t *x[MT], *xs[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t row = min(m0 + i * 16 + r, m1 - 1);
+    x[i] = a.x + row * a.ldx + q * 32;
+    xs[i] = a.xs + row * a.ldxs + q * 2;
+  }
+  f32x4_t acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  i32x4_t fw[U][2], fx[U][MT][2];
+  int sw[U], sx[U][MT];
+  const bool odd = a.units & 1;  // the last chunk has one unit: lanes q >= 2 have nothing there
+  // chunk c of this wave's into slot s; past the end the first chunk again (not used)
+  auto load = [&](int c, int s) {
+    const bool none = c >= chunks || (odd && c == chunks - 1 && q >= 2);
+    const int64_t at = none ? -(int64_t)q * 32 : (int64_t)c * 128, as = none ? -(int64_t)q * 2 : (int64_t)c * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      fw[s][h] = *reinterpret_cast<const i32x4_t*>(w + at + h * 16);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fx[s][i][h] = *reinterpret_cast<const i32x4_t*>(x[i] + at + h * 16);
+    }
+    sw[s] = *reinterpret_cast<const uint16_t*>(ws + as);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sx[s][i] = *reinterpret_cast<const uint16_t*>(xs[i] + as);
+  };
+  auto use = [&](int c, int s) {
+    if (c >= chunks) return;
+    if (odd && c == chunks - 1 && q >= 2) {  // zeros, whatever scales
+      fw[s][0] = fw[s][1] = i32x4_t{0, 0, 0, 0};
+      sw[s] = 0;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        fx[s][i][0] = fx[s][i][1] = i32x4_t{0, 0, 0, 0};
+        sx[s][i] = 0;
+      }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < MT; ++i) {
+      acc[i] = mfma4<0>(fw[s][0], fx[s][i][0], acc[i], sw[s], sx[s][i]);
+      acc[i] = mfma4<1>(fw[s][1], fx[s][i][1], acc[i], sw[s], sx[s][i]);
+    }
+  };
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma4(fw[j], fx[i], acc[i][j], sw[j], sx[i]);
+  for (int s = 0; s < U; ++s) load(wave + s * waves, s);
+  const int64_t nb = (int64_t)g * (GLU ? 2 * e.N : e.N);
+  Extra<4> extra;
+  if (wave < MT && m0 + wave * 16 + r < m1 && n0 + 4 * q < e.N && (!GLU || q < 2))
+    mm_fetch<T, 4, GLU>(e, m0 + wave * 16 + r, n0 + 4 * q, nb, &extra);
+  int c = wave;
+  for (; c + U * waves < chunks; c += U * waves) {
+#pragma unroll
+    for (int s = 0; s < U; ++s) {
+      use(c + s * waves, s);
+      load(c + (s + U) * waves, s);
+    }
   }
-  const int64_t nb = (int64_t)g * (GLU ? 2 * m_.N : m_.N);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t m = m0 + wm + i * 16 + r;
-    if (m >= m1) continue;
+  for (int s = 0; s < U; ++s) use(c + s * waves, s);
 #pragma unroll
-    for (int j = 0; j < (GLU ? 1 : 2); ++j) {
-      const int64_t n = GLU ? n0 + (wn >> 1) + 4 * q : n0 + wn + j * 16 + 4 * q;
-      float z[4], u[4];
+  for (int i = 0; i < MT; ++i) s_acc[(wave * MT + i) * 64 + lane] = acc[i];
+  __syncthreads();
+  // one wave per 16 rows of x: lane's row m = r, W rows 4 q .. 4 q + 3 of the slice
+  for (int i = wave; i < MT; i += waves) {
+    const int64_t m = m0 + i * 16 + r, n = n0 + 4 * q;
+    f32x4_t sum = s_acc[i * 64 + lane];
+    for (int v = 1; v < waves; ++v) sum += s_acc[(v * MT + i) * 64 + lane];
+    float z[4], u[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        z[c] = acc[i][j][c];
-        if (GLU) u[c] = acc[i][1][c];
-      }
-      mm_finish<T, 4, GLU>(m_, m, n, nb, 0, z, u);
+    for (int k = 0; k < 4; ++k) {
+      z[k] = sum[k];
+      if (GLU) u[k] = __shfl_down(z[k], 32);
+    }
+    if (m < m1 && n < e.N && (!GLU || q < 2)) {
+      if (i != wave) mm_fetch<T, 4, GLU>(e, m, n, nb, &extra);
+      mm_apply<T, 4, GLU>(e, m, n, 0, z, u, extra);
     }
   }
 }
@@ -236,29 +442,119 @@ hipError_t launch_mx4_dequantize(const Mx4Rows& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-bool mx4_matmul_fits(const Mx4Args& a) {
-  const int64_t nw = a.e.act == EFF_ACT_SWIGLU ? 2 * a.e.N : a.e.N;
-  const int64_t rows = a.e.mode == MM_ROW_GROUPS ? group_tiles(a.e.M, a.e.groups, kMxBM) : ceil_div(a.e.M, kMxBM);
-  return fits(ceil_div(nw, kMxBN) * rows, 256);
+namespace {
+
+// ---- which kernel ----------------------------------------------------------------------------------------
+
+typedef TileCfg<256, 256, 2, 4, 64, 2, false> MxBig;
+typedef TileCfg<128, 128, 2, 2, 64, 2, false> MxMid;
+typedef TileCfg<64, 128, 1, 4, 64, 3, false> MxLow;
+
+enum { MX_FEW1, MX_FEW2, MX_BIG, MX_MID, MX_LOW };
+
+struct MxPlan {
+  int kind, splits;
+  int64_t part;  // workspace bytes
+};
+
+int64_t mx4_rows(const MmArgs& e, int64_t BM) { return e.mode == MM_ROW_GROUPS ? group_tiles(e.M, e.groups, BM) : ceil_div(e.M, BM); }
+
+MxPlan plan_mx4(const Mx4Args& a) {
+  const MmArgs& e = a.e;
+  const bool glu = e.act == EFF_ACT_SWIGLU;
+  const int64_t n = glu ? 2 * e.N : e.N, groups = std::max<int64_t>(1, e.groups);
+  const int64_t rows = e.mode == MM_ROW_GROUPS ? e.M / std::max<int64_t>(1, std::min(groups, e.M)) : e.M;
+  const bool fill = mx4_rows(e, MxLow::BM) * ceil_div(n, MxLow::BN) >= 512;
+  if (rows <= 16 && !fill) return {MX_FEW1, 1, 0};
+  if (rows <= 32 && !fill) return {MX_FEW2, 1, 0};
+  // a tile's lanes hold unsigned 32-bit byte offsets from its first row
+  const int64_t far = std::max(a.ldx, a.ldw);
+  struct Tile { int kind; int64_t bm, bn; int occ; double alone, step, fixed; };
+  const Tile tiles[] = {{MX_BIG, MxBig::BM, MxBig::BN, 1, 1.55, 1.55, 14},
+                        {MX_MID, MxMid::BM, MxMid::BN, 2, 0.75, 1.0, 7},
+                        {MX_LOW, MxLow::BM, MxLow::BN, 2, 0.42, 0.64, 6}};
+  const int64_t steps = ceil_div(a.units, 2);
+  MxPlan p = {MX_FEW2, 1, 0};
+  double best = 0;
+  for (const Tile& t : tiles) {
+    if (far * std::max(t.bm, t.bn) >= (int64_t)1 << 32) continue;
+    double count = (double)ceil_div(n, t.bn);
+    if (e.mode == MM_ROW_GROUPS) count *= std::max<double>((double)ceil_div(rows, t.bm) * std::min(groups, e.M), e.M / (double)t.bm);
+    else count *= (double)ceil_div(e.M, t.bm);
+    for (int64_t s = 1; s <= 16 && (s == 1 || (e.mode == MM_DENSE && s * 4 <= steps)); ++s) {
+      const double each = (double)ceil_div(steps, s), full = std::floor(count * s / (256.0 * t.occ)), rest = count * s - full * 256 * t.occ;
+      double us = full * (t.step * each + t.fixed);
+      if (rest > 0) us += (rest <= 256 ? t.alone : t.step) * each + t.fixed;
+      if (s > 1) us += 5 + s * (double)e.M * n * 8 / 8e6;
+      if (best == 0 || us < best) best = us, p.kind = t.kind, p.splits = (int)s;
+    }
+  }
+  if (p.splits > 1) {
+    p.splits = (int)ceil_div(steps, ceil_div(steps, p.splits));
+    p.part = up((int64_t)p.splits * e.M * (glu ? 2 : 1) * up(e.N, 8) * 4, 256);
+  }
+  return p;
 }
 
-int64_t mx4_matmul_workspace(const Mx4Args&) { return 0; }
+template <typename T, class C, bool GLU>
+hipError_t launch_mx4_tile(const Mx4Args& a, int splits, hipStream_t s) {
+  const int64_t tiles = ceil_div(a.e.N, GLU ? C::BN / 2 : C::BN) * mx4_rows(a.e, C::BM);
+  constexpr int lds = C::S * (C::BM + C::BN) * 128 + 2 * (C::BM + C::BN) * 16;
+  auto* fn = &k_mx4_tile<T, C, GLU>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t set = allow_lds(reinterpret_cast<const void*>(fn), lds, &done);
+  if (set != hipSuccess) return set;
+  hipLaunchKernelGGL(fn, dim3((unsigned)tiles, (unsigned)splits), dim3(C::TH), lds, s, a);
+  if (splits > 1)
+    hipLaunchKernelGGL((k_mm_join<T, GLU>), dim3((unsigned)ceil_div(a.e.M * ceil_div(a.e.N, 8), 256)), dim3(256), 0, s, a.e, splits);
+  return hipGetLastError();
+}
 
-hipError_t launch_mx4_matmul(const Mx4Args& in, void*, hipStream_t s) {
+template <typename T, int MT, bool GLU>
+hipError_t launch_mx4_few(const Mx4Args& a, hipStream_t s) {
+  const int64_t slices = ceil_div(a.e.N, GLU ? 8 : 16), jobs = slices * mx4_rows(a.e, 16 * MT);
+  // waves per workgroup: up to 32 per CU over the launch, each with at least two chunks of k
+  int waves = 16;
+  while (waves > 1 && (jobs * waves > 8192 || waves * 4 > a.units + 3)) waves /= 2;
+  hipLaunchKernelGGL((k_mx4_few<T, MT, GLU>), dim3((unsigned)jobs), dim3(64 * waves), waves * MT * 1024, s, a, (int)slices);
+  return hipGetLastError();
+}
+
+template <typename T, bool GLU>
+hipError_t launch_mx4_kind(const Mx4Args& a, const MxPlan& p, hipStream_t s) {
+  if (p.kind == MX_FEW1) return launch_mx4_few<T, 1, GLU>(a, s);
+  if (p.kind == MX_FEW2) return launch_mx4_few<T, 2, GLU>(a, s);
+  if (p.kind == MX_BIG) return launch_mx4_tile<T, MxBig, GLU>(a, p.splits, s);
+  if (p.kind == MX_MID) return launch_mx4_tile<T, MxMid, GLU>(a, p.splits, s);
+  return launch_mx4_tile<T, MxLow, GLU>(a, p.splits, s);
+}
+
+}  // namespace
+
+bool mx4_matmul_fits(const Mx4Args& a) {
+  const int64_t nw = a.e.act == EFF_ACT_SWIGLU ? 2 * a.e.N : a.e.N;
+  const MxPlan p = plan_mx4(a);
+  if (p.kind == MX_FEW1 || p.kind == MX_FEW2) return fits(ceil_div(nw, 16) * mx4_rows(a.e, p.kind == MX_FEW1 ? 16 : 32), 1024);
+  return fits(ceil_div(nw, 128) * mx4_rows(a.e, 64), 512);
+}
+
+int64_t mx4_matmul_workspace(const Mx4Args& a) { return plan_mx4(a).part; }
+
+hipError_t launch_mx4_matmul(const Mx4Args& in, void* workspace, hipStream_t s) {
   Mx4Args a = in;
   MmArgs& e = a.e;
   e.vec = aligned16({e.y, e.bias, e.residual, e.pre}, {e.N, e.ldy, e.residual ? e.ldr : 0, e.pre ? e.ldp : 0}, 2);
+  e.stream = e.M * e.N * (e.y_f32 ? 4 : 2) > (int64_t)256 << 20;  // past the caches, as launch_matmul
+  e.simple = e.vec && !e.bias && !e.pre && !e.y_f32 && (e.act == EFF_ACT_NONE || e.act == EFF_ACT_SWIGLU);
+  const MxPlan p = plan_mx4(a);
   const bool glu = e.act == EFF_ACT_SWIGLU;
-  const int64_t rows = e.mode == MM_ROW_GROUPS ? group_tiles(e.M, e.groups, kMxBM) : ceil_div(e.M, kMxBM);
-  const dim3 g((unsigned)(ceil_div(e.N, glu ? kMxBN / 2 : kMxBN) * rows));
-  auto go = [&](auto t) {
-    typedef decltype(t) T;
-    if (glu) hipLaunchKernelGGL((k_mx4_any<T, true>), g, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((k_mx4_any<T, false>), g, dim3(256), 0, s, a);
-  };
-  if (e.dtype == EFF_DT_BF16) go(bf16_t{});
-  else go(f16_t{});
-  return hipGetLastError();
+  if (p.splits > 1) {
+    e.part = static_cast<float*>(workspace);
+    e.ldpart = (glu ? 2 : 1) * up(e.N, 8), e.simple = 0;
+    e.split_steps = (int)ceil_div(ceil_div(a.units, 2), p.splits);
+  }
+  if (e.dtype == EFF_DT_BF16) return glu ? launch_mx4_kind<bf16_t, true>(a, p, s) : launch_mx4_kind<bf16_t, false>(a, p, s);
+  return glu ? launch_mx4_kind<f16_t, true>(a, p, s) : launch_mx4_kind<f16_t, false>(a, p, s);
 }
 
 }  // namespace eff

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <atomic>
 #include <initializer_list>
+#include <type_traits>
 
 #include "eff_internal.h"
 
@@ -130,11 +131,28 @@ __device__ inline bool find_tile(const int32_t* offsets, int E, int64_t m, int t
     }
   }
   __syncthreads();
-  *group = s[16];
-  *row0 = s[17];
-  *row1 = s[18];
+  *group = __builtin_amdgcn_readfirstlane(s[16]);
+  *row0 = __builtin_amdgcn_readfirstlane(s[17]);
+  *row1 = __builtin_amdgcn_readfirstlane(s[18]);
   __syncthreads();
   return *group >= 0;
+}
+
+// ---- fp16 operands scaled by powers of two ---------------------------------------------------------------
+//
+// dz of a backward pass may be far larger or smaller than fp16 holds although the gradients are not (an fp32 dy, dy * up,
+// a mean over many tokens).  In fp16 it enters dx scaled per row and dw per column of its group, by the power of two that
+// brings the largest finite magnitude there into [2^14, 2^15), and the sums are scaled back: both are exact, what is
+// left is the rounding to 11 bits, and 2^-39 of the largest where an element is that small.  bf16 has fp32's range.
+__device__ inline int top_exponent(uint32_t largest) { return max((int)(largest >> 23), 15); }  // both powers stay normal
+__device__ inline float scale_to_fp16(uint32_t largest) { return __uint_as_float((uint32_t)(268 - top_exponent(largest)) << 23); }
+__device__ inline float scale_back(uint32_t largest) { return __uint_as_float((uint32_t)(top_exponent(largest) - 14) << 23); }
+// what the sums of output row m (of group g) are multiplied with
+template <typename T>
+__device__ inline float unscale(const MmArgs& a, int g, int64_t m) {
+  if constexpr (std::is_same<T, f16_t>::value)
+    if (a.row_max) return scale_back(a.row_max[(a.mode == MM_K_GROUPS ? g * a.M : 0) + m]);
+  return 1.0f;
 }
 
 // ---- epilogue of CL consecutive columns n.. of row m -----------------------------------------------------
@@ -230,6 +248,161 @@ __device__ __forceinline__ void meet() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// ---- tiles through LDS ----------------------------------------------------------------------------------
+
+// 16-byte chunk `phys` of LDS row `row` holds the row's chunk phys ^ swizzle
+// (k-contiguous operand of BK k a row, whose rows are read 16 at a time, as 4 rows of each of 4 runs of GRP rows with
+// GRP > 1: 8 lanes hit 8 different 16-byte places of the 128 bytes of all banks)
+template <int BK, int GRP>
+__device__ inline int swz_rows(int row) {
+  if (BK == 32) return GRP == 1 ? (row >> 1) & 3 : ((row >> 1) & 1) | (((row / GRP) & 1) << 1);
+  return GRP == 1 ? row & 7 : (row & 3) | (((row / GRP) & 1) << 2);
+}
+// BM x BN tile, WM x WN waves, BK k per step, S steps in LDS; AHEAD: operands are read half a step ahead (below)
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_, bool AHEAD_>
+struct TileCfg {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_, TH = 64 * WM_ * WN_;
+  static constexpr bool AHEAD = AHEAD_;
+};
+
+// subtiles of 16 rows per wave that the epilogue's LDS holds at once
+template <class C>
+constexpr int rows_fit(int mt) {
+  int ip = mt;
+  while (ip > 1 && C::WM * 16 * ip * (C::BN + 4) * 4 > C::S * (C::BM + C::BN) * C::BK * 2) ip /= 2;
+  return ip;
+}
+
+// A tile's sums to y: bias, activation, residual, pre.  Called by the whole workgroup; s_tile: its S steps of LDS.
+template <typename T, class C, bool WK, bool GLU, int MT, int NT>
+__device__ __forceinline__ void store_tile(const MmArgs& a, f32x4_t (&acc)[MT][NT], uint8_t* s_tile, int g, int64_t m0, int64_t m1, int64_t n0) {
+  typedef typename Vec8<T>::V V8;
+  constexpr int BN = C::BN, TH = C::TH, TM = C::BM / C::WM, TN = BN / C::WN;
+  constexpr int HALVES = GLU ? 2 : 1, NTH = NT / HALVES, TNH = TN / HALVES, BNH = BN / HALVES, RUN = NTH * 4;
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % C::WM, wn = wave / C::WM;
+  // Epilogue through LDS, RP rows at a time: the sums change from the matrix core's layout to whole rows, so that
+  // bias, residual, pre and y move as 16-byte vectors, a row's side by side.
+  constexpr int LDC = BN + 4;
+  constexpr int IP = rows_fit<C>(MT) ;
+  constexpr int RP = C::WM * 16 * IP, VR = BNH / 8, ROUND = TH / VR;
+  static_assert(TH % VR == 0 && RP % ROUND == 0, "rows of a round");
+  const int64_t yo = a.mode == MM_K_GROUPS ? g * a.syg : 0;
+  float* s_c = reinterpret_cast<float*>(s_tile);
+  const int64_t nb = (int64_t)g * (GLU ? 2 * a.N : a.N);
+  const int64_t n = n0 + (tid % VR) * 8;
+  constexpr int NR = RP / ROUND;
+  auto row_of = [&](int p, int rr) { return m0 + (rr / (16 * IP)) * TM + p * (16 * IP) + rr % (16 * IP); };
+#pragma unroll
+  for (int p = 0; p < MT / IP; ++p) {
+    V8 res[NR];
+    if (a.simple && a.residual) {  // on its way while the sums go through LDS
+#pragma unroll
+      for (int h = 0; h < NR; ++h) {
+        const int64_t m = row_of(p, tid / VR + h * ROUND);
+        if (m < m1 && n < a.N) res[h] = *reinterpret_cast<const V8*>(reinterpret_cast<const T*>(a.residual) + m * a.ldr + n);
+      }
+    }
+    meet();
+#pragma unroll
+    for (int i = 0; i < IP; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int col = (j / NTH) * BNH + wn * TNH + (WK ? q * RUN + (j % NTH) * 4 : (j % NTH) * 16 + q * 4);
+        *reinterpret_cast<f32x4_t*>(s_c + ((wm * IP + i) * 16 + r) * LDC + col) = acc[p * IP + i][j];
+      }
+    meet();
+    // Whole vectors, no bias, nothing saved, no other activation: every round's accesses at once.  8192 x 4096 x 2048 by epilogue:
+    // none 125 us, residual 134; the general rounds below: fp32 output 133, silu 142, gelu 168, bias, gelu and pre 175.
+    if (a.simple) {
+#pragma unroll
+      for (int h = 0; h < NR; ++h) {
+        const int64_t m = row_of(p, tid / VR + h * ROUND);
+        const float* c = s_c + (tid / VR + h * ROUND) * LDC + (tid % VR) * 8;
+        const float back = unscale<T>(a, g, min(m, m1 - 1));
+        V8 o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float z = c[e] * back;
+          if (GLU) z = act_silu(z) * c[BNH + e];
+          if (a.residual) z += (float)res[h][e];
+          o[e] = (T)z;
+        }
+        if (m < m1 && n < a.N) {
+          V8* d = reinterpret_cast<V8*>(reinterpret_cast<T*>(a.y) + yo + m * a.ldy + n);
+          if (a.stream) __builtin_nontemporal_store(o, d);
+          else *d = o;
+        }
+      }
+      continue;
+    }
+#pragma unroll 1
+    for (int rr = tid / VR; rr < RP; rr += ROUND) {
+      const int64_t m = row_of(p, rr);
+      if (m >= m1) continue;
+      const float* c = s_c + rr * LDC + (tid % VR) * 8;
+      float z[8], u[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(c + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[4 * h + e] = v[e];
+        if (GLU) {
+          const f32x4_t v2 = *reinterpret_cast<const f32x4_t*>(c + BNH + 4 * h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u[4 * h + e] = v2[e];
+        }
+      }
+      if (a.part) {
+        float* o = a.part + ((int64_t)blockIdx.y * a.M + m) * a.ldpart + n;
+        if (n < a.N) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            *reinterpret_cast<f32x4_t*>(o + 4 * h) = f32x4_t{z[4 * h], z[4 * h + 1], z[4 * h + 2], z[4 * h + 3]};
+            if (GLU) *reinterpret_cast<f32x4_t*>(o + a.ldpart / 2 + 4 * h) = f32x4_t{u[4 * h], u[4 * h + 1], u[4 * h + 2], u[4 * h + 3]};
+          }
+        }
+      } else {
+        const float back = unscale<T>(a, g, m);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] *= back;
+        mm_finish<T, 8, GLU>(a, m, n, nb, yo, z, u);
+      }
+    }
+  }
+}
+
+// A split k's sums added in order of k, and the epilogue (333 x 515, 7 splits: 6 us, a launch and two trips to memory).  grid: ceil(M * vectors / 256); a thread takes 8 columns.
+template <typename T, bool GLU>
+__global__ void __launch_bounds__(256)
+k_mm_join(MmArgs a, int splits) {
+  const int64_t vr = (a.N + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.M * vr) return;
+  const int64_t m = i / vr, n = i % vr * 8;
+  float z[8], u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = u[e] = 0.f;
+  const float* p = a.part + m * a.ldpart + n;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s, p += a.M * a.ldpart)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + 4 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[4 * h + e] += v[e];
+      if (GLU) {
+        const f32x4_t v2 = *reinterpret_cast<const f32x4_t*>(p + a.ldpart / 2 + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[4 * h + e] += v2[e];
+      }
+    }
+  const float back = unscale<T>(a, 0, m);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] *= back;
+  mm_finish<T, 8, GLU>(a, m, n, 0, 0, z, u);
 }
 
 // ---- launches ----------------------------------------------------------------------------------------
