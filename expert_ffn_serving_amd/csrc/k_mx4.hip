@@ -24,89 +24,191 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 // ---- rows to 4 bits and back -----------------------------------------------------------------------------
 
 constexpr int kNaNScale = 255;
+typedef bf16_t bf16x2_t __attribute__((ext_vector_type(2)));
+typedef f16_t f16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x8_t __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+template <>
+struct Vec8<float> { typedef f32x8_t V; };
 
-// The block exponent's byte from the bits of the largest magnitude (fp32, below infinity).  A subnormal number's exponent
-// is below -126, and -127 is the least there is.
-__device__ inline int mx4_scale(uint32_t largest) {
-  return largest >= 0x7f800000u ? kNaNScale : max((int)(largest >> 23) - 2, 0);
+// the largest of v over the 4 lanes of a quad
+__device__ inline uint32_t quad_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));  // lanes 1 0 3 2
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
 }
-// 2^-(scale - 127) for a scale byte up to 252 (no fp32 number has a larger one)
-__device__ inline float mx4_inverse(int scale) { return __uint_as_float((uint32_t)(254 - min(scale, 252)) << 23); }
+// the scale byte of a block from the largest magnitude of this lane's 8 values; the 4 lanes of a quad hold a block.  The
+// magnitudes of 16-bit values are compared as integers, two at a time.  A subnormal fp32 number's exponent is below -126,
+// and -127 is the least there is.
+__device__ inline int mx4_scale(uint32_t bits) {  // of the largest magnitude in fp32
+  return bits >= 0x7f800000u ? kNaNScale : max((int)(bits >> 23) - 2, 0);
+}
+template <typename V>
+__device__ inline uint32_t top_of_16(const V& v) {
+  struct Pairs { u16x2_t p[4]; };
+  const Pairs w = __builtin_bit_cast(Pairs, v);
+  u16x2_t m = w.p[0] & (uint16_t)0x7fff;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, w.p[i] & (uint16_t)0x7fff);
+  return max((uint32_t)m[0], (uint32_t)m[1]);
+}
+__device__ inline int block_scale(const bf16x8_t& v) { return mx4_scale(quad_max(top_of_16(v)) << 16); }
+__device__ inline int block_scale(const f16x8_t& v) {
+  const uint16_t t = (uint16_t)quad_max(top_of_16(v));
+  return mx4_scale(__float_as_uint((float)__builtin_bit_cast(f16_t, t)));
+}
+__device__ inline int block_scale(const f32x8_t& v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  return mx4_scale(quad_max(m));
+}
+// 2^(scale - 127) as the conversions take it: they look at the exponent, of which 0 is 2^-127
+__device__ inline float scale_value(int scale) { return __uint_as_float((uint32_t)scale << 23); }
 
-// the e2m1 code of v: nearest, ties to even, 6 beyond
-__device__ inline uint32_t mx4_code(float v) {
-  const float a = fabsf(v);
-  const uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
-  return c | (__float_as_uint(v) >> 31 << 3);
+// 8 values to codes: v_cvt_scalef32_pk_fp4_* rounds to nearest, ties to even, and gives 6 beyond 6
+__device__ inline uint32_t to_codes(const bf16x8_t& v, float s) {
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(0, bf16x2_t{v[0], v[1]}, s, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16x2_t{v[2], v[3]}, s, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16x2_t{v[4], v[5]}, s, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16x2_t{v[6], v[7]}, s, 3);
 }
-// the value of a code times 2^(scale - 127); scale 255: NaN
-__device__ inline float mx4_value(uint32_t code, int scale) {
-  const uint32_t m = code & 7;
-  const float mag = m < 2 ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126) << 23 | (m & 1) << 22);
-  const float v = scale == kNaNScale ? __builtin_nanf("") : mag * (scale ? __uint_as_float((uint32_t)scale << 23) : 0x1p-127f);
-  return code & 8 ? -v : v;
+__device__ inline uint32_t to_codes(const f16x8_t& v, float s) {
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(0, f16x2_t{v[0], v[1]}, s, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, f16x2_t{v[2], v[3]}, s, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, f16x2_t{v[4], v[5]}, s, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, f16x2_t{v[6], v[7]}, s, 3);
+}
+__device__ inline uint32_t to_codes(const f32x8_t& v, float s) {
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0, v[0], v[1], s, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
+}
+// and back, rounded once to T
+__device__ inline void from_codes(uint32_t c, float s, bf16x8_t* v) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2), e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3);
+  *v = bf16x8_t{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+}
+__device__ inline void from_codes(uint32_t c, float s, f32x8_t* v) {
+  const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+  const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2), e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+  *v = f32x8_t{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
+}
+__device__ inline void from_codes(uint32_t c, float s, f16x8_t* v) {
+  const f16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 1);
+  const f16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 2), e = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 3);
+  *v = f16x8_t{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
 
-// 16 threads a unit, 8 consecutive values each, 4 threads a block.  grid: ceil(rows * units / 16).
-template <typename T, bool VEC>
+// Pieces of 8 values, 4 a block and 16 a unit.  A workgroup takes 1024 consecutive ones, a thread 4 of them 256 apart, whose
+// loads are all under way before the first is used.  ROWS_FLAT: the rows of both sides follow each other without a gap, so
+// that the number of a piece is its place; ROWS_VECTORS: whole pieces are read at once; ROWS_ANY: value by value.
+enum { ROWS_ANY, ROWS_VECTORS, ROWS_FLAT };
+constexpr int kPieces = 4;
+
+// where a piece is: its row and first value in the row
+__device__ inline void piece_at(const Mx4Rows& a, uint32_t i, int64_t* row, int64_t* k0, int64_t* unit) {
+  const uint32_t u = i >> 4, r = u / (uint32_t)a.units;
+  *row = r;
+  *unit = u - r * (uint32_t)a.units;
+  *k0 = *unit * 128 + (i & 15) * 8;
+}
+
+template <typename T, int MODE>
 __global__ void __launch_bounds__(256)
 k_mx4_quantize(Mx4Rows a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, u = i >> 4;
-  if (u >= a.rows * a.units) return;
-  const int64_t row = u / a.units;
-  const int unit = (int)(u - row * a.units), part = threadIdx.x & 15;
-  if (a.offsets && (a.row0 + row < a.offsets[0] || a.row0 + row >= a.offsets[a.groups])) return;  // rows in no group are not read
-  const int64_t k0 = (int64_t)unit * 128 + part * 8;
-  const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx + k0;
-  float v[8];
-  if (VEC && k0 + 8 <= a.k) {
-    typedef T V8 __attribute__((ext_vector_type(8)));
-    const V8 r = *reinterpret_cast<const V8*>(x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (float)r[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = k0 + e < a.k ? (float)x[e] : 0.f;
+  typedef typename Vec8<T>::V V8;
+  const uint32_t i0 = blockIdx.x * (256 * kPieces) + threadIdx.x;
+  uint32_t lo = 0, hi = (uint32_t)(a.rows * a.units * 16);
+  if (a.offsets) {  // rows in no group are not read
+    const int64_t per = a.units * 16;
+    lo = (uint32_t)(min(max((int64_t)a.offsets[0] - a.row0, (int64_t)0), a.rows) * per);
+    hi = (uint32_t)(min(max((int64_t)a.offsets[a.groups] - a.row0, (int64_t)0), a.rows) * per);
   }
-  uint32_t top = 0;
+  if (lo >= hi) return;
+  const T* x = reinterpret_cast<const T*>(a.x);
+  V8 v[kPieces];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
-  top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-  top = max(top, (uint32_t)__shfl_xor((int)top, 2));
-  const int scale = mx4_scale(top);
-  const float inv = mx4_inverse(scale);
-  uint32_t c = 0;
-  if (scale != kNaNScale) {
+  for (int p = 0; p < kPieces; ++p) {
+    const uint32_t i = min(max(i0 + p * 256, lo), hi - 1);  // outside: the nearest piece again, which is not used
+    v[p] = V8{};
+    if constexpr (MODE == ROWS_FLAT) {
+      v[p] = *reinterpret_cast<const V8*>(x + (int64_t)i * 8);
+    } else {
+      int64_t row, k0, unit;
+      piece_at(a, i, &row, &k0, &unit);
+      const T* at = x + row * a.ldx + k0;
+      if (MODE == ROWS_VECTORS && k0 + 8 <= a.k) {
+        v[p] = *reinterpret_cast<const V8*>(at);
+      } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c |= mx4_code(v[e] * inv) << (4 * e);
+        for (int e = 0; e < 8; ++e)
+          if (k0 + e < a.k) v[p][e] = at[e];
+      }
+    }
   }
-  *reinterpret_cast<uint32_t*>(a.codes + row * a.ldc + (int64_t)unit * 64 + part * 4) = c;
-  if ((part & 3) == 0) a.scales[row * a.lds + (int64_t)unit * 4 + (part >> 2)] = (uint8_t)scale;
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const uint32_t i = i0 + p * 256;
+    const int scale = block_scale(v[p]);  // lo, hi and the end are multiples of 16: a quad is inside or not
+    const uint32_t c = scale == kNaNScale ? 0u : to_codes(v[p], scale_value(scale));
+    if (i < lo || i >= hi) continue;
+    if constexpr (MODE == ROWS_FLAT) {
+      *reinterpret_cast<uint32_t*>(a.codes + (int64_t)i * 4) = c;
+      if ((threadIdx.x & 3) == 0) a.scales[i >> 2] = (uint8_t)scale;
+    } else {
+      int64_t row, k0, unit;
+      piece_at(a, i, &row, &k0, &unit);
+      *reinterpret_cast<uint32_t*>(a.codes + row * a.ldc + unit * 64 + (i & 15) * 4) = c;
+      if ((threadIdx.x & 3) == 0) a.scales[row * a.lds + unit * 4 + ((i & 15) >> 2)] = (uint8_t)scale;
+    }
+  }
 }
 
-// the same threads back
-template <typename T, bool VEC>
+template <typename T, int MODE>
 __global__ void __launch_bounds__(256)
 k_mx4_dequantize(Mx4Rows a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, u = i >> 4;
-  if (u >= a.rows * a.units) return;
-  const int64_t row = u / a.units;
-  const int unit = (int)(u - row * a.units), part = threadIdx.x & 15;
-  const int64_t k0 = (int64_t)unit * 128 + part * 8;
-  if (k0 >= a.k) return;
-  const uint32_t c = *reinterpret_cast<const uint32_t*>(a.codes + row * a.ldc + (int64_t)unit * 64 + part * 4);
-  const int scale = a.scales[row * a.lds + (int64_t)unit * 4 + (part >> 2)];
-  T* y = reinterpret_cast<T*>(a.y) + row * a.ldy + k0;
-  typedef T V8 __attribute__((ext_vector_type(8)));
-  V8 r;
+  typedef typename Vec8<T>::V V8;
+  const uint32_t i0 = blockIdx.x * (256 * kPieces) + threadIdx.x, hi = (uint32_t)(a.rows * a.units * 16);
+  uint32_t c[kPieces];
+  int scale[kPieces];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = (T)mx4_value(c >> (4 * e) & 15, scale);
-  if (VEC && k0 + 8 <= a.k) {
-    *reinterpret_cast<V8*>(y) = r;
-  } else {
+  for (int p = 0; p < kPieces; ++p) {
+    const uint32_t i = min(i0 + p * 256, hi - 1);
+    if constexpr (MODE == ROWS_FLAT) {
+      c[p] = *reinterpret_cast<const uint32_t*>(a.codes + (int64_t)i * 4);
+      scale[p] = a.scales[i >> 2];
+    } else {
+      int64_t row, k0, unit;
+      piece_at(a, i, &row, &k0, &unit);
+      c[p] = *reinterpret_cast<const uint32_t*>(a.codes + row * a.ldc + unit * 64 + (i & 15) * 4);
+      scale[p] = a.scales[row * a.lds + unit * 4 + ((i & 15) >> 2)];
+    }
+  }
+  T* y = reinterpret_cast<T*>(a.y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (k0 + e < a.k) y[e] = r[e];
+  for (int p = 0; p < kPieces; ++p) {
+    const uint32_t i = i0 + p * 256;
+    if (i >= hi) continue;
+    V8 v;
+    from_codes(c[p], scale_value(scale[p]), &v);
+    if (scale[p] == kNaNScale) v = (V8)(T)__builtin_nanf("");
+    if constexpr (MODE == ROWS_FLAT) {
+      *reinterpret_cast<V8*>(y + (int64_t)i * 8) = v;
+    } else {
+      int64_t row, k0, unit;
+      piece_at(a, i, &row, &k0, &unit);
+      T* at = y + row * a.ldy + k0;
+      if (MODE == ROWS_VECTORS && k0 + 8 <= a.k) {
+        *reinterpret_cast<V8*>(at) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (k0 + e < a.k) at[e] = v[e];
+      }
+    }
   }
 }
 
@@ -396,17 +498,22 @@ int64_t mx4_units(int64_t k) { return ceil_div(k, 128); }
 
 namespace {
 
-// calls f(type, rows) over parts of the rows that a grid holds (its threads stay below 2^32)
+// calls f(rows, grid, mode) over parts of the rows that a grid and 32 bits hold; v: the 16-bit or fp32 side
 template <typename F>
-void over_rows(const Mx4Rows& a, int64_t x_bytes, F f) {
+void over_rows(const Mx4Rows& a, const void* v, int64_t ldv, int64_t bytes, F f) {
+  const bool vectors = (uintptr_t)v % (8 * bytes) == 0 && (ldv % 8 == 0 || a.rows == 1);
+  const bool flat = vectors && (a.rows == 1 || (ldv == a.k && a.ldc == a.units * 64 && a.lds == a.units * 4)) && a.k % 128 == 0;
   const int64_t most = std::max<int64_t>(1, ((int64_t)1 << 27) / a.units);
   for (int64_t r = 0; r < a.rows; r += most) {
     Mx4Rows p = a;
     p.row0 = r, p.rows = std::min(most, a.rows - r);
-    if (a.x) p.x = static_cast<const char*>(a.x) + r * a.ldx * x_bytes;
-    if (a.y) p.y = static_cast<char*>(a.y) + r * a.ldy * x_bytes;
+    if (a.x) p.x = static_cast<const char*>(a.x) + r * a.ldx * bytes;
+    if (a.y) p.y = static_cast<char*>(a.y) + r * a.ldy * bytes;
     p.codes = a.codes + r * a.ldc, p.scales = a.scales + r * a.lds;
-    f(p, dim3((unsigned)ceil_div(p.rows * a.units, 16)));
+    const dim3 g((unsigned)ceil_div(p.rows * a.units * 16, 256 * kPieces));
+    if (flat) f(p, g, std::integral_constant<int, ROWS_FLAT>{});
+    else if (vectors) f(p, g, std::integral_constant<int, ROWS_VECTORS>{});
+    else f(p, g, std::integral_constant<int, ROWS_ANY>{});
   }
 }
 template <typename F>
@@ -421,10 +528,8 @@ void with_row_type(int dtype, F f) {
 hipError_t launch_mx4_quantize(const Mx4Rows& a, hipStream_t s) {
   with_row_type(a.dtype, [&](auto t) {
     typedef decltype(t) T;
-    const bool vec = (uintptr_t)a.x % (8 * sizeof(T)) == 0 && a.ldx % 8 == 0;  // 8 values at a time
-    over_rows(a, sizeof(T), [&](const Mx4Rows& p, dim3 g) {
-      if (vec) hipLaunchKernelGGL((k_mx4_quantize<T, true>), g, dim3(256), 0, s, p);
-      else hipLaunchKernelGGL((k_mx4_quantize<T, false>), g, dim3(256), 0, s, p);
+    over_rows(a, a.x, a.ldx, sizeof(T), [&](const Mx4Rows& p, dim3 g, auto mode) {
+      hipLaunchKernelGGL((k_mx4_quantize<T, decltype(mode)::value>), g, dim3(256), 0, s, p);
     });
   });
   return hipGetLastError();
@@ -433,10 +538,8 @@ hipError_t launch_mx4_quantize(const Mx4Rows& a, hipStream_t s) {
 hipError_t launch_mx4_dequantize(const Mx4Rows& a, hipStream_t s) {
   with_row_type(a.dtype, [&](auto t) {
     typedef decltype(t) T;
-    const bool vec = (uintptr_t)a.y % (8 * sizeof(T)) == 0 && a.ldy % 8 == 0;
-    over_rows(a, sizeof(T), [&](const Mx4Rows& p, dim3 g) {
-      if (vec) hipLaunchKernelGGL((k_mx4_dequantize<T, true>), g, dim3(256), 0, s, p);
-      else hipLaunchKernelGGL((k_mx4_dequantize<T, false>), g, dim3(256), 0, s, p);
+    over_rows(a, a.y, a.ldy, sizeof(T), [&](const Mx4Rows& p, dim3 g, auto mode) {
+      hipLaunchKernelGGL((k_mx4_dequantize<T, decltype(mode)::value>), g, dim3(256), 0, s, p);
     });
   });
   return hipGetLastError();
