@@ -239,8 +239,8 @@ k_mx4_tile(Mx4Args a) {
   constexpr int TM = BM / C::WM, TN = BN / C::WN, MT = TM / 16, NT = TN / 16;
   constexpr int HALVES = GLU ? 2 : 1, NTH = NT / HALVES, TNH = TN / HALVES, BNH = BN / HALVES, RUN = NTH * 4;
   constexpr int XB = BM * 128, WB = BN * 128, STEP = XB + WB, SCALES = (BM + BN) * 16;
-  constexpr int SX = BM * CK / TH, SW = BN * CK / TH, CP = SX + SW;
-  static_assert(C::BK == 64 && BM * CK % TH == 0 && BN * CK % TH == 0 && (BM + BN) * 4 % TH == 0 && NT % HALVES == 0, "tile");
+  constexpr int SX = BM * CK / TH, SW = BN * CK / TH, SC = (BM + BN) * 4 / TH, CP = SX + SW;  // copies of one thread per step, SC every other one
+  static_assert(C::BK == 64 && BM * CK % TH == 0 && BN * CK % TH == 0 && BM * 4 % TH == 0 && BN * 4 % TH == 0 && TNH % 16 == 0 && NT % HALVES == 0, "tile");
   extern __shared__ __attribute__((aligned(128))) uint8_t s_tile[];
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -269,60 +269,48 @@ k_mx4_tile(Mx4Args a) {
   }
   const int64_t n0 = (int64_t)nt_i * BNH;
 
-  // this thread's copies: byte offsets from uniform addresses (plan_mx4 keeps them < 2^32)
+  // this thread's copies: byte offsets from uniform addresses that advance with the steps (plan_mx4 keeps them < 2^32)
   const uint8_t *bx = a.x + m0 * a.ldx + (int64_t)u0 * 64, *bw = a.w + g * a.sw + n0 * a.ldw + (int64_t)u0 * 64;
   const int64_t up_codes = GLU ? e.N * a.ldw : 0;
   const int bytes = (u1 - u0) * 64;
-  uint32_t ox[SX], ow[SW];
-  int kx[SX], kw[SW];  // the copy's first byte inside a step
+  uint32_t ox[SX], ow[SW], os[SC];
+  const int cx = (tid % CK) ^ swz_rows<64, 1>(tid / CK), cw = (tid % CK) ^ swz_rows<64, RUN>(tid / CK);  // the chunk of every copy
+  static_assert(TH / CK % 8 == 0 && TH / CK % (2 * RUN) == 0, "copies TH / CK rows apart have the same chunk");
+  auto w_col = [&](int row) { return min((int64_t)((row / TN) * TNH + row % TNH), e.N - 1 - n0); };  // of an LDS row, from n0
 #pragma unroll
-  for (int i = 0; i < SX; ++i) {
-    const int idx = i * TH + tid, row = idx / CK, c = (idx % CK) ^ swz_rows<64, 1>(row);
-    kx[i] = c * 16;
-    ox[i] = (uint32_t)(min((int64_t)row, m1 - 1 - m0) * a.ldx + c * 16);
-  }
+  for (int i = 0; i < SX; ++i) ox[i] = (uint32_t)(min((int64_t)((i * TH + tid) / CK), m1 - 1 - m0) * a.ldx + cx * 16);
 #pragma unroll
-  for (int i = 0; i < SW; ++i) {
-    const int idx = i * TH + tid, row = idx / CK, c = (idx % CK) ^ swz_rows<64, RUN>(row);
-    const int col = (row / TN) * TNH + (row % TNH);
-    kw[i] = c * 16;
-    ow[i] = (uint32_t)(min((int64_t)col, e.N - 1 - n0) * a.ldw + c * 16);
+  for (int i = 0; i < SW; ++i) ow[i] = (uint32_t)(w_col((i * TH + tid) / CK) * a.ldw + cw * 16);
+#pragma unroll
+  for (int i = 0; i < SC; ++i) {
+    const int row = (i * TH + tid) / 4;
+    os[i] = (uint32_t)((row < BM ? min((int64_t)row, m1 - 1 - m0) * a.ldxs : w_col(row - BM) * a.ldws) + (tid & 3) * 4);
   }
+  const uint8_t *bxs = a.xs + m0 * a.ldxs + u0 * 4, *bws = a.ws + g * a.sws + n0 * a.ldws + u0 * 4;
+  const int64_t up_scales = GLU ? e.N * a.ldws : 0;
   const uint32_t lds0 = lds_address(s_tile), lds_s = lds0 + S * STEP;
   const int steps = (u1 - u0 + 1) / 2;
-  const char* zero = reinterpret_cast<const char*>(g_zero16);
 
+  // Where a row ends inside a step its last unit (or the first one, of the scales) is copied once more; drop() takes it out.
   auto issue = [&](int t) __attribute__((always_inline)) {
     const uint32_t base = lds0 + (t % S) * STEP + wave * 1024;
     const int left = min(128, bytes - t * 128);
     const uint8_t *sx = bx + (int64_t)t * 128, *sw = bw + (int64_t)t * 128;
+    // a wave copies whole rows, on one side of a tile's gate and up rows
     auto side = [&](int i) { return GLU && ((i * TH + wave * 64) / CK) % TN >= TNH ? sw + up_codes : sw; };
-    if (left == 128) {
+    const uint32_t back_x = left < 128 && cx >= 4 ? 64 : 0, back_w = left < 128 && cw >= 4 ? 64 : 0;
 #pragma unroll
-      for (int i = 0; i < SX; ++i) lds_copy16(sx, ox[i], base + i * (TH * 16));
+    for (int i = 0; i < SX; ++i) lds_copy16(sx, ox[i] - back_x, base + i * (TH * 16));
 #pragma unroll
-      for (int i = 0; i < SW; ++i) lds_copy16(side(i), ow[i], base + XB + i * (TH * 16));
-    } else {
+    for (int i = 0; i < SW; ++i) lds_copy16(side(i), ow[i] - back_w, base + XB + i * (TH * 16));
+    if (t % 2 == 0) {  // the scales of steps t and t + 1, 4 units: a wave's copy has 16 rows of 4 times 4 bytes
+      const uint32_t at = lds_s + (t / 2 % 2) * SCALES + wave * 256;
+      const int units = u1 - u0 - t * 2;
+      const uint8_t *sxs = bxs + (int64_t)t * 8, *sws = bws + (int64_t)t * 8;
+      auto from = [&](int i) { return i * (TH / 4) < BM ? sxs : GLU && (i * (TH / 4) + wave * 16 - BM) % TN >= TNH ? sws + up_scales : sws; };
+      const uint32_t back = (tid & 3) < units ? 0 : (tid & 3) * 4;
 #pragma unroll
-      for (int i = 0; i < SX; ++i) lds_copy16(kx[i] < left ? (const char*)sx + ox[i] : zero, base + i * (TH * 16));
-#pragma unroll
-      for (int i = 0; i < SW; ++i) lds_copy16(kw[i] < left ? (const char*)side(i) + ow[i] : zero, base + XB + i * (TH * 16));
-    }
-    if (t % 2 == 0) {  // the scales of steps t and t + 1, 4 units
-      const uint32_t at = lds_s + (t / 2 % 2) * SCALES;
-      const int u = u0 + t * 2, n = min(4, u1 - u);
-#pragma unroll
-      for (int c = 0; c < (BM + BN) * 4 / TH; ++c) {  // a wave's copy: 16 rows of 4 bytes x 4
-        const int i = c * (TH / 4) + wave * 16, row = i + (lane >> 2), unit = lane & 3;
-        const uint8_t* p;
-        if (row < BM) {
-          p = a.xs + (m0 + min((int64_t)row, m1 - 1 - m0)) * a.ldxs;
-        } else {
-          const int w = row - BM, col = (w / TN) * TNH + (w % TNH);
-          p = a.ws + g * a.sws + ((w % TN >= TNH ? e.N : 0) + n0 + min((int64_t)col, e.N - 1 - n0)) * a.ldws;
-        }
-        lds_copy4(unit < n ? (const char*)p + (u + unit) * 4 : zero, at + i * 16);
-      }
+      for (int i = 0; i < SC; ++i) lds_copy4(from(i), os[i] - back, at + i * (TH * 4));
     }
   };
 
@@ -347,41 +335,117 @@ k_mx4_tile(Mx4Args a) {
   };
   auto buffer = [&](int t) { return s_tile + (t % S) * STEP; };
 
+  // this wave's operands of a step's instruction ks
+  i32x4_t fw[2][NT], fx[MT];
+  int sw[NT], sx[MT];
+  auto read_w = [&](int into, int t, int ks) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fw[into][j] = frag_w(buffer(t), j, ks);
+  };
+  auto products = [&](auto ks, int i) __attribute__((always_inline)) {
+    constexpr int B = decltype(ks)::value;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = mfma4<B>(fw[B][j], fx[i], acc[i][j], sw[j], sx[i]);
+    if constexpr (C::AHEAD) {
+      // the products stay on this side of the barrier and of the branches around it (no instruction, only a use of the sums),
+      // and an operand is read again behind them, not into a second register
+#pragma unroll
+      for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // the last step's second unit where there is none: zeros on W's side, for the lanes q >= 2 that hold it
+  const bool odd = (u1 - u0) & 1;
+  auto drop = [&](int set) __attribute__((always_inline)) {
+    if (odd && q >= 2) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fw[set][j] = i32x4_t{0, 0, 0, 0}, sw[j] = 0;
+    }
+  };
+  const std::integral_constant<int, 0> first;
+  const std::integral_constant<int, 1> second;
 #pragma unroll
   for (int t = 0; t < S - 1; ++t)
     if (t < steps) issue(t);
-  for (int t = 0; t < steps; ++t) {
-    // copies issued after step t's: at least CP for every later step (scales beside, which only makes the wait stricter)
-    if (t + S - 1 > steps) vm_wait<0>();
-    else vm_wait<(S - 2) * CP>();
+  if constexpr (C::AHEAD) {
+    // as in k_mm_tile: an x operand is read again as soon as its products are issued, the w operands half a step ahead into a
+    // second set, and the barrier of a step stands inside the last half's products
+    static_assert(S == 2, "two buffers");
+    constexpr int LATE = 2;  // x operands whose products stand before the barrier
+    vm_wait<0>();
     meet();
-    if (t + S - 1 < steps) issue(t + S - 1);
-    int sx[MT], sw[NT];
+    if (steps > 1) issue(1);
+    read_w(0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) sx[i] = scale_of(t, x_row(i));
+    for (int j = 0; j < NT; ++j) sw[j] = scale_of(0, BM + w_row(j));
 #pragma unroll
-    for (int j = 0; j < NT; ++j) sw[j] = scale_of(t, BM + w_row(j));
-    {
-      i32x4_t fw[NT], fx[MT];
-#pragma unroll
-      for (int j = 0; j < NT; ++j) fw[j] = frag_w(buffer(t), j, 0);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fx[i] = frag_x(buffer(t), i, 0);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mfma4<0>(fw[j], fx[i], acc[i][j], sw[j], sx[i]);
+    for (int i = 0; i < MT; ++i) {
+      sx[i] = scale_of(0, x_row(i));
+      fx[i] = frag_x(buffer(0), i, 0);
     }
-    {
-      i32x4_t fw[NT], fx[MT];
+    for (int t = 0; t < steps - 1; ++t) {
+      read_w(1, t, 1);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) fw[j] = frag_w(buffer(t), j, 1);
+      for (int i = 0; i < MT; ++i) {
+        products(first, i);
+        fx[i] = frag_x(buffer(t), i, 1);
+      }
 #pragma unroll
-      for (int i = 0; i < MT; ++i) fx[i] = frag_x(buffer(t), i, 1);
+      for (int i = 0; i < LATE; ++i) products(second, i);
+      vm_wait<0>();
+      meet();  // step t + 1 is in LDS and step t in registers
+      if (t + 2 < steps) issue(t + 2);
+      read_w(0, t + 1, 0);
+      int next[NT];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int j = 0; j < NT; ++j) next[j] = scale_of(t + 1, BM + w_row(j));
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mfma4<1>(fw[j], fx[i], acc[i][j], sw[j], sx[i]);
+      for (int i = 0; i < LATE; ++i) {
+        sx[i] = scale_of(t + 1, x_row(i));
+        fx[i] = frag_x(buffer(t + 1), i, 0);
+      }
+#pragma unroll
+      for (int i = LATE; i < MT; ++i) {
+        products(second, i);
+        sx[i] = scale_of(t + 1, x_row(i));
+        fx[i] = frag_x(buffer(t + 1), i, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) sw[j] = next[j];
+    }
+    read_w(1, steps - 1, 1);
+    drop(0);
+    drop(1);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      products(first, i);
+      fx[i] = frag_x(buffer(steps - 1), i, 1);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) products(second, i);
+  } else {
+    for (int t = 0; t < steps; ++t) {
+      // copies issued after step t's: at least CP for every later step (scales beside, which only makes the wait stricter)
+      if (t + S - 1 > steps) vm_wait<0>();
+      else vm_wait<(S - 2) * CP>();
+      meet();
+      if (t + S - 1 < steps) issue(t + S - 1);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) sx[i] = scale_of(t, x_row(i));
+#pragma unroll
+      for (int j = 0; j < NT; ++j) sw[j] = scale_of(t, BM + w_row(j));
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        read_w(ks, t, ks);
+        if (t == steps - 1) drop(ks);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) fx[i] = frag_x(buffer(t), i, ks);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          if (ks == 0) products(first, i);
+          else products(second, i);
+        }
+      }
     }
   }
   store_tile<T, C, true, GLU>(e, acc, s_tile, g, m0, m1, n0);
@@ -549,7 +613,7 @@ namespace {
 
 // ---- which kernel ----------------------------------------------------------------------------------------
 
-typedef TileCfg<256, 256, 2, 4, 64, 2, false> MxBig;
+typedef TileCfg<256, 256, 2, 4, 64, 2, true> MxBig;
 typedef TileCfg<128, 128, 2, 2, 64, 2, false> MxMid;
 typedef TileCfg<64, 128, 1, 4, 64, 3, false> MxLow;
 
