@@ -497,7 +497,10 @@ struct Mx4Args {
   int64_t ldx, ldxs, ldw, ldws, sw, sws;  // bytes between rows, and between groups
   int units;
 };
+// Which kernel a product takes: W streamed past 16, 32 or 64 rows, or tiles of 256 x 256, 128 x 128, 64 x 128 or 16 x 128.
+enum { MX_FEW1, MX_FEW2, MX_FEW4, MX_BIG, MX_MID, MX_LOW, MX_THIN };
+int mx4_choice(const eff_mx4_desc& d);
+int mx4_choice(const Mx4Args& a);
 bool mx4_matmul_fits(const Mx4Args& a);
-int64_t mx4_matmul_workspace(const Mx4Args& a);
-hipError_t launch_mx4_matmul(const Mx4Args& a, void* workspace, hipStream_t s);
+hipError_t launch_mx4_matmul(const Mx4Args& a, hipStream_t s);
 }  // namespace eff

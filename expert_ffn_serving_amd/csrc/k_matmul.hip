@@ -402,6 +402,36 @@ k_mm_tile(MmArgs a) {
   store_tile<T, C, WK, GLU>(a, acc, s_tile, g, m0, m1, n0);
 }
 
+// A split k's sums added in order of k, and the epilogue (333 x 515, 7 splits: 6 us, a launch and two trips to memory).  grid: ceil(M * vectors / 256); a thread takes 8 columns.
+template <typename T, bool GLU>
+__global__ void __launch_bounds__(256)
+k_mm_join(MmArgs a, int splits) {
+  const int64_t vr = (a.N + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.M * vr) return;
+  const int64_t m = i / vr, n = i % vr * 8;
+  float z[8], u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = u[e] = 0.f;
+  const float* p = a.part + m * a.ldpart + n;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s, p += a.M * a.ldpart)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + 4 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[4 * h + e] += v[e];
+      if (GLU) {
+        const f32x4_t v2 = *reinterpret_cast<const f32x4_t*>(p + a.ldpart / 2 + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[4 * h + e] += v2[e];
+      }
+    }
+  const float back = unscale<T>(a, 0, m);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] *= back;
+  mm_finish<T, 8, GLU>(a, m, n, 0, 0, z, u);
+}
+
 // ---- operands that cannot be copied 16 bytes at a time ---------------------------------------------------
 // rows x cols values with any stride into rows of ceil(cols / 8) * 8 values, zeros behind cols (rows = groups *
 // group_rows), for both operands in one launch.  A thread writes 16 bytes.  Reading and writing the matrix once more

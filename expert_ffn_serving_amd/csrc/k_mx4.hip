@@ -232,15 +232,25 @@ __device__ inline f32x4_t mfma4(i32x4_t w, i32x4_t x, f32x4_t c, int sw, int sx)
 //
 // Scales come to LDS for two steps at a time, 16 bytes a row (one line of a row holds those of 16 steps: fetched step by step
 // it would be requested as often as the codes' lines): [buffer][row][16], x rows first.
+template <int BM, int BN, int WM, int WN, int S, bool AHEAD>
+using MxCfg = TileCfg<BM, BN, WM, WN, 64, S, AHEAD>;
+
+
+// Buffers of two steps' scales: step t + S - 1 is copied while step t is used, so its buffer's last steps are behind t.
+constexpr int scale_buffers(int S) { return (S + 2) / 2; }
+
 template <typename T, class C, bool GLU>
 __global__ void __launch_bounds__(C::TH)
 k_mx4_tile(Mx4Args a) {
   constexpr int BM = C::BM, BN = C::BN, S = C::S, TH = C::TH, CK = 8, KB = 256;
   constexpr int TM = BM / C::WM, TN = BN / C::WN, MT = TM / 16, NT = TN / 16;
   constexpr int HALVES = GLU ? 2 : 1, NTH = NT / HALVES, TNH = TN / HALVES, BNH = BN / HALVES, RUN = NTH * 4;
-  constexpr int XB = BM * 128, WB = BN * 128, STEP = XB + WB, SCALES = (BM + BN) * 16;
-  constexpr int SX = BM * CK / TH, SW = BN * CK / TH, SC = (BM + BN) * 4 / TH, CP = SX + SW;  // copies of one thread per step, SC every other one
-  static_assert(C::BK == 64 && BM * CK % TH == 0 && BN * CK % TH == 0 && BM * 4 % TH == 0 && BN * 4 % TH == 0 && TNH % 16 == 0 && NT % HALVES == 0, "tile");
+  constexpr int XB = BM * 128, WB = BN * 128, STEP = XB + WB, SCALES = (BM + BN) * 16, SB = scale_buffers(S);
+  // copies of one thread per step, and of scales every other one; where x has fewer rows than that, by the first waves alone
+  constexpr int SX = (BM * CK + TH - 1) / TH, SW = BN * CK / TH, SCX = (BM * 4 + TH - 1) / TH, SCW = BN * 4 / TH;
+  constexpr bool ALL_X = BM * CK % TH == 0, ALL_XS = BM * 4 % TH == 0;
+  constexpr int CP = (ALL_X ? SX : 0) + SW;  // at least
+  static_assert(C::BK == 64 && BN * CK % TH == 0 && BN * 4 % TH == 0 && (ALL_X || SX == 1) && (ALL_XS || SCX == 1) && TNH % 16 == 0 && NT % HALVES == 0, "tile");
   extern __shared__ __attribute__((aligned(128))) uint8_t s_tile[];
   const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -248,48 +258,42 @@ k_mx4_tile(Mx4Args a) {
   const MmArgs& e = a.e;
 
   const int nt = (int)((e.N + BNH - 1) / BNH);
-  int g = 0, mt_i, nt_i, u0 = 0, u1 = a.units;  // units of 128 k
+  int g = 0, nt_i;
   int64_t m0, m1;
   if (e.mode == MM_ROW_GROUPS) {
-    mt_i = blockIdx.x / nt;
     nt_i = blockIdx.x % nt;
-    if (!find_tile<BM>(e.offsets, e.groups, e.M, mt_i, reinterpret_cast<int*>(s_tile), &g, &m0, &m1)) return;
+    if (!find_tile<BM>(e.offsets, e.groups, e.M, blockIdx.x / nt, reinterpret_cast<int*>(s_tile), &g, &m0, &m1)) return;
   } else {
     // an XCD's workgroups take a contiguous part of the tiles, in bands of 8 row tiles, as in k_mm_tile
     const int all = gridDim.x, xcd = blockIdx.x & 7, id = xcd * (all >> 3) + min(xcd, all & 7) + (blockIdx.x >> 3);
     const int mts = all / nt, band = id / (8 * nt), in_band = id - band * 8 * nt, height = min(8, mts - band * 8);
-    mt_i = band * 8 + in_band % height;
     nt_i = in_band / height;
-    m0 = (int64_t)mt_i * BM;
+    m0 = (int64_t)(band * 8 + in_band % height) * BM;
     m1 = min(e.M, m0 + BM);
-    if (e.part) {
-      u0 = blockIdx.y * e.split_steps * 2;
-      u1 = min(a.units, u0 + e.split_steps * 2);
-    }
   }
   const int64_t n0 = (int64_t)nt_i * BNH;
 
   // this thread's copies: byte offsets from uniform addresses that advance with the steps (plan_mx4 keeps them < 2^32)
-  const uint8_t *bx = a.x + m0 * a.ldx + (int64_t)u0 * 64, *bw = a.w + g * a.sw + n0 * a.ldw + (int64_t)u0 * 64;
+  const uint8_t *bx = a.x + m0 * a.ldx, *bw = a.w + g * a.sw + n0 * a.ldw;
   const int64_t up_codes = GLU ? e.N * a.ldw : 0;
-  const int bytes = (u1 - u0) * 64;
-  uint32_t ox[SX], ow[SW], os[SC];
+  const int bytes = a.units * 64;
+  uint32_t ox[SX], ow[SW], osx[SCX], osw[SCW];
   const int cx = (tid % CK) ^ swz_rows<64, 1>(tid / CK), cw = (tid % CK) ^ swz_rows<64, RUN>(tid / CK);  // the chunk of every copy
   static_assert(TH / CK % 8 == 0 && TH / CK % (2 * RUN) == 0, "copies TH / CK rows apart have the same chunk");
-  auto w_col = [&](int row) { return min((int64_t)((row / TN) * TNH + row % TNH), e.N - 1 - n0); };  // of an LDS row, from n0
+  auto x_row_at = [&](int row) { return min((int64_t)row, m1 - 1 - m0); };                                // of an LDS row, from m0
+  auto w_row_at = [&](int row) { return min((int64_t)((row / TN) * TNH + row % TNH), e.N - 1 - n0); };  // and from n0
 #pragma unroll
-  for (int i = 0; i < SX; ++i) ox[i] = (uint32_t)(min((int64_t)((i * TH + tid) / CK), m1 - 1 - m0) * a.ldx + cx * 16);
+  for (int i = 0; i < SX; ++i) ox[i] = (uint32_t)(x_row_at((i * TH + tid) / CK) * a.ldx + cx * 16);
 #pragma unroll
-  for (int i = 0; i < SW; ++i) ow[i] = (uint32_t)(w_col((i * TH + tid) / CK) * a.ldw + cw * 16);
+  for (int i = 0; i < SW; ++i) ow[i] = (uint32_t)(w_row_at((i * TH + tid) / CK) * a.ldw + cw * 16);
 #pragma unroll
-  for (int i = 0; i < SC; ++i) {
-    const int row = (i * TH + tid) / 4;
-    os[i] = (uint32_t)((row < BM ? min((int64_t)row, m1 - 1 - m0) * a.ldxs : w_col(row - BM) * a.ldws) + (tid & 3) * 4);
-  }
-  const uint8_t *bxs = a.xs + m0 * a.ldxs + u0 * 4, *bws = a.ws + g * a.sws + n0 * a.ldws + u0 * 4;
+  for (int i = 0; i < SCX; ++i) osx[i] = (uint32_t)(x_row_at((i * TH + tid) / 4) * a.ldxs + (tid & 3) * 4);
+#pragma unroll
+  for (int i = 0; i < SCW; ++i) osw[i] = (uint32_t)(w_row_at((i * TH + tid) / 4) * a.ldws + (tid & 3) * 4);
+  const uint8_t *bxs = a.xs + m0 * a.ldxs, *bws = a.ws + g * a.sws + n0 * a.ldws;
   const int64_t up_scales = GLU ? e.N * a.ldws : 0;
   const uint32_t lds0 = lds_address(s_tile), lds_s = lds0 + S * STEP;
-  const int steps = (u1 - u0 + 1) / 2;
+  const int steps = (a.units + 1) / 2;
 
   // Where a row ends inside a step its last unit (or the first one, of the scales) is copied once more; drop() takes it out.
   auto issue = [&](int t) __attribute__((always_inline)) {
@@ -300,17 +304,21 @@ k_mx4_tile(Mx4Args a) {
     auto side = [&](int i) { return GLU && ((i * TH + wave * 64) / CK) % TN >= TNH ? sw + up_codes : sw; };
     const uint32_t back_x = left < 128 && cx >= 4 ? 64 : 0, back_w = left < 128 && cw >= 4 ? 64 : 0;
 #pragma unroll
-    for (int i = 0; i < SX; ++i) lds_copy16(sx, ox[i] - back_x, base + i * (TH * 16));
+    for (int i = 0; i < SX; ++i)
+      if (ALL_X || wave * 64 < BM * CK) lds_copy16(sx, ox[i] - back_x, base + i * (TH * 16));
 #pragma unroll
     for (int i = 0; i < SW; ++i) lds_copy16(side(i), ow[i] - back_w, base + XB + i * (TH * 16));
     if (t % 2 == 0) {  // the scales of steps t and t + 1, 4 units: a wave's copy has 16 rows of 4 times 4 bytes
-      const uint32_t at = lds_s + (t / 2 % 2) * SCALES + wave * 256;
-      const int units = u1 - u0 - t * 2;
+      const uint32_t at = lds_s + (t / 2 % SB) * SCALES + wave * 256;
+      const int units = a.units - t * 2;
       const uint8_t *sxs = bxs + (int64_t)t * 8, *sws = bws + (int64_t)t * 8;
-      auto from = [&](int i) { return i * (TH / 4) < BM ? sxs : GLU && (i * (TH / 4) + wave * 16 - BM) % TN >= TNH ? sws + up_scales : sws; };
       const uint32_t back = (tid & 3) < units ? 0 : (tid & 3) * 4;
 #pragma unroll
-      for (int i = 0; i < SC; ++i) lds_copy4(from(i), os[i] - back, at + i * (TH * 4));
+      for (int i = 0; i < SCX; ++i)
+        if (ALL_XS || wave * 64 < BM * 4) lds_copy4(sxs, osx[i] - back, at + i * (TH * 4));
+#pragma unroll
+      for (int i = 0; i < SCW; ++i)
+        lds_copy4(GLU && (i * (TH / 4) + wave * 16) % TN >= TNH ? sws + up_scales : sws, osw[i] - back, at + BM * 16 + i * (TH * 4));
     }
   };
 
@@ -331,7 +339,7 @@ k_mx4_tile(Mx4Args a) {
     return *reinterpret_cast<const i32x4_t*>(b + XB + row * 128 + (((2 * q + ks) ^ swz_rows<64, RUN>(row)) << 4));
   };
   auto scale_of = [&](int t, int row) -> int {
-    return *reinterpret_cast<const uint16_t*>(s_tile + S * STEP + (t / 2 % 2) * SCALES + row * 16 + (t & 1) * 8 + q * 2);
+    return *reinterpret_cast<const uint16_t*>(s_tile + S * STEP + (t / 2 % SB) * SCALES + row * 16 + (t & 1) * 8 + q * 2);
   };
   auto buffer = [&](int t) { return s_tile + (t % S) * STEP; };
 
@@ -355,7 +363,7 @@ k_mx4_tile(Mx4Args a) {
     }
   };
   // the last step's second unit where there is none: zeros on W's side, for the lanes q >= 2 that hold it
-  const bool odd = (u1 - u0) & 1;
+  const bool odd = a.units & 1;
   auto drop = [&](int set) __attribute__((always_inline)) {
     if (odd && q >= 2) {
 #pragma unroll
@@ -448,7 +456,10 @@ k_mx4_tile(Mx4Args a) {
       }
     }
   }
-  store_tile<T, C, true, GLU>(e, acc, s_tile, g, m0, m1, n0);
+  // through LDS where there is more to do than SwiGLU and a residual, whose code would stand there for every piece
+  if (e.simple) store_regs<T, C, GLU, true>(e, acc, g, m0, m1, n0);
+  else if constexpr (C::BM < 64) store_regs<T, C, GLU, false>(e, acc, g, m0, m1, n0);
+  else store_tile<T, C, true, GLU>(e, acc, s_tile, g, m0, m1, n0);
 }
 
 // ---- few rows --------------------------------------------------------------------------------------------
@@ -457,7 +468,7 @@ k_mx4_tile(Mx4Args a) {
 // k_mm_few does for 16 bits: every wave keeps U chunks of 256 k (2 KiB of W each) in flight in registers, nothing waits for a
 // barrier before the end, where the waves' sums meet in LDS in wave order.
 template <int MT>
-constexpr int mx4_unroll() { return MT == 1 ? 4 : 2; }
+constexpr int mx4_unroll() { return MT >= 4 ? 1 : 2; }
 
 template <typename T, int MT, bool GLU>
 __global__ void __launch_bounds__(1024)
@@ -613,74 +624,66 @@ namespace {
 
 // ---- which kernel ----------------------------------------------------------------------------------------
 
-typedef TileCfg<256, 256, 2, 4, 64, 2, true> MxBig;
-typedef TileCfg<128, 128, 2, 2, 64, 2, false> MxMid;
-typedef TileCfg<64, 128, 1, 4, 64, 3, false> MxLow;
-
-enum { MX_FEW1, MX_FEW2, MX_BIG, MX_MID, MX_LOW };
-
-struct MxPlan {
-  int kind, splits;
-  int64_t part;  // workspace bytes
-};
+typedef MxCfg<256, 256, 2, 4, 2, true> MxBig;
+typedef MxCfg<128, 128, 2, 2, 2, false> MxMid;
+typedef MxCfg<64, 128, 1, 4, 3, false> MxLow;
+typedef MxCfg<16, 128, 1, 4, 4, false> MxThin;
 
 int64_t mx4_rows(const MmArgs& e, int64_t BM) { return e.mode == MM_ROW_GROUPS ? group_tiles(e.M, e.groups, BM) : ceil_div(e.M, BM); }
 
-MxPlan plan_mx4(const Mx4Args& a) {
+// An estimate of each kernel's time in us, with constants fitted to what they take forced everywhere (warm, 256 CUs).
+// Streamed, 16, 32 or 64 rows at a time: a launch and the way to memory, and W once per row tile from the caches.  4096 ->
+// 4096, 16 / 32 / 64 rows at a time and 64 x 128 tiles: 1 row 5.6, 5.8, 6.4, 11; 16 rows 6.6, 6.9, 7.4, 13; 32 rows 9.3, 8.0,
+// 8.4, 13; 64 rows -, 12.1, 10.8, 13.4; 128 rows -, 20, -, 13.5.  2563 -> 520, 256 rows -, 7.4, 6.3, 10.3; 512 rows -, 9.3, 8.9,
+// 10.3; 1024 rows -, -, 11.5, 10.5.  A k split over workgroups and joined never won (4096 -> 4096, 64 rows, 4 parts 12.3).
+// Tiles: rounds of workgroups (`occ` on a CU, slower each when they share it) of so many steps and a start and end.  64 x 128,
+// 128 x 128 and 256 x 256: 4096 -> 4096, 1024 rows 19.4, 21.3, 36; 2048 rows 35, 30, 38; 4096 rows 66, 56, 43; 256 experts of 16,
+// 48, 64, 96 and 128 rows, 4096 -> 2 x 2048: 388, 486, 669; 457, 513, 683; 539, 526, 690; 647, 600, 709; 776, 740, 729.
+// Groups of up to 8 rows stream W in 16 x 128 tiles, four steps of it in LDS: 512 groups, 2560 -> 2 x 640, a row each 134 and
+// 138 (64 x 128); 4 rows 155 and 160; 16 rows 203 and 177.
+int plan_mx4(const Mx4Args& a) {
   const MmArgs& e = a.e;
-  const bool glu = e.act == EFF_ACT_SWIGLU;
-  const int64_t n = glu ? 2 * e.N : e.N, groups = std::max<int64_t>(1, e.groups);
-  const int64_t rows = e.mode == MM_ROW_GROUPS ? e.M / std::max<int64_t>(1, std::min(groups, e.M)) : e.M;
-  const bool fill = mx4_rows(e, MxLow::BM) * ceil_div(n, MxLow::BN) >= 512;
-  if (rows <= 16 && !fill) return {MX_FEW1, 1, 0};
-  if (rows <= 32 && !fill) return {MX_FEW2, 1, 0};
+  const bool grouped = e.mode == MM_ROW_GROUPS;
+  const int64_t n = e.act == EFF_ACT_SWIGLU ? 2 * e.N : e.N, groups = grouped ? std::min<int64_t>(e.groups, std::max<int64_t>(1, e.M)) : 1;
+  const int64_t rows = e.M / groups, steps = ceil_div(a.units, 2);
+  int best = MX_FEW4;  // any size
+  double least = 0;
+  auto offer = [&](int kind, double us) {
+    if (least == 0 || us < least) least = us, best = kind;
+  };
+  const double mb = (double)n * a.units * 68e-6;  // W of a group, as it lies in memory
+  const struct { int kind; int64_t rows; double us; } few[] = {{MX_FEW1, 16, 0.40}, {MX_FEW2, 32, 0.56}, {MX_FEW4, 64, 0.88}};
+  for (const auto& f : few) offer(f.kind, 3.0 + f.us * mb * groups * ceil_div(std::max<int64_t>(1, rows), f.rows));
   // a tile's lanes hold unsigned 32-bit byte offsets from its first row
-  const int64_t far = std::max(a.ldx, a.ldw);
-  struct Tile { int kind; int64_t bm, bn; int occ; double alone, step, fixed; };
-  const Tile tiles[] = {{MX_BIG, MxBig::BM, MxBig::BN, 1, 1.55, 1.55, 14},
-                        {MX_MID, MxMid::BM, MxMid::BN, 2, 0.75, 1.0, 7},
-                        {MX_LOW, MxLow::BM, MxLow::BN, 2, 0.42, 0.64, 6}};
-  const int64_t steps = ceil_div(a.units, 2);
-  MxPlan p = {MX_FEW2, 1, 0};
-  double best = 0;
-  for (const Tile& t : tiles) {
-    if (far * std::max(t.bm, t.bn) >= (int64_t)1 << 32) continue;
-    double count = (double)ceil_div(n, t.bn);
-    if (e.mode == MM_ROW_GROUPS) count *= std::max<double>((double)ceil_div(rows, t.bm) * std::min(groups, e.M), e.M / (double)t.bm);
-    else count *= (double)ceil_div(e.M, t.bm);
-    for (int64_t s = 1; s <= 16 && (s == 1 || (e.mode == MM_DENSE && s * 4 <= steps)); ++s) {
-      const double each = (double)ceil_div(steps, s), full = std::floor(count * s / (256.0 * t.occ)), rest = count * s - full * 256 * t.occ;
-      double us = full * (t.step * each + t.fixed);
-      if (rest > 0) us += (rest <= 256 ? t.alone : t.step) * each + t.fixed;
-      if (s > 1) us += 5 + s * (double)e.M * n * 8 / 8e6;
-      if (best == 0 || us < best) best = us, p.kind = t.kind, p.splits = (int)s;
-    }
+  const int64_t far = std::max(std::max(a.ldx, a.ldw), std::max(a.ldxs, a.ldws));
+  const struct { int kind; int64_t bm, bn; int occ; double alone, step, fixed; } tiles[] = {
+      {MX_BIG, MxBig::BM, MxBig::BN, 1, 1.65, 1.65, 12}, {MX_MID, MxMid::BM, MxMid::BN, 2, 1.05, 1.5, 4.5},
+      {MX_LOW, MxLow::BM, MxLow::BN, 2, 0.62, 0.9, 3.5}, {MX_THIN, MxThin::BM, MxThin::BN, 2, 0.45, 0.7, 3.3}};
+  for (const auto& t : tiles) {
+    if (far * std::max(t.bm, t.bn) >= (int64_t)1 << 32 || (t.kind == MX_THIN && (!grouped || rows > 8))) continue;
+    const double rt = grouped ? std::max<double>((double)ceil_div(rows, t.bm) * groups, e.M / (double)t.bm) : (double)ceil_div(e.M, t.bm);
+    const double count = rt * ceil_div(n, t.bn), full = std::floor(count / (256.0 * t.occ)), rest = count - full * 256 * t.occ;
+    offer(t.kind, full * (t.step * steps + t.fixed) + (rest > 0 ? (rest <= 256 ? t.alone : t.step) * steps + t.fixed : 0));
   }
-  if (p.splits > 1) {
-    p.splits = (int)ceil_div(steps, ceil_div(steps, p.splits));
-    p.part = up((int64_t)p.splits * e.M * (glu ? 2 : 1) * up(e.N, 8) * 4, 256);
-  }
-  return p;
+  return best;
 }
 
 template <typename T, class C, bool GLU>
-hipError_t launch_mx4_tile(const Mx4Args& a, int splits, hipStream_t s) {
+hipError_t launch_mx4_tile(const Mx4Args& a, hipStream_t s) {
   const int64_t tiles = ceil_div(a.e.N, GLU ? C::BN / 2 : C::BN) * mx4_rows(a.e, C::BM);
-  constexpr int lds = C::S * (C::BM + C::BN) * 128 + 2 * (C::BM + C::BN) * 16;
+  constexpr int lds = (C::S * 128 + scale_buffers(C::S) * 16) * (C::BM + C::BN);
   auto* fn = &k_mx4_tile<T, C, GLU>;
   static std::atomic<uint64_t> done{0};
   const hipError_t set = allow_lds(reinterpret_cast<const void*>(fn), lds, &done);
   if (set != hipSuccess) return set;
-  hipLaunchKernelGGL(fn, dim3((unsigned)tiles, (unsigned)splits), dim3(C::TH), lds, s, a);
-  if (splits > 1)
-    hipLaunchKernelGGL((k_mm_join<T, GLU>), dim3((unsigned)ceil_div(a.e.M * ceil_div(a.e.N, 8), 256)), dim3(256), 0, s, a.e, splits);
+  hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3(C::TH), lds, s, a);
   return hipGetLastError();
 }
 
 template <typename T, int MT, bool GLU>
 hipError_t launch_mx4_few(const Mx4Args& a, hipStream_t s) {
   const int64_t slices = ceil_div(a.e.N, GLU ? 8 : 16), jobs = slices * mx4_rows(a.e, 16 * MT);
-  // waves per workgroup: up to 32 per CU over the launch, each with at least two chunks of k
+  // waves per workgroup: up to 32 per CU over the launch, each with at least two chunks of k, their sums within 64 KiB of LDS
   int waves = 16;
   while (waves > 1 && (jobs * waves > 8192 || waves * 4 > a.units + 3)) waves /= 2;
   hipLaunchKernelGGL((k_mx4_few<T, MT, GLU>), dim3((unsigned)jobs), dim3(64 * waves), waves * MT * 1024, s, a, (int)slices);
@@ -688,40 +691,40 @@ hipError_t launch_mx4_few(const Mx4Args& a, hipStream_t s) {
 }
 
 template <typename T, bool GLU>
-hipError_t launch_mx4_kind(const Mx4Args& a, const MxPlan& p, hipStream_t s) {
-  if (p.kind == MX_FEW1) return launch_mx4_few<T, 1, GLU>(a, s);
-  if (p.kind == MX_FEW2) return launch_mx4_few<T, 2, GLU>(a, s);
-  if (p.kind == MX_BIG) return launch_mx4_tile<T, MxBig, GLU>(a, p.splits, s);
-  if (p.kind == MX_MID) return launch_mx4_tile<T, MxMid, GLU>(a, p.splits, s);
-  return launch_mx4_tile<T, MxLow, GLU>(a, p.splits, s);
+hipError_t launch_mx4_kind(const Mx4Args& a, int kind, hipStream_t s) {
+  switch (kind) {
+    case MX_FEW1: return launch_mx4_few<T, 1, GLU>(a, s);
+    case MX_FEW2: return launch_mx4_few<T, 2, GLU>(a, s);
+    case MX_FEW4: return launch_mx4_few<T, 4, GLU>(a, s);
+    case MX_BIG: return launch_mx4_tile<T, MxBig, GLU>(a, s);
+    case MX_MID: return launch_mx4_tile<T, MxMid, GLU>(a, s);
+    case MX_LOW: return launch_mx4_tile<T, MxLow, GLU>(a, s);
+    default: return launch_mx4_tile<T, MxThin, GLU>(a, s);
+  }
 }
 
 }  // namespace
 
+int mx4_choice(const Mx4Args& a) { return plan_mx4(a); }
+
+// whether the launch holds the problem (a grid's threads stay below 2^32)
 bool mx4_matmul_fits(const Mx4Args& a) {
   const int64_t nw = a.e.act == EFF_ACT_SWIGLU ? 2 * a.e.N : a.e.N;
-  const MxPlan p = plan_mx4(a);
-  if (p.kind == MX_FEW1 || p.kind == MX_FEW2) return fits(ceil_div(nw, 16) * mx4_rows(a.e, p.kind == MX_FEW1 ? 16 : 32), 1024);
-  return fits(ceil_div(nw, 128) * mx4_rows(a.e, 64), 512);
+  const int kind = plan_mx4(a);
+  if (kind <= MX_FEW4) return fits(ceil_div(nw, 16) * mx4_rows(a.e, kind == MX_FEW1 ? 16 : kind == MX_FEW2 ? 32 : 64), 1024);
+  return fits(ceil_div(nw, 128) * mx4_rows(a.e, kind == MX_THIN ? 16 : 64), 512);
 }
 
-int64_t mx4_matmul_workspace(const Mx4Args& a) { return plan_mx4(a).part; }
-
-hipError_t launch_mx4_matmul(const Mx4Args& in, void* workspace, hipStream_t s) {
+hipError_t launch_mx4_matmul(const Mx4Args& in, hipStream_t s) {
   Mx4Args a = in;
   MmArgs& e = a.e;
   e.vec = aligned16({e.y, e.bias, e.residual, e.pre}, {e.N, e.ldy, e.residual ? e.ldr : 0, e.pre ? e.ldp : 0}, 2);
   e.stream = e.M * e.N * (e.y_f32 ? 4 : 2) > (int64_t)256 << 20;  // past the caches, as launch_matmul
   e.simple = e.vec && !e.bias && !e.pre && !e.y_f32 && (e.act == EFF_ACT_NONE || e.act == EFF_ACT_SWIGLU);
-  const MxPlan p = plan_mx4(a);
+  const int kind = plan_mx4(a);
   const bool glu = e.act == EFF_ACT_SWIGLU;
-  if (p.splits > 1) {
-    e.part = static_cast<float*>(workspace);
-    e.ldpart = (glu ? 2 : 1) * up(e.N, 8), e.simple = 0;
-    e.split_steps = (int)ceil_div(ceil_div(a.units, 2), p.splits);
-  }
-  if (e.dtype == EFF_DT_BF16) return glu ? launch_mx4_kind<bf16_t, true>(a, p, s) : launch_mx4_kind<bf16_t, false>(a, p, s);
-  return glu ? launch_mx4_kind<f16_t, true>(a, p, s) : launch_mx4_kind<f16_t, false>(a, p, s);
+  if (e.dtype == EFF_DT_BF16) return glu ? launch_mx4_kind<bf16_t, true>(a, kind, s) : launch_mx4_kind<bf16_t, false>(a, kind, s);
+  return glu ? launch_mx4_kind<f16_t, true>(a, kind, s) : launch_mx4_kind<f16_t, false>(a, kind, s);
 }
 
 }  // namespace eff

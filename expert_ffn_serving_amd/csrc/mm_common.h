@@ -375,34 +375,50 @@ __device__ __forceinline__ void store_tile(const MmArgs& a, f32x4_t (&acc)[MT][N
   }
 }
 
-// A split k's sums added in order of k, and the epilogue (333 x 515, 7 splits: 6 us, a launch and two trips to memory).  grid: ceil(M * vectors / 256); a thread takes 8 columns.
-template <typename T, bool GLU>
-__global__ void __launch_bounds__(256)
-k_mm_join(MmArgs a, int splits) {
-  const int64_t vr = (a.N + 7) / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.M * vr) return;
-  const int64_t m = i / vr, n = i % vr * 8;
-  float z[8], u[8];
+// The same straight from the registers of a tile with k-contiguous weights, where a lane's columns of a row are consecutive:
+// no LDS, no barrier, accesses of up to 16 bytes of 4 lanes side by side.  SIMPLE: a.simple, and nothing else in the code.
+template <typename T, class C, bool GLU, bool SIMPLE, int MT, int NT>
+__device__ __forceinline__ void store_regs(const MmArgs& a, f32x4_t (&acc)[MT][NT], int g, int64_t m0, int64_t m1, int64_t n0) {
+  constexpr int TM = C::BM / C::WM, TN = C::BN / C::WN, HALVES = GLU ? 2 : 1, NTH = NT / HALVES, TNH = TN / HALVES, RUN = NTH * 4;
+  constexpr int CL = RUN < 8 ? RUN : 8;
+  typedef T V __attribute__((ext_vector_type(CL)));
+  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave % C::WM, wn = wave / C::WM;
+  const int64_t nb = (int64_t)g * (GLU ? 2 * a.N : a.N);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) z[e] = u[e] = 0.f;
-  const float* p = a.part + m * a.ldpart + n;
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s, p += a.M * a.ldpart)
+  for (int i = 0; i < MT; ++i) {
+    const int64_t m = m0 + wm * TM + i * 16 + r;
+    if (m >= m1) continue;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + 4 * h);
+    for (int h = 0; h < RUN / CL; ++h) {
+      const int64_t n = n0 + wn * TNH + q * RUN + h * CL;
+      float z[CL], u[CL];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[4 * h + e] += v[e];
-      if (GLU) {
-        const f32x4_t v2 = *reinterpret_cast<const f32x4_t*>(p + a.ldpart / 2 + 4 * h);
+      for (int e = 0; e < CL; ++e) {
+        z[e] = acc[i][(h * CL + e) / 4][e % 4];
+        if (GLU) u[e] = acc[i][NTH + (h * CL + e) / 4][e % 4];
+      }
+      if constexpr (SIMPLE) {
+        if (n >= a.N) continue;
+        V o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[4 * h + e] += v2[e];
+        for (int e = 0; e < CL; ++e) z[e] = GLU ? act_silu(z[e]) * u[e] : z[e];
+        if (a.residual) {
+          const V res = *reinterpret_cast<const V*>(reinterpret_cast<const T*>(a.residual) + m * a.ldr + n);
+#pragma unroll
+          for (int e = 0; e < CL; ++e) z[e] += (float)res[e];
+        }
+#pragma unroll
+        for (int e = 0; e < CL; ++e) o[e] = (T)z[e];
+        V* d = reinterpret_cast<V*>(reinterpret_cast<T*>(a.y) + m * a.ldy + n);
+        if (a.stream) __builtin_nontemporal_store(o, d);
+        else *d = o;
+      } else {
+        mm_finish<T, CL, GLU>(a, m, n, nb, 0, z, u);
       }
     }
-  const float back = unscale<T>(a, 0, m);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) z[e] *= back;
-  mm_finish<T, 8, GLU>(a, m, n, 0, 0, z, u);
+  }
 }
 
 // ---- launches ----------------------------------------------------------------------------------------

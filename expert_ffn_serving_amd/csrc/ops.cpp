@@ -168,6 +168,8 @@ MmChoice eff::matmul_choice(const eff_matmul_desc& d, int product) {
   return matmul_choice(product == 0 ? forward_args(&d) : product == 1 ? dx_args(&d) : dw_args(&d));
 }
 
+int eff::mx4_choice(const eff_mx4_desc& d) { return mx4_choice(mx4_args(&d)); }
+
 extern "C" {
 
 int64_t eff_matmul_workspace(const eff_matmul_desc* d, int backward) {
@@ -425,7 +427,7 @@ int eff_mx4_dequantize(int dtype, const uint8_t* codes, int64_t ld_codes, const 
 int64_t eff_mx4_matmul_workspace(const eff_mx4_desc* d) {
   if (const char* why = check_mx4_desc(d)) return bad("eff_mx4_matmul_workspace", why);
   if (d->m == 0) return 0;
-  return x_code_bytes(d) + x_scale_bytes(d) + align256(mx4_matmul_workspace(mx4_args(d)));
+  return x_code_bytes(d) + x_scale_bytes(d);
 }
 
 int eff_mx4_matmul(const eff_mx4_desc* d, const void* x, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, const void* bias,
@@ -459,9 +461,8 @@ int eff_mx4_matmul(const eff_mx4_desc* d, const void* x, const uint8_t* xs, cons
     q.codes = tmp, q.ldc = a.ldx, q.scales = tmp + x_code_bytes(d), q.lds = a.ldxs;
     if (int rc = launched(fn, launch_mx4_quantize(q, (hipStream_t)stream))) return rc;
     a.x = q.codes, a.xs = q.scales;
-    tmp += x_code_bytes(d) + x_scale_bytes(d);
   }
-  return launched(fn, launch_mx4_matmul(a, tmp, (hipStream_t)stream));
+  return launched(fn, launch_mx4_matmul(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

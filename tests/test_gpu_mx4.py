@@ -1,11 +1,13 @@
 """Microscaled 4-bit rows, bit for bit, and the products of such operands against 64 bits."""
-import math
+import itertools
 
 import pytest
 import torch
 
 from tests import block_ref as B
 from tests import ops_ref as R
+from tests.matmul_paths import group_sizes
+from tests.mx4_paths import PATHS
 
 pytestmark = pytest.mark.gpu
 BF, HF, F32, I32, U8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8
@@ -215,6 +217,37 @@ def test_groups(eff, groups, m):
     for n, k, act in ((24, 130, R.SWIGLU), (72, 512, R.NONE)):
         check(eff, m, n, k, act=act, bias=True, pre=True, groups=groups)
         check(eff, m, n, k, dt=HF, act=act, groups=groups, coded=True, residual=True)
+
+
+@pytest.mark.parametrize("path", PATHS, ids=lambda p: "-".join(map(str, p)))
+def test_every_kernel(eff, path):
+    """References on the GPU in float64: the sizes that reach the large tiles are large."""
+    kind, m, n, k, act, groups = path
+    nw = 2 * n if act == R.SWIGLU else n
+    g = torch.Generator(device="cuda").manual_seed(m + n)
+    x = torch.randn(m, k, generator=g, device="cuda", dtype=BF)
+    wq, ws = quantised(eff, torch.randn(max(1, groups), nw, k, generator=g, device="cuda", dtype=BF) * k ** -0.5)
+    off = None
+    if groups:
+        off = torch.tensor([0] + list(itertools.accumulate(group_sizes(m, groups))), dtype=I32, device="cuda")
+    else:
+        wq, ws = wq[0], ws[0]
+    xc, xs = quantised(eff, x)
+    b = torch.randn(*((groups,) if groups else ()), nw, generator=g, device="cuda").to(BF)
+    res = torch.randn(m, n, generator=g, device="cuda").to(BF)
+    for bias, residual, pre, out in ((None, None, False, BF), (None, res, False, BF), (b, res, True, F32)):
+        y, p = torch.full((m, n), 7.0, dtype=out, device="cuda"), torch.full((m, nw), 7.0, dtype=BF, device="cuda") if pre else None
+        kw = dict(x_scales=xs, bias=bias, residual=residual, pre=p, act=act)
+        if groups:
+            eff.grouped_mx4_matmul(xc, wq, ws, off, y, **kw)
+        else:
+            eff.mx4_matmul(xc, wq, ws, y, **kw)
+        ry, ye, rz, ze = R.matmul64(B.values(xc, xs), B.values(wq, ws), bias, act, residual, off, n)
+        R.assert_within(y, ry, ye, "y")
+        if pre:
+            R.assert_within(p, rz, ze, "pre")
+    del ry, ye, rz, ze
+    torch.cuda.empty_cache()
 
 
 def test_groups_at_their_borders(eff):
