@@ -432,7 +432,7 @@ struct NormArgs {
 };
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 
-// dx null: not written.  part: norm_parts(T) rows of 2 H fp32 where dw or db is wanted, else null.
+// dx null: not written.  part: norm_parts rows of 2 H fp32 where dw or db is wanted, else null.
 struct NormGradArgs {
   const void *dy, *x, *w, *residual;
   const float *mean, *rstd;
@@ -441,7 +441,7 @@ struct NormGradArgs {
   int64_t lddy, ldx, ldr, lddx, T, H;
   int dtype, w_dtype;
 };
-int64_t norm_parts(int64_t T);
+int64_t norm_parts(int64_t T, int64_t H);
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s);
 
 // The router's losses (k_balance.hip).
@@ -457,8 +457,7 @@ struct BalanceArgs {
   // of the workspace, set by launch_balance
   double* total_p;   // [E + 1], the last: sum of lse^2
   int32_t* done;
-  float* part_p;     // [parts][E + 1]
-  int32_t* part_c;
+  int2* part;        // [parts][E + 1]: bits of the fp32 sum, count
 };
 int64_t balance_workspace(int64_t T, int E);
 hipError_t launch_balance(BalanceArgs a, void* workspace, hipStream_t s);

@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "eff_internal.h"
+#include "wave.h"
 
 namespace eff {
 namespace {
@@ -30,39 +31,33 @@ struct LogitVec<T, 1> {
   typedef T V;
 };
 
-// lane's values of a row of E logits in fp32: columns (i * 64 + lane) * VEC + e; past the end `fill`
+// A lane's values of a row of E logits: columns (i * 64 + lane) * VEC + e.
 template <typename T, int VEC, int NV>
-__device__ inline void load_row(const T* p, int E, int lane, float fill, float (*v)[VEC]) {
-  typedef typename LogitVec<T, VEC>::V V;
-  V raw[NV];
+struct LogitRow {
+  typename LogitVec<T, VEC>::V raw[NV];
+  __device__ void load(const T* p, int E, int lane) {  // past the end the row's first values, which are not used
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if ((i * 64 + lane) * VEC < E) raw[i] = *reinterpret_cast<const V*>(p + (i * 64 + lane) * VEC);
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      if constexpr (VEC == 1) v[i][e] = (i * 64 + lane) * VEC < E ? (float)raw[i] : fill;
-      else v[i][e] = (i * 64 + lane) * VEC < E ? (float)raw[i][e] : fill;
+    for (int i = 0; i < NV; ++i) {
+      const int j = (i * 64 + lane) * VEC;
+      raw[i] = *reinterpret_cast<const typename LogitVec<T, VEC>::V*>(p + (j < E ? j : 0));
     }
-}
+  }
+  __device__ void widen(int E, int lane, float (*v)[VEC]) const {  // past the end -infinity
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        if constexpr (VEC == 1) v[i][e] = (i * 64 + lane) * VEC < E ? (float)raw[i] : -kInf;
+        else v[i][e] = (i * 64 + lane) * VEC < E ? (float)raw[i][e] : -kInf;
+      }
+  }
+};
 
 // LDS writes of this wave before, reads of its other lanes after (a wave's LDS accesses complete in order)
 __device__ inline void wave_order() {
   asm volatile("" : : : "memory");
   __builtin_amdgcn_wave_barrier();
 }
-__device__ inline float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-__device__ inline float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
-}
-
 // grid: parts.  Wave w of part p takes rows p kWaves + w, then parts kWaves further; the part's sums of p and of lse^2 and
 // its counts go to one row of the workspace each.
 template <typename T, int VEC, int NV>
@@ -81,14 +76,30 @@ k_balance(BalanceArgs a) {
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) sum[i][e] = 0.f;
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < a.T; t += (int64_t)gridDim.x * kWaves) {
-    if (a.mask && !a.mask[t]) {
+  // a row is in flight while the one before it is used; a masked token's is not read, past the end the last row is
+  const int64_t step = (int64_t)gridDim.x * kWaves;
+  LogitRow<T, VEC, NV> next;
+  int next_id = -1;
+  bool next_set = false;
+  auto fetch = [&](int64_t t) {
+    t = min(t, a.T - 1);
+    next_set = !a.mask || a.mask[t];
+    if (!next_set) return;
+    next.load(reinterpret_cast<const T*>(a.logits) + t * a.ld, E, lane);
+    next_id = lane < K ? a.ids[t * K + lane] : -1;
+  };
+  int64_t t = (int64_t)blockIdx.x * kWaves + wave;
+  if (t < a.T) fetch(t);
+  for (; t < a.T; t += step) {
+    float v[NV][VEC], top = -kInf;
+    const bool set = next_set;
+    const int id = next_id;
+    if (set) next.widen(E, lane, v);
+    fetch(t + step);
+    if (!set) {
       if (lane == 0) a.lse[t] = -kInf;
       continue;
     }
-    float v[NV][VEC], top = -kInf;
-    load_row<T, VEC, NV>(reinterpret_cast<const T*>(a.logits) + t * a.ld, E, lane, -kInf, v);
-    const int id = lane < K ? a.ids[t * K + lane] : -1;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -130,17 +141,13 @@ k_balance(BalanceArgs a) {
     }
   }
   __syncthreads();
-  float* pp = a.part_p + (int64_t)blockIdx.x * (E + 1);
-  int* pc = a.part_c + (int64_t)blockIdx.x * (E + 1);
-  for (int e = threadIdx.x; e <= E; e += 64 * kWaves) {
-    pp[e] = e < E ? s_p[e] : (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
-    pc[e] = s_count[e];
-  }
+  for (int e = threadIdx.x; e <= E; e += 64 * kWaves)
+    a.part[(int64_t)blockIdx.x * (E + 1) + e] = make_int2(__float_as_int(e < E ? s_p[e] : (s_z[0] + s_z[1]) + (s_z[2] + s_z[3])), s_count[e]);
 }
 
 // grid: ceil((E + 1) / 64).  Columns' sums over the parts: 16 waves take every 16th part, sums in double, in order.  The
 // workgroup that finishes last adds up the losses (in order of e, so which one it is changes nothing).
-constexpr int kJoin = 1024;
+constexpr int kJoin = 1024, kParts = 256;
 
 __global__ void __launch_bounds__(kJoin)
 k_balance_join(BalanceArgs a, int parts) {
@@ -151,10 +158,15 @@ k_balance_join(BalanceArgs a, int parts) {
   double p = 0.0;
   int c = 0;
   if (e <= E) {
-#pragma unroll 4
-    for (int i = wave; i < parts; i += kJoin / 64) {
-      p += (double)a.part_p[(int64_t)i * (E + 1) + e];
-      c += a.part_c[(int64_t)i * (E + 1) + e];
+    constexpr int MOST = kParts / (kJoin / 64);  // all of a wave's parts at once; past the last one the last again, not used
+    int2 v[MOST];
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) v[i] = a.part[(int64_t)min(wave + i * (kJoin / 64), parts - 1) * (E + 1) + e];
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+      if (wave + i * (kJoin / 64) >= parts) continue;
+      p += (double)__int_as_float(v[i].x);
+      c += v[i].y;
     }
   }
   s_p[wave][lane] = p;
@@ -213,18 +225,43 @@ k_balance_grad(BalanceGradArgs a) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) mine[(i * 64 + lane) * VEC + e] = 0.f;
   }
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < a.T; t += (int64_t)gridDim.x * kWaves) {
+  // a row is in flight while the one before it is used; one that is not live is not read, past the end the last row is
+  const int64_t step = (int64_t)gridDim.x * kWaves;
+  LogitRow<T, VEC, NV> next;
+  float next_lse = -kInf, next_w = 0.f, next_dw = 0.f;
+  int next_id = -1;
+  auto fetch = [&](int64_t t, float lse) {
+    t = min(t, a.T - 1);
+    next_lse = lse;
+    if (lse == -kInf) return;
+    if (a.dlosses) next.load(reinterpret_cast<const T*>(a.logits) + t * a.ld, E, lane);
+    if (a.w && lane < K) {
+      next_id = a.ids[t * K + lane];
+      next_w = a.w[t * K + lane];
+      next_dw = a.dw[t * K + lane];
+    }
+  };
+  int64_t t = (int64_t)blockIdx.x * kWaves + wave;
+  float after = -kInf;  // the lse of the row after the next
+  if (t < a.T) {
+    fetch(t, a.lse[t]);
+    after = a.lse[min(t + step, a.T - 1)];
+  }
+  for (; t < a.T; t += step) {
     T* out = reinterpret_cast<T*>(a.dlogits) + t * a.ldd;
-    const float lse = a.lse[t];
+    const float lse = next_lse, w_k = next_w, dw_k = next_dw;
+    const int id = next_id;
     float v[NV][VEC];
-    if (lse == -kInf) {  // the logits of such a token are not read
+    if (lse != -kInf && a.dlosses) next.widen(E, lane, v);
+    fetch(t + step, after);
+    after = a.lse[min(t + 2 * step, a.T - 1)];
+    if (lse == -kInf) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
     } else {
       if (a.dlosses) {
-        load_row<T, VEC, NV>(reinterpret_cast<const T*>(a.logits) + t * a.ld, E, lane, -kInf, v);
         // the softmax anew and not exp(l - lse): far from 0 the saved lse has lost digits that p needs
         float top = -kInf, both[2] = {0.f, 0.f};
 #pragma unroll
@@ -252,14 +289,13 @@ k_balance_grad(BalanceGradArgs a) {
           for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
       }
       if (a.w) {
-        const int id = lane < K ? a.ids[t * K + lane] : -1;
-        const bool ok = id >= 0 && id < E;
-        const float w = ok ? a.w[t * K + lane] : 0.f, dw = ok ? a.dw[t * K + lane] : 0.f;
+        const bool ok = lane < K && id >= 0 && id < E;
+        const float w = ok ? w_k : 0.f, dw = ok ? dw_k : 0.f;
         const float g = w * (dw - wave_sum(w * dw));
         float sum = 0.f;  // of the pairs with this pair's id, in order of k
         for (int k = 0; k < K; ++k) {
-          const float o = __shfl(g, k);
-          if (__shfl(id, k) == id) sum += o;
+          const float o = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), k));
+          if (__builtin_amdgcn_readlane(id, k) == id) sum += o;
         }
         if (ok) mine[id] = sum;
         wave_order();
@@ -314,8 +350,8 @@ bool rows_of_vectors(int dtype, int E, const void* p, int64_t ld, const void* q,
 
 }  // namespace
 
-// Workgroups of the pass over the logits: one per CU, fewer where each wave would have fewer than two rows.
-int64_t balance_parts(int64_t T) { return std::max<int64_t>(1, std::min<int64_t>(256, (T + 2 * kWaves - 1) / (2 * kWaves))); }
+// Workgroups of the pass over the logits: one per CU, fewer where each wave would have fewer than four rows.
+int64_t balance_parts(int64_t T) { return std::max<int64_t>(1, std::min<int64_t>(kParts, (T + 4 * kWaves - 1) / (4 * kWaves))); }
 
 int64_t balance_workspace(int64_t T, int E) {
   const int64_t row = balance_parts(T) * (E + 1);
@@ -326,8 +362,7 @@ hipError_t launch_balance(BalanceArgs a, void* workspace, hipStream_t s) {
   const int parts = (int)balance_parts(a.T);
   a.total_p = static_cast<double*>(workspace);
   a.done = reinterpret_cast<int32_t*>(a.total_p + a.E + 1);
-  a.part_p = reinterpret_cast<float*>(a.done + 2);
-  a.part_c = reinterpret_cast<int32_t*>(a.part_p + (int64_t)parts * (a.E + 1));
+  a.part = reinterpret_cast<int2*>(a.done + 2);
   with_logits(a.dtype, rows_of_vectors(a.dtype, a.E, a.logits, a.ld, nullptr, 0), a.E, [&](auto t, auto vec, auto nv) {
     hipLaunchKernelGGL((k_balance<decltype(t), decltype(vec)::value, decltype(nv)::value>), dim3(parts), dim3(64 * kWaves),
                        (2 * a.E + 1) * 4, s, a);

@@ -10,6 +10,7 @@
 #include <type_traits>
 
 #include "eff_internal.h"
+#include "wave.h"
 
 namespace eff {
 namespace {
@@ -57,14 +58,19 @@ __device__ inline void norm_store(void* p, int64_t i, const float* v) {
   *reinterpret_cast<typename NormVec<T, VEC>::V*>(reinterpret_cast<T*>(p) + i) = o;
 }
 
+template <int VEC>
+__device__ inline void norm_put_f32(float* p, const float* v) {
+  constexpr int C = VEC > 4 ? 4 : VEC;
+#pragma unroll
+  for (int c = 0; c < VEC; c += C) norm_store<float, C>(p, c, v + c);
+}
+
 // sums of N values over the TH threads of a row (TH = 64: the wave; else the wave's sums meet in LDS, s: [TH / 64][N],
 // in wave order).  Every thread of the workgroup takes part.
 template <int TH, int N>
 __device__ inline void row_sum(float* v, float* s) {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o);
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if constexpr (TH > 64) {
     const int wave = (threadIdx.x % TH) >> 6;
     if ((threadIdx.x & 63) == 0) {
@@ -204,19 +210,43 @@ k_norm_grad(NormGradArgs a) {
     for (int e = 0; e < VEC; ++e) w[i][e] = 1.f, sw[i][e] = sb[i][e] = 0.f;
     if (a.w && h < a.H) norm_get<W, VEC>(a.w, h, w[i]);
   }
+  // a row is in flight while the one before it is used, where the registers hold both; past the end the last row again, not used
+  constexpr bool AHEAD = NV * VEC <= 8;
+  typedef typename NormVec<T, VEC>::V V;
+  V xn[NV], dn[NV], rn[NV];
+  float mean_n = 0.f, rstd_n = 0.f;
+  auto fetch = [&](int64_t row) {
+    row = min(row, a.T - 1);
+    mean_n = a.mean[row], rstd_n = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t h = (int64_t)(i * TH + tid) * VEC, at = h < a.H ? h : 0;
+      xn[i] = norm_load<T, VEC>(a.x, row * a.ldx + at);
+      dn[i] = norm_load<T, VEC>(a.dy, row * a.lddy + at);
+      if (a.residual) rn[i] = norm_load<T, VEC>(a.residual, row * a.ldr + at);
+    }
+  };
   int phase = 0;
   const int64_t step = (int64_t)gridDim.x * R;
+  if (AHEAD) fetch((int64_t)blockIdx.x * R + sub);
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.T; r0 += step, phase ^= 1) {
     const int64_t row = r0 + sub;
     const bool live = row < a.T;
     float xh[NV][VEC], g[NV][VEC], sum[2] = {0.f, 0.f};
-    const float mean = live ? a.mean[row] : 0.f, rstd = live ? a.rstd[row] : 0.f;
+    V res[NV];
+    if (!AHEAD) fetch(row);
+    const float mean = mean_n, rstd = rstd_n;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      norm_widen<T, VEC>(xn[i], xh[i]);
+      norm_widen<T, VEC>(dn[i], g[i]);
+      res[i] = rn[i];
+    }
+    if (AHEAD) fetch(row + step);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t h = (int64_t)(i * TH + tid) * VEC;
       if (live && h < a.H) {
-        norm_widen<T, VEC>(norm_load<T, VEC>(a.x, row * a.ldx + h), xh[i]);
-        norm_widen<T, VEC>(norm_load<T, VEC>(a.dy, row * a.lddy + h), g[i]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           xh[i][e] = (xh[i][e] - mean) * rstd;
@@ -241,7 +271,7 @@ k_norm_grad(NormGradArgs a) {
       for (int e = 0; e < VEC; ++e) g[i][e] = rstd * (g[i][e] - c1 - xh[i][e] * c2);
       if (a.residual) {
         float r[VEC];
-        norm_widen<T, VEC>(norm_load<T, VEC>(a.residual, row * a.ldr + h), r);
+        norm_widen<T, VEC>(res[i], r);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) g[i][e] += r[e];
       }
@@ -266,12 +296,12 @@ k_norm_grad(NormGradArgs a) {
             float v = s_col[e * TH + tid];
 #pragma unroll
             for (int r = 1; r < R; ++r) v += s_col[(r * VEC + e) * TH + tid];
-            part[k * a.H + h + e] = v;
+            (k ? sb : sw)[i][e] = v;
           }
+          norm_put_f32<VEC>(part + k * a.H + h, (k ? sb : sw)[i]);
         }
       } else if (h < a.H) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) part[k * a.H + h + e] = k ? sb[i][e] : sw[i][e];
+        norm_put_f32<VEC>(part + k * a.H + h, (k ? sb : sw)[i]);
       }
     }
 }
@@ -378,6 +408,25 @@ void with_shape(int64_t n, F f, G g) {
     else g();
   }
 }
+// the same for the gradients, whose threads hold the columns' sums besides
+template <bool VECTORS, typename F, typename G>
+void with_grad_shape(int64_t n, F f, G g) {
+  if constexpr (VECTORS) {
+    if (n <= 64) f(NormShape<64, 1, 4>{});
+    else if (n <= 128) f(NormShape<128, 1, 4>{});
+    else if (n <= 256) f(NormShape<256, 1, 2>{});
+    else if (n <= 512) f(NormShape<512, 1, 2>{});
+    else if (n <= 1024) f(NormShape<1024, 1, 1>{});
+    else if (n <= 2048) f(NormShape<1024, 2, 1>{});
+    else g();
+  } else {
+    if (n <= 256) f(NormShape<64, 4, 4>{});
+    else if (n <= 1024) f(NormShape<256, 4, 2>{});
+    else if (n <= 4096) f(NormShape<512, 8, 2>{});
+    else if (n <= 16384) f(NormShape<1024, 16, 1>{});
+    else g();
+  }
+}
 
 // calls f with the rows' and the weights' types
 template <typename F>
@@ -428,13 +477,13 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Parts of the columns' sums: as many as there are rows, up to 512.
-int64_t norm_parts(int64_t T) { return std::min<int64_t>(T, 512); }
+// Parts of the columns' sums, a workgroup's each: as many as fill the chip with 16 waves a CU.
+int64_t norm_parts(int64_t T, int64_t H) { return std::min<int64_t>(T, H <= 512 ? 1024 : H <= 2048 ? 512 : 256); }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
   const int b = a.dtype == EFF_DT_F32 ? 4 : 2;
   const bool vec = whole_vectors(b, a.H, {a.x, a.dy, a.dx, a.w, a.residual}, {a.ldx, a.lddy, a.dx ? a.lddx : 0, a.residual ? a.ldr : 0});
-  const int64_t parts = norm_parts(a.T);
+  const int64_t parts = norm_parts(a.T, a.H);
   with_types(a.dtype, a.w_dtype, [&](auto t, auto wt) {
     typedef decltype(t) T;
     typedef decltype(wt) W;
@@ -461,8 +510,8 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
       hipLaunchKernelGGL((k_norm_grad<T, W, V, S::th, S::nv, S::r>), dim3((unsigned)grid), dim3(S::th * S::r), lds, s, a);
     };
     if (a.T > 0) {
-      if (vec) with_shape<true>(a.H / VEC, [&](auto sh) { go(sh, std::integral_constant<int, VEC>{}); }, lengthy);
-      else with_shape<false>(a.H, [&](auto sh) { go(sh, std::integral_constant<int, 1>{}); }, lengthy);
+      if (vec) with_grad_shape<true>(a.H / VEC, [&](auto sh) { go(sh, std::integral_constant<int, VEC>{}); }, lengthy);
+      else with_grad_shape<false>(a.H, [&](auto sh) { go(sh, std::integral_constant<int, 1>{}); }, lengthy);
     }
     if (a.dw || a.db)
       hipLaunchKernelGGL((k_norm_join<W>), dim3((unsigned)cdiv(a.H, 64), 2), dim3(1024), 0, s, a.part, a.T > 0 ? written : 0, a.H, a.dw, a.db);

@@ -331,7 +331,7 @@ int eff_layer_norm(int dtype, int w_dtype, const void* x, int64_t ld_x, const vo
 
 int64_t eff_layer_norm_backward_workspace(int64_t T, int64_t H) {
   if (const char* why = check_norm(EFF_DT_F32, EFF_DT_F32, T, H)) return bad("eff_layer_norm_backward_workspace", why);
-  return align256(norm_parts(T) * 2 * H * 4);
+  return align256(norm_parts(T, H) * 2 * H * 4);
 }
 
 int eff_layer_norm_backward(int dtype, int w_dtype, const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, const void* w,
