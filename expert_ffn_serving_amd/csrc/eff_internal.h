@@ -454,10 +454,7 @@ struct BalanceArgs {
   float *lse, *losses;
   int64_t T;
   int K, E, dtype;
-  // of the workspace, set by launch_balance
-  double* total_p;   // [E + 1], the last: sum of lse^2
-  int32_t* done;
-  int2* part;        // [parts][E + 1]: bits of the fp32 sum, count
+  int2* part;           // set by launch_balance: [parts][E + 1] of the workspace, bits of the fp32 sum of p (the last: of lse^2) and count
 };
 int64_t balance_workspace(int64_t T, int E);
 hipError_t launch_balance(BalanceArgs a, void* workspace, hipStream_t s);

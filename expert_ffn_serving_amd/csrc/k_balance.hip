@@ -19,7 +19,10 @@ namespace {
 typedef _Float16 f16_t;
 typedef __bf16 bf16_t;
 
-constexpr int kWaves = 4;  // a wave per row
+// A wave takes a row; waves of a workgroup, 16 where the registers of so many hold it.
+template <int VEC, int NV>
+constexpr int waves_of() { return VEC * NV <= 16 ? 16 : 4; }
+constexpr int kGradWaves = 4;
 constexpr float kInf = __builtin_inff();
 
 template <typename T, int VEC>
@@ -53,48 +56,62 @@ struct LogitRow {
   }
 };
 
+// e^x to about 2 units in the last place and 0 below 2^-126, for x <= 0 or NaN: 2^(x log2 e), the product's rounding error
+// put back
+__device__ inline float exp_down(float x) {
+  x = x < -104.f ? -104.f : x;
+  const float t = x * 1.44269504088896341f, lo = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504088896341f, -t));
+  return __builtin_amdgcn_exp2f(t) * fmaf(lo, 0.693147180559945309f, 1.0f);
+}
+
+// A copy that stays one: the value is taken out of the register that the next load goes to before that load is issued (else the
+// copies stand at the end of the loop, behind a wait for everything under way).
+template <typename V>
+__device__ inline void keep(V& v) { asm volatile("" : "+v"(v)); }
+
 // LDS writes of this wave before, reads of its other lanes after (a wave's LDS accesses complete in order)
 __device__ inline void wave_order() {
   asm volatile("" : : : "memory");
   __builtin_amdgcn_wave_barrier();
 }
-// grid: parts.  Wave w of part p takes rows p kWaves + w, then parts kWaves further; the part's sums of p and of lse^2 and
-// its counts go to one row of the workspace each.
+// grid: parts.  Wave w of part p takes rows p W + w, then parts W further (W waves); the part's sums of p and of lse^2 and
+// its counts go to one row of the workspace.  2048 x 256: bound by the way to memory and back, two rows a wave.
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(64 * kWaves)
+__global__ void __launch_bounds__(64 * (waves_of<VEC, NV>()))
 k_balance(BalanceArgs a) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t s_dyn[];
-  int* s_count = reinterpret_cast<int*>(s_dyn);         // [E + 1], the last: live tokens
-  float* s_p = reinterpret_cast<float*>(s_dyn) + a.E + 1;  // [E]
-  __shared__ float s_z[kWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.E, K = a.K;
-  for (int e = threadIdx.x; e <= E; e += 64 * kWaves) s_count[e] = 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;  // k_balance_join counts its workgroups from here
+  constexpr int W = waves_of<VEC, NV>();
+  extern __shared__ int s_count[];  // [E + 1], the last: live tokens
+  __shared__ float s_p[W][64 * VEC], s_z[W];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), E = a.E, K = a.K;
+  for (int e = threadIdx.x; e <= E; e += 64 * W) s_count[e] = 0;
   __syncthreads();
   float sum[NV][VEC], z = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) sum[i][e] = 0.f;
-  // a row is in flight while the one before it is used; a masked token's is not read, past the end the last row is
-  const int64_t step = (int64_t)gridDim.x * kWaves;
+  // a row is in flight while the one before it is used, masked or not; past the end the last row again, which is not used
+  const int64_t step = (int64_t)gridDim.x * W;
   LogitRow<T, VEC, NV> next;
-  int next_id = -1;
-  bool next_set = false;
+  int next_id = -1, next_set = 1;
   auto fetch = [&](int64_t t) {
     t = min(t, a.T - 1);
-    next_set = !a.mask || a.mask[t];
-    if (!next_set) return;
+    if (a.mask) next_set = a.mask[t];
     next.load(reinterpret_cast<const T*>(a.logits) + t * a.ld, E, lane);
-    next_id = lane < K ? a.ids[t * K + lane] : -1;
+    next_id = a.ids[t * K + min(lane, K - 1)];
   };
-  int64_t t = (int64_t)blockIdx.x * kWaves + wave;
+  int64_t t = (int64_t)blockIdx.x * W + wave;
   if (t < a.T) fetch(t);
   for (; t < a.T; t += step) {
     float v[NV][VEC], top = -kInf;
-    const bool set = next_set;
-    const int id = next_id;
-    if (set) next.widen(E, lane, v);
+    const int set = next_set;
+    int id = next_id;
+    next.widen(E, lane, v);
+    keep(id);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) keep(v[i][e]);
     fetch(t + step);
     if (!set) {
       if (lane == 0) a.lse[t] = -kInf;
@@ -111,7 +128,7 @@ k_balance(BalanceArgs a) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        v[i][e] = expf(v[i][e] - top);
+        v[i][e] = exp_down(v[i][e] - top);
         total += v[i][e];
       }
     total = wave_sum(total);
@@ -124,44 +141,47 @@ k_balance(BalanceArgs a) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < VEC; ++e) sum[i][e] = fmaf(v[i][e], inv, sum[i][e]);
-    if (id >= 0 && id < E) atomicAdd(&s_count[id], 1);
+    if (lane < K && id >= 0 && id < E) atomicAdd(&s_count[id], 1);
     if (lane == 0) atomicAdd(&s_count[E], 1);
   }
   if (lane == 0) s_z[wave] = z;
-  for (int w = 0; w < kWaves; ++w) {  // the waves' sums in wave order
+  int2* part = a.part + (int64_t)blockIdx.x * (E + 1);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {  // the waves' sums in wave order, 64 VEC columns at a time
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s_p[wave][lane * VEC + e] = sum[i][e];
     __syncthreads();
-    if (wave == w) {
+    for (int c = threadIdx.x; c < 64 * VEC; c += 64 * W) {
+      const int j = i * 64 * VEC + c;
+      float v = s_p[0][c];
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const int j = (i * 64 + lane) * VEC + e;
-          if (j < E) s_p[j] = w == 0 ? sum[i][e] : s_p[j] + sum[i][e];
-        }
+      for (int w = 1; w < W; ++w) v += s_p[w][c];
+      if (j < E) part[j] = make_int2(__float_as_int(v), s_count[j]);
     }
+    __syncthreads();
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += 64 * kWaves)
-    a.part[(int64_t)blockIdx.x * (E + 1) + e] = make_int2(__float_as_int(e < E ? s_p[e] : (s_z[0] + s_z[1]) + (s_z[2] + s_z[3])), s_count[e]);
+  if (threadIdx.x) return;
+  for (int w = 1; w < W; ++w) z += s_z[w];
+  part[E] = make_int2(__float_as_int(z), s_count[E]);
 }
 
-// grid: ceil((E + 1) / 64).  Columns' sums over the parts: 16 waves take every 16th part, sums in double, in order.  The
-// workgroup that finishes last adds up the losses (in order of e, so which one it is changes nothing).
+// Column sums over the parts, in double and in order: many columns or parts are added up by many workgroups first
+// (k_balance_columns, grid: ceil((E + 1) / 64), one row left), the rest by the one that computes the losses.  One workgroup for
+// all of 64 parts of 257 columns takes 5 us, five and a last one to finish 10.
 constexpr int kJoin = 1024, kParts = 256;
 
 __global__ void __launch_bounds__(kJoin)
-k_balance_join(BalanceArgs a, int parts) {
+k_balance_columns(const int2* __restrict__ part, int parts, int E, int2* __restrict__ out) {
   __shared__ double s_p[kJoin / 64][64];
   __shared__ int s_c[kJoin / 64][64];
-  __shared__ int s_last;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.E, e = blockIdx.x * 64 + lane;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.x * 64 + lane;
   double p = 0.0;
   int c = 0;
   if (e <= E) {
     constexpr int MOST = kParts / (kJoin / 64);  // all of a wave's parts at once; past the last one the last again, not used
     int2 v[MOST];
 #pragma unroll
-    for (int i = 0; i < MOST; ++i) v[i] = a.part[(int64_t)min(wave + i * (kJoin / 64), parts - 1) * (E + 1) + e];
+    for (int i = 0; i < MOST; ++i) v[i] = part[(int64_t)min(wave + i * (kJoin / 64), parts - 1) * (E + 1) + e];
 #pragma unroll
     for (int i = 0; i < MOST; ++i) {
       if (wave + i * (kJoin / 64) >= parts) continue;
@@ -172,52 +192,87 @@ k_balance_join(BalanceArgs a, int parts) {
   s_p[wave][lane] = p;
   s_c[wave][lane] = c;
   __syncthreads();
-  if (wave == 0 && e <= E) {
-    for (int w = 1; w < kJoin / 64; ++w) {
-      p += s_p[w][lane];
-      c += s_c[w][lane];
-    }
-    a.total_p[e] = p;
-    a.counts[e] = c;
-    __threadfence();
+  if (wave || e > E) return;
+  for (int w = 1; w < kJoin / 64; ++w) {
+    p += s_p[w][lane];
+    c += s_c[w][lane];
   }
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  const volatile double* tp = a.total_p;
-  const volatile int32_t* tc = a.counts;
+  out[e] = make_int2(__float_as_int((float)p), c);
+}
+
+__global__ void __launch_bounds__(kJoin)
+k_balance_join(BalanceArgs a, const int2* __restrict__ part, int parts) {
+  __shared__ double s_p[kJoin];
+  __shared__ int s_c[kJoin];
+  __shared__ double s_sum[kJoin / 64], s_z;
+  __shared__ int s_n;
+  const int tid = threadIdx.x, E = a.E;
+  const int per = min(kJoin, (E + 64) / 64 * 64), slices = kJoin / per;  // threads of a slice of the parts, a column each
+  const int slice = tid / per, lane_col = tid - slice * per;
   double sum = 0.0;
-  for (int i = threadIdx.x; i < E; i += kJoin) sum += tp[i] * (double)tc[i];
+  for (int c0 = 0; c0 <= E; c0 += per) {
+    const int e = c0 + lane_col;
+    double p = 0.0;
+    int c = 0;
+    if (slice < slices && e <= E) {
+      constexpr int B = 24;  // parts under way at once; past the last one the last again, not used
+      for (int i0 = slice; i0 < parts; i0 += B * slices) {
+        int2 v[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) v[b] = part[(int64_t)min(i0 + b * slices, parts - 1) * (E + 1) + e];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+          if (i0 + b * slices >= parts) continue;
+          p += (double)__int_as_float(v[b].x);
+          c += v[b].y;
+        }
+      }
+    }
+    s_p[tid] = p;
+    s_c[tid] = c;
+    __syncthreads();
+    if (slice == 0 && e <= E) {
+      for (int s = 1; s < slices; ++s) {
+        p += s_p[s * per + lane_col];
+        c += s_c[s * per + lane_col];
+      }
+      a.counts[e] = c;
+      if (e < E) sum += p * (double)c;
+      else s_z = p, s_n = c;
+    }
+    __syncthreads();
+  }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-  if (lane == 0) s_p[wave][0] = sum;
+  if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
   __syncthreads();
-  if (threadIdx.x) return;
-  for (int w = 1; w < kJoin / 64; ++w) sum += s_p[w][0];
-  const double n = (double)tc[E];
+  if (tid) return;
+  for (int w = 1; w < kJoin / 64; ++w) sum += s_sum[w];
+  const double n = (double)s_n;
   a.losses[0] = n > 0 ? (float)(sum * E / (n * n * a.K)) : 0.f;
-  a.losses[1] = n > 0 ? (float)(tp[E] / n) : 0.f;
+  a.losses[1] = n > 0 ? (float)(s_z / n) : 0.f;
 }
 
 // grid: as many workgroups as fill the chip; a wave per row.  f of the lane's columns stays in registers.
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(64 * kWaves)
+__global__ void __launch_bounds__(64 * kGradWaves)
 k_balance_grad(BalanceGradArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float s_pairs[];  // [kWaves][E rounded up to 64 VEC NV], with w
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.E, K = a.K;
+  constexpr int W = kGradWaves;
+  extern __shared__ __attribute__((aligned(16))) float s_pairs[];  // [W][E rounded up to 64 VEC NV], with w
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), E = a.E, K = a.K;
   const float n = (float)a.counts[E];
   const float ga = a.dlosses && n > 0 ? a.dlosses[0] * ((float)E / n) : 0.f, gb = a.dlosses && n > 0 ? a.dlosses[1] * (2.f / n) : 0.f;
   const float per = n > 0 ? 1.f / (n * (float)K) : 0.f;
   float f[NV][VEC];
+  int count[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int j = (i * 64 + lane) * VEC + e;
-      f[i][e] = j < E ? (float)a.counts[j] * per : 0.f;
-    }
+    for (int e = 0; e < VEC; ++e) count[i][e] = a.counts[min((i * 64 + lane) * VEC + e, E - 1)];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[i][e] = (i * 64 + lane) * VEC + e < E ? (float)count[i][e] * per : 0.f;
   float* mine = s_pairs + wave * (64 * VEC * NV);
   if (a.w) {
 #pragma unroll
@@ -225,36 +280,36 @@ k_balance_grad(BalanceGradArgs a) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) mine[(i * 64 + lane) * VEC + e] = 0.f;
   }
-  // a row is in flight while the one before it is used; one that is not live is not read, past the end the last row is
-  const int64_t step = (int64_t)gridDim.x * kWaves;
+  // a row is in flight while the one before it is used, live or not; past the end the last row again, which is not used
+  const int64_t step = (int64_t)gridDim.x * W;
   LogitRow<T, VEC, NV> next;
   float next_lse = -kInf, next_w = 0.f, next_dw = 0.f;
   int next_id = -1;
-  auto fetch = [&](int64_t t, float lse) {
+  auto fetch = [&](int64_t t) {
     t = min(t, a.T - 1);
-    next_lse = lse;
-    if (lse == -kInf) return;
+    next_lse = a.lse[t];
     if (a.dlosses) next.load(reinterpret_cast<const T*>(a.logits) + t * a.ld, E, lane);
-    if (a.w && lane < K) {
-      next_id = a.ids[t * K + lane];
-      next_w = a.w[t * K + lane];
-      next_dw = a.dw[t * K + lane];
+    if (a.w) {
+      const int64_t at = t * K + min(lane, K - 1);
+      next_id = a.ids[at];
+      next_w = a.w[at];
+      next_dw = a.dw[at];
     }
   };
-  int64_t t = (int64_t)blockIdx.x * kWaves + wave;
-  float after = -kInf;  // the lse of the row after the next
-  if (t < a.T) {
-    fetch(t, a.lse[t]);
-    after = a.lse[min(t + step, a.T - 1)];
-  }
+  int64_t t = (int64_t)blockIdx.x * W + wave;
+  fetch(t);
   for (; t < a.T; t += step) {
     T* out = reinterpret_cast<T*>(a.dlogits) + t * a.ldd;
-    const float lse = next_lse, w_k = next_w, dw_k = next_dw;
-    const int id = next_id;
-    float v[NV][VEC];
-    if (lse != -kInf && a.dlosses) next.widen(E, lane, v);
-    fetch(t + step, after);
-    after = a.lse[min(t + 2 * step, a.T - 1)];
+    const float lse = next_lse;
+    float w_k = next_w, dw_k = next_dw, v[NV][VEC];
+    int id = next_id;
+    if (a.dlosses) next.widen(E, lane, v);
+    keep(w_k), keep(dw_k), keep(id);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) keep(v[i][e]);
+    fetch(t + step);
     if (lse == -kInf) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -273,7 +328,7 @@ k_balance_grad(BalanceGradArgs a) {
         for (int i = 0; i < NV; ++i)
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            v[i][e] = expf(v[i][e] - top);
+            v[i][e] = exp_down(v[i][e] - top);
             both[0] += v[i][e];
             both[1] = fmaf(f[i][e], v[i][e], both[1]);
           }
@@ -350,32 +405,33 @@ bool rows_of_vectors(int dtype, int E, const void* p, int64_t ld, const void* q,
 
 }  // namespace
 
-// Workgroups of the pass over the logits: one per CU, fewer where each wave would have fewer than four rows.
-int64_t balance_parts(int64_t T) { return std::max<int64_t>(1, std::min<int64_t>(kParts, (T + 4 * kWaves - 1) / (4 * kWaves))); }
+// Workgroups of the pass over the logits: one per CU, fewer where its 16 waves (at most) would have fewer than two rows each.
+int64_t balance_parts(int64_t T) { return std::max<int64_t>(1, std::min<int64_t>(kParts, (T + 31) / 32)); }
 
-int64_t balance_workspace(int64_t T, int E) {
-  const int64_t row = balance_parts(T) * (E + 1);
-  return ((E + 1) * 8 + 8 + row * 8 + 255) / 256 * 256;
-}
+int64_t balance_workspace(int64_t T, int E) { return ((balance_parts(T) + 1) * (E + 1) * 8 + 255) / 256 * 256; }
 
 hipError_t launch_balance(BalanceArgs a, void* workspace, hipStream_t s) {
-  const int parts = (int)balance_parts(a.T);
-  a.total_p = static_cast<double*>(workspace);
-  a.done = reinterpret_cast<int32_t*>(a.total_p + a.E + 1);
-  a.part = reinterpret_cast<int2*>(a.done + 2);
+  int parts = (int)balance_parts(a.T);
+  a.part = static_cast<int2*>(workspace);
   with_logits(a.dtype, rows_of_vectors(a.dtype, a.E, a.logits, a.ld, nullptr, 0), a.E, [&](auto t, auto vec, auto nv) {
-    hipLaunchKernelGGL((k_balance<decltype(t), decltype(vec)::value, decltype(nv)::value>), dim3(parts), dim3(64 * kWaves),
-                       (2 * a.E + 1) * 4, s, a);
+    constexpr int V = decltype(vec)::value, N = decltype(nv)::value;
+    hipLaunchKernelGGL((k_balance<decltype(t), V, N>), dim3(parts), dim3(64 * waves_of<V, N>()), (a.E + 1) * 4, s, a);
   });
-  hipLaunchKernelGGL(k_balance_join, dim3((a.E + 64) / 64), dim3(kJoin), 0, s, a, parts);
+  const int2* part = a.part;
+  if ((int64_t)parts * (a.E + 1) > 65536) {
+    int2* out = a.part + (int64_t)parts * (a.E + 1);
+    hipLaunchKernelGGL(k_balance_columns, dim3((a.E + 64) / 64), dim3(kJoin), 0, s, part, parts, a.E, out);
+    part = out, parts = 1;
+  }
+  hipLaunchKernelGGL(k_balance_join, dim3(1), dim3(kJoin), 0, s, a, part, parts);
   return hipGetLastError();
 }
 
 hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s) {
-  const int grid = (int)std::min<int64_t>(2048, (a.T + kWaves - 1) / kWaves);
+  const int grid = (int)std::min<int64_t>(1024, (a.T + kGradWaves - 1) / kGradWaves);
   with_logits(a.dtype, rows_of_vectors(a.dtype, a.E, a.logits, a.ld, a.dlogits, a.ldd), a.E, [&](auto t, auto vec, auto nv) {
     constexpr int V = decltype(vec)::value, N = decltype(nv)::value;
-    hipLaunchKernelGGL((k_balance_grad<decltype(t), V, N>), dim3(grid), dim3(64 * kWaves), a.w ? kWaves * 64 * V * N * 4 : 0, s, a);
+    hipLaunchKernelGGL((k_balance_grad<decltype(t), V, N>), dim3(grid), dim3(64 * kGradWaves), a.w ? kGradWaves * 64 * V * N * 4 : 0, s, a);
   });
   return hipGetLastError();
 }

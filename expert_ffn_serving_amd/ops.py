@@ -434,7 +434,7 @@ def balance_loss(logits, ids, counts, lse, losses, mask=None, stream=None):
     """eff_balance_loss: the router's losses over tokens with logits [T,E] (float32, bfloat16 or float16) and ids int32
     [T,K] as route writes them.  Writes losses, float32 [2]: E * sum of f * P (1 for an even load), and the mean of lse^2;
     counts, int32 [E+1]: the pairs of every expert, then the live tokens; lse, float32 [T], for balance_loss_backward.
-    mask, bool [T]: tokens that count (padding is not read); a token without a logit above -infinity does not count."""
+    mask, bool [T]: tokens that count (padding may hold anything); a token without a logit above -infinity does not count."""
     try:
         dev = _device("logits", logits)
         T, E, pi, K = _router(logits, ids, dev)

@@ -491,8 +491,8 @@ int eff_layer_norm_backward(int dtype, int w_dtype, const void* dy, int64_t ld_d
 /* The router's losses over T tokens' logits [T,E] (dtype EFF_DT_*; E <= 4096), p = softmax, lse = log sum exp of a row:
  *   losses[0] = E sum over e of f[e] P[e]  (balance: 1 where both are even),  losses[1] = mean of lse^2,
  * f[e] the share of the n K places that id e takes, P[e] the mean of p[t,e], both over the n live tokens.  A token is live
- * if mask (uint8 [T], NULL: all set) is not 0 and some logit is above -infinity; other tokens' logits under a mask of 0 and
- * their ids are not read.  ids int32 [T,K] as eff_route writes them, K <= 32; ids outside [0,E) count nowhere.
+ * if mask (uint8 [T], NULL: all set) is not 0 and some logit is above -infinity; the logits and ids of a token under a mask
+ * of 0 are not used, whatever they hold.  ids int32 [T,K] as eff_route writes them, K <= 32; ids outside [0,E) count nowhere.
  * counts int32 [E+1]: live tokens' pairs of each expert, then n; lse fp32 [T] (-infinity for a token that is not live);
  * losses fp32 [2] (0 where n = 0).  Logits of +infinity or NaN make both losses NaN. */
 int64_t eff_balance_loss_workspace(int64_t T, int num_experts);
@@ -504,7 +504,7 @@ int eff_balance_loss(int dtype, const void* logits, int64_t ld_logits, const int
  * fp32 [2]; NULL: 0; the counts have no gradient) and, with w and dw (fp32 [T,K], both or neither), of routing weights w =
  * softmax over the selected logits whose own gradient is dw (as eff_combine_tokens_backward writes it): the pairs of a
  * token add w[k] (dw[k] - sum w dw) at their ids, over its routed pairs; w and dw of unrouted pairs are not used.  counts
- * and lse as eff_balance_loss wrote them; tokens whose lse is -infinity get zeros and are not read. */
+ * and lse as eff_balance_loss wrote them; tokens whose lse is -infinity get zeros, whatever they hold. */
 int eff_balance_loss_backward(int dtype, const void* logits, int64_t ld_logits, const int32_t* ids, const int32_t* counts,
                               const float* lse, const float* dlosses, const float* w, const float* dw, int64_t T, int K,
                               int num_experts, void* dlogits, int64_t ld_dlogits, eff_stream_t stream);
