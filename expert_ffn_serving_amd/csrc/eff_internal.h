@@ -497,6 +497,8 @@ struct Mx4Args {
 enum { MX_FEW1, MX_FEW2, MX_FEW4, MX_BIG, MX_MID, MX_LOW, MX_THIN };
 int mx4_choice(const eff_mx4_desc& d);
 int mx4_choice(const Mx4Args& a);
+// whether the kernel quantises 16-bit x itself: then x is that, ldx in values, and xs null
+bool mx4_takes_raw(const Mx4Args& a);
 bool mx4_matmul_fits(const Mx4Args& a);
 hipError_t launch_mx4_matmul(const Mx4Args& a, hipStream_t s);
 }  // namespace eff

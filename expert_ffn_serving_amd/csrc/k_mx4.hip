@@ -52,11 +52,14 @@ __device__ inline uint32_t top_of_16(const V& v) {
   for (int i = 1; i < 4; ++i) m = __builtin_elementwise_max(m, w.p[i] & (uint16_t)0x7fff);
   return max((uint32_t)m[0], (uint32_t)m[1]);
 }
-__device__ inline int block_scale(const bf16x8_t& v) { return mx4_scale(quad_max(top_of_16(v)) << 16); }
-__device__ inline int block_scale(const f16x8_t& v) {
-  const uint16_t t = (uint16_t)quad_max(top_of_16(v));
-  return mx4_scale(__float_as_uint((float)__builtin_bit_cast(f16_t, t)));
+// the magnitude's bits in fp32
+__device__ inline uint32_t bits_of_16(const bf16x8_t&, uint32_t top) { return top << 16; }
+__device__ inline uint32_t bits_of_16(const f16x8_t&, uint32_t top) {
+  const uint16_t t = (uint16_t)top;
+  return __float_as_uint((float)__builtin_bit_cast(f16_t, t));
 }
+__device__ inline int block_scale(const bf16x8_t& v) { return mx4_scale(bits_of_16(v, quad_max(top_of_16(v)))); }
+__device__ inline int block_scale(const f16x8_t& v) { return mx4_scale(bits_of_16(v, quad_max(top_of_16(v)))); }
 __device__ inline int block_scale(const f32x8_t& v) {
   uint32_t m = 0;
 #pragma unroll
@@ -213,6 +216,25 @@ k_mx4_dequantize(Mx4Rows a) {
 }
 
 // ---- products --------------------------------------------------------------------------------------------
+
+// 16-bit values at any place (the hardware takes 16-byte loads at any address)
+template <typename T>
+struct Loose8 {
+  typedef typename Vec8<T>::V V __attribute__((aligned(2)));
+};
+// A block of 32 16-bit values in one lane: its codes and scale.
+template <typename V8>
+__device__ inline i32x4_t quantise_block(const V8* v, int* scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, top_of_16(v[i]));
+  *scale = mx4_scale(bits_of_16(v[0], top));
+  const float s = scale_value(*scale);
+  i32x4_t c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = *scale == kNaNScale ? 0 : (int)to_codes(v[i], s);
+  return c;
+}
 
 // 16 W rows against 16 x rows over 128 k: lane (r, q) holds 32 values of row r, the q-th of 4 blocks, and their scale in byte
 // B of sw and sx.  The sums: W rows 4 q .. 4 q + 3 of x row r.
@@ -467,13 +489,17 @@ k_mx4_tile(Mx4Args a) {
 // Up to 16 MT rows of x against 16 rows of W per workgroup (SwiGLU: 8 gate and 8 up rows), the k split over its waves, as
 // k_mm_few does for 16 bits: every wave keeps U chunks of 256 k (2 KiB of W each) in flight in registers, nothing waits for a
 // barrier before the end, where the waves' sums meet in LDS in wave order.
+//
+// RAW: x comes in 16 bits and every wave quantises what it multiplies, a lane its own blocks: for up to 16 rows, whose x
+// is small next to W (16 rows, 4096 -> 2 x 2048: one launch of 7.5 us instead of two of 2.8 and 6, and no workspace).
 template <int MT>
 constexpr int mx4_unroll() { return MT >= 4 ? 1 : 2; }
 
-template <typename T, int MT, bool GLU>
+template <typename T, int MT, bool GLU, bool RAW>
 __global__ void __launch_bounds__(1024)
 k_mx4_few(Mx4Args a, int slices) {
   constexpr int U = mx4_unroll<MT>(), BM = 16 * MT;
+  typedef typename Vec8<T>::V V8;
   extern __shared__ __attribute__((aligned(16))) uint8_t s_few[];
   f32x4_t* s_acc = reinterpret_cast<f32x4_t*>(s_few);  // [waves][MT][64]
   const MmArgs& e = a.e;
@@ -486,18 +512,20 @@ k_mx4_few(Mx4Args a, int slices) {
   const int chunks = (a.units + 1) / 2;
   const int64_t col = min(n0 + (GLU ? r & 7 : r), e.N - 1), wr = col + (GLU && r >= 8 ? e.N : 0);
   const uint8_t *w = a.w + g * a.sw + wr * a.ldw + q * 32, *ws = a.ws + g * a.sws + wr * a.ldws + q * 2;
-  const uint8_t *x[MT], *xs[MT];
+  const uint8_t *x[MT], *xs[MT];  // RAW: x the row's first value
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int64_t row = min(m0 + i * 16 + r, m1 - 1);
-    x[i] = a.x + row * a.ldx + q * 32;
+    x[i] = RAW ? a.x + row * a.ldx * 2 : a.x + row * a.ldx + q * 32;
     xs[i] = a.xs + row * a.ldxs + q * 2;
   }
   f32x4_t acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   i32x4_t fw[U][2], fx[U][MT][2];
+  V8 raw[U][MT][RAW ? 8 : 1];
   int sw[U], sx[U][MT];
+  const int K = (int)e.K;
   const bool odd = a.units & 1;  // the last chunk has one unit: lanes q >= 2 have nothing there
   // chunk c of this wave's into slot s; past the end the first chunk again (not used)
   auto load = [&](int c, int s) {
@@ -506,15 +534,41 @@ k_mx4_few(Mx4Args a, int slices) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       fw[s][h] = *reinterpret_cast<const i32x4_t*>(w + at + h * 16);
+      if constexpr (!RAW) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) fx[s][i][h] = *reinterpret_cast<const i32x4_t*>(x[i] + at + h * 16);
+        for (int i = 0; i < MT; ++i) fx[s][i][h] = *reinterpret_cast<const i32x4_t*>(x[i] + at + h * 16);
+      }
     }
     sw[s] = *reinterpret_cast<const uint16_t*>(ws + as);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) sx[s][i] = *reinterpret_cast<const uint16_t*>(xs[i] + as);
+    for (int i = 0; i < MT; ++i) {
+      if constexpr (RAW) {  // 8 values at a time, k being a multiple of 8; past its end the row's first ones
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          const int k = c * 256 + q * 64 + p * 8;
+          raw[s][i][p] = *reinterpret_cast<const typename Loose8<T>::V*>(reinterpret_cast<const T*>(x[i]) + (c < chunks && k < K ? k : 0));
+        }
+      } else {
+        sx[s][i] = *reinterpret_cast<const uint16_t*>(xs[i] + as);
+      }
+    }
   };
   auto use = [&](int c, int s) {
     if (c >= chunks) return;
+    if constexpr (RAW) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (c == chunks - 1) {
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            if (c * 256 + q * 64 + p * 8 >= K) raw[s][i][p] = V8{};
+        }
+        int first, second;
+        fx[s][i][0] = quantise_block(raw[s][i], &first);
+        fx[s][i][1] = quantise_block(raw[s][i] + 4, &second);
+        sx[s][i] = first | second << 8;
+      }
+    }
     if (odd && c == chunks - 1 && q >= 2) {  // zeros, whatever scales
       fw[s][0] = fw[s][1] = i32x4_t{0, 0, 0, 0};
       sw[s] = 0;
@@ -680,22 +734,22 @@ hipError_t launch_mx4_tile(const Mx4Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int MT, bool GLU>
+template <typename T, int MT, bool GLU, bool RAW>
 hipError_t launch_mx4_few(const Mx4Args& a, hipStream_t s) {
   const int64_t slices = ceil_div(a.e.N, GLU ? 8 : 16), jobs = slices * mx4_rows(a.e, 16 * MT);
   // waves per workgroup: up to 32 per CU over the launch, each with at least two chunks of k, their sums within 64 KiB of LDS
   int waves = 16;
   while (waves > 1 && (jobs * waves > 8192 || waves * 4 > a.units + 3)) waves /= 2;
-  hipLaunchKernelGGL((k_mx4_few<T, MT, GLU>), dim3((unsigned)jobs), dim3(64 * waves), waves * MT * 1024, s, a, (int)slices);
+  hipLaunchKernelGGL((k_mx4_few<T, MT, GLU, RAW>), dim3((unsigned)jobs), dim3(64 * waves), waves * MT * 1024, s, a, (int)slices);
   return hipGetLastError();
 }
 
 template <typename T, bool GLU>
 hipError_t launch_mx4_kind(const Mx4Args& a, int kind, hipStream_t s) {
   switch (kind) {
-    case MX_FEW1: return launch_mx4_few<T, 1, GLU>(a, s);
-    case MX_FEW2: return launch_mx4_few<T, 2, GLU>(a, s);
-    case MX_FEW4: return launch_mx4_few<T, 4, GLU>(a, s);
+    case MX_FEW1: return a.xs ? launch_mx4_few<T, 1, GLU, false>(a, s) : launch_mx4_few<T, 1, GLU, true>(a, s);
+    case MX_FEW2: return launch_mx4_few<T, 2, GLU, false>(a, s);
+    case MX_FEW4: return launch_mx4_few<T, 4, GLU, false>(a, s);
     case MX_BIG: return launch_mx4_tile<T, MxBig, GLU>(a, s);
     case MX_MID: return launch_mx4_tile<T, MxMid, GLU>(a, s);
     case MX_LOW: return launch_mx4_tile<T, MxLow, GLU>(a, s);
@@ -706,6 +760,7 @@ hipError_t launch_mx4_kind(const Mx4Args& a, int kind, hipStream_t s) {
 }  // namespace
 
 int mx4_choice(const Mx4Args& a) { return plan_mx4(a); }
+bool mx4_takes_raw(const Mx4Args& a) { return a.e.K % 8 == 0 && plan_mx4(a) == MX_FEW1; }
 
 // whether the launch holds the problem (a grid's threads stay below 2^32)
 bool mx4_matmul_fits(const Mx4Args& a) {

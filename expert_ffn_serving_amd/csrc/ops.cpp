@@ -158,9 +158,9 @@ Mx4Args mx4_args(const eff_mx4_desc* d) {
   a.sw = d->groups ? d->stride_w : 0, a.sws = d->groups ? d->stride_ws : 0;
   return a;
 }
-// the workspace's first part: x in 4 bits, where it comes in 16
-int64_t x_code_bytes(const eff_mx4_desc* d) { return d->x_dtype == EFF_DT_MX4 ? 0 : align256(d->m * mx4_units(d->k) * 64); }
-int64_t x_scale_bytes(const eff_mx4_desc* d) { return d->x_dtype == EFF_DT_MX4 ? 0 : align256(d->m * mx4_units(d->k) * 4); }
+// the workspace: x in 4 bits, where it comes in 16 and the kernel does not quantise it itself
+int64_t x_code_bytes(const eff_mx4_desc* d) { return align256(d->m * mx4_units(d->k) * 64); }
+int64_t x_scale_bytes(const eff_mx4_desc* d) { return align256(d->m * mx4_units(d->k) * 4); }
 
 }  // namespace
 
@@ -426,7 +426,7 @@ int eff_mx4_dequantize(int dtype, const uint8_t* codes, int64_t ld_codes, const 
 
 int64_t eff_mx4_matmul_workspace(const eff_mx4_desc* d) {
   if (const char* why = check_mx4_desc(d)) return bad("eff_mx4_matmul_workspace", why);
-  if (d->m == 0) return 0;
+  if (d->m == 0 || d->x_dtype == EFF_DT_MX4 || mx4_takes_raw(mx4_args(d))) return 0;
   return x_code_bytes(d) + x_scale_bytes(d);
 }
 
@@ -455,7 +455,9 @@ int eff_mx4_matmul(const eff_mx4_desc* d, const void* x, const uint8_t* xs, cons
   a.e.offsets = offsets, a.e.bias = bias, a.e.residual = residual, a.e.y = y, a.e.pre = pre;
   a.w = w, a.ws = ws, a.x = static_cast<const uint8_t*>(x), a.xs = xs;
   uint8_t* tmp = static_cast<uint8_t*>(workspace);
-  if (!coded) {
+  if (!coded && mx4_takes_raw(a)) {
+    a.ldx = d->ld_x, a.xs = nullptr;
+  } else if (!coded) {
     Mx4Rows q = {};
     q.dtype = d->dtype, q.x = x, q.ldx = d->ld_x, q.rows = d->m, q.k = d->k, q.units = a.units, q.offsets = offsets, q.groups = d->groups;
     q.codes = tmp, q.ldc = a.ldx, q.scales = tmp + x_code_bytes(d), q.lds = a.ldxs;

@@ -493,14 +493,14 @@ def mx4_row_bytes(k):
     return units * 64, units * 4
 
 
-def _flat_rows(name, t):
-    """A matrix, or a stack of them as one matrix."""
-    if t.dim() == 3:
-        try:
-            return t.view(-1, t.shape[2])
-        except RuntimeError:
-            _bad("%s must have one distance between all rows" % name)
-    return t
+def _flat_stack(name, t, codes, scales):
+    """A stack of matrices, its codes and scales as matrices."""
+    if t.dim() != 3 or codes.shape[:-1] != t.shape[:-1] or scales.shape[:-1] != t.shape[:-1]:
+        _bad("%s must be a matrix or a stack of them, codes and scales have its leading sizes" % name)
+    try:
+        return [v.view(-1, v.shape[2]) for v in (t, codes, scales)]
+    except RuntimeError:
+        _bad("%s, codes and scales must each have one distance between all rows" % name)
 
 
 def mx4_quantize(x, codes, scales, stream=None):
@@ -508,14 +508,12 @@ def mx4_quantize(x, codes, scales, stream=None):
     uint8, of x's leading sizes and mx4_row_bytes(k) bytes a row, written.  Rows of codes begin at multiples of 16 bytes."""
     try:
         dev = _device("x", x)
-        if x.shape[:-1] != codes.shape[:-1] or x.shape[:-1] != scales.shape[:-1]:
-            _bad("codes and scales must have x's leading sizes")
-        x2 = _flat_rows("x", x)
+        x2, codes2, scales2 = (x, codes, scales) if x.dim() == 2 else _flat_stack("x", x, codes, scales)
         m, k = _rows_of("x", x2)
         cb, sb = mx4_row_bytes(k)
         px, ldx = _matrix("x", x2, x.dtype, m, k, dev)
-        pc, ldc = _matrix("codes", _flat_rows("codes", codes), _U8, m, cb, dev, True)
-        ps, lds = _matrix("scales", _flat_rows("scales", scales), _U8, m, sb, dev, True)
+        pc, ldc = _matrix("codes", codes2, _U8, m, cb, dev, True)
+        ps, lds = _matrix("scales", scales2, _U8, m, sb, dev, True)
         _call(lib().eff_mx4_quantize, dev, stream, (_DT[x.dtype], px, ldx, m, k, pc, ldc, ps, lds))
         _written((codes, scales))
     except AttributeError as e:
@@ -526,14 +524,12 @@ def mx4_dequantize(codes, scales, y, stream=None):
     """eff_mx4_dequantize: what codes and scales stand for, into y [m,k] or [E,n,k] (bfloat16, float16 or float32)."""
     try:
         dev = _device("y", y)
-        if y.shape[:-1] != codes.shape[:-1] or y.shape[:-1] != scales.shape[:-1]:
-            _bad("codes and scales must have y's leading sizes")
-        y2 = _flat_rows("y", y)
+        y2, codes2, scales2 = (y, codes, scales) if y.dim() == 2 else _flat_stack("y", y, codes, scales)
         m, k = _rows_of("y", y2)
         cb, sb = mx4_row_bytes(k)
         py, ldy = _matrix("y", y2, y.dtype, m, k, dev, True)
-        pc, ldc = _matrix("codes", _flat_rows("codes", codes), _U8, m, cb, dev)
-        ps, lds = _matrix("scales", _flat_rows("scales", scales), _U8, m, sb, dev)
+        pc, ldc = _matrix("codes", codes2, _U8, m, cb, dev)
+        ps, lds = _matrix("scales", scales2, _U8, m, sb, dev)
         _call(lib().eff_mx4_dequantize, dev, stream, (_DT[y.dtype], pc, ldc, ps, lds, m, k, py, ldy))
         _written((y,))
     except AttributeError as e:
@@ -585,7 +581,7 @@ def _mx4(x, w, w_scales, offsets, y, x_scales, bias, act, residual, pre, stream)
         d = _pack_mx4(3 if coded else _HALF[dt], _HALF[dt], _DT[yt], act, groups, 0, m, n, k, ldx, ldxs, ldw, ldws, sw, sws,
                       ldy, ldr, ldp)
         L = lib()
-        _call(L.eff_mx4_matmul, dev, stream, (d, px, pxs, pw, pws, pb, pr, po, py, pp), L.eff_mx4_matmul_workspace(d))
+        _call(L.eff_mx4_matmul, dev, stream, (d, px, pxs, pw, pws, pb, pr, po, py, pp), 0 if coded else L.eff_mx4_matmul_workspace(d))
         _written((y,) if pre is None else (y, pre))
     except AttributeError as e:
         _no_tensor(e)

@@ -329,6 +329,33 @@ def test_operand_strides(eff):
     torch.testing.assert_close(y2.float(), want.float(), rtol=2 ** -7, atol=1e-3)
 
 
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("m,n,k,act", [(1, 40, 8, 0), (3, 72, 136, 4), (16, 64, 1000, 0), (9, 520, 2560, 4), (13, 40, 264, 4), (5, 24, 520, 0)])
+def test_16_bit_rows_quantised_inside(eff, m, n, k, act, dt):
+    """Few rows: the kernel quantises x itself, at any place and row distance, k inside a block, a unit and a chunk of two: the bits
+    of quantising first.  What lies beside the rows may hold anything."""
+    nw = 2 * n if act == R.SWIGLU else n
+    x, wq, ws = operands(eff, m, nw, k, dt, m + k)
+    if k >= 264:
+        x[0, 100], x[m - 1, 5] = 0.0, 3e4
+        x[m // 2, 64:96] = 0
+    want = torch.empty(m, n, dtype=dt, device="cuda")
+    xc, xs = quantised(eff, x.cuda())
+    eff.mx4_matmul(xc, wq, ws, want, x_scales=xs, act=act)
+    for off, pad in ((0, 0), (1, 5), (3, 13)):
+        big = torch.full((m, k + off + pad), NAN, dtype=dt, device="cuda")
+        big[:, off:off + k] = x.cuda()
+        y = torch.empty_like(want)
+        eff.mx4_matmul(big[:, off:off + k], wq, ws, y, act=act)
+        assert torch.equal(y, want), (off, pad)
+    g3 = torch.empty(m, n, dtype=dt, device="cuda")
+    eff.grouped_mx4_matmul(x.cuda(), wq[None], ws[None], torch.tensor([0, m], dtype=I32, device="cuda"), g3, act=act)
+    assert torch.equal(g3, want)
+    x[m - 1, k - 1] = INF
+    eff.mx4_matmul(x.cuda(), wq, ws, g3, act=act)
+    assert torch.isnan(g3[m - 1]).all() and torch.equal(g3[:m - 1], want[:m - 1])
+
+
 def test_residual_in_place_and_no_rows(eff):
     x, wq, ws = operands(eff, 33, 64, 128, BF, 7)
     r = torch.randn(33, 64).to(BF).cuda()

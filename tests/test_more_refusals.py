@@ -127,9 +127,11 @@ def test_products(eff):
     assert product(eff, desc(ld_pre=7), pre=A) == eff.EFF_EINVAL
     assert product(eff, desc(out_dtype=2), residual=A) == eff.EFF_EINVAL  # in place, of another type
     assert product(eff, desc(ld_residual=16), residual=A) == eff.EFF_EINVAL
-    d = desc(x_dtype=0, ld_x=256, ld_xs=0)
+    assert L.eff_mx4_matmul_workspace(ctypes.addressof(desc())) == 0 and L.eff_mx4_matmul_workspace(ctypes.addressof(desc(x_dtype=0, ld_x=256))) == 0
+    assert product(eff, desc(x_dtype=0, ld_x=256)) == eff.EFF_EINVAL      # xs with 16-bit x
+    d = desc(m=4000, x_dtype=0, ld_x=256, ld_xs=0)                         # more rows than the kernel quantises itself
     need = L.eff_mx4_matmul_workspace(ctypes.addressof(d))
-    assert need >= 4 * 128 + 4 * 8 and need % 256 == 0
+    assert need >= 4000 * 128 + 4000 * 8 and need % 256 == 0
     assert product(eff, d) == eff.EFF_EINVAL                               # xs with 16-bit x
     for kw in (dict(tmp=None, n=need), dict(tmp=A, n=need - 1), dict(tmp=A + 16, n=need)):
         assert product(eff, d, xs=None, **kw) == eff.EFF_EINVAL, kw
