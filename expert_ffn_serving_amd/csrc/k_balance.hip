@@ -25,34 +25,48 @@ constexpr int waves_of() { return VEC * NV <= 16 ? 16 : 4; }
 constexpr int kGradWaves = 4;
 constexpr float kInf = __builtin_inff();
 
+// VEC consecutive logits at any place (the hardware takes 16-byte accesses at any address)
 template <typename T, int VEC>
 struct LogitVec {
   typedef T V __attribute__((ext_vector_type(VEC)));
-};
-template <typename T>
-struct LogitVec<T, 1> {
-  typedef T V;
+  typedef V Loose __attribute__((aligned(sizeof(T))));
 };
 
-// A lane's values of a row of E logits: columns (i * 64 + lane) * VEC + e.
-template <typename T, int VEC, int NV>
+// A lane's values of a row of E logits: columns (i * 64 + lane) * VEC + e.  WHOLE: E is a multiple of VEC.
+template <typename T, int VEC, bool WHOLE, int NV>
 struct LogitRow {
   typename LogitVec<T, VEC>::V raw[NV];
   __device__ void load(const T* p, int E, int lane) {  // past the end the row's first values, which are not used
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = (i * 64 + lane) * VEC;
-      raw[i] = *reinterpret_cast<const typename LogitVec<T, VEC>::V*>(p + (j < E ? j : 0));
+      if (WHOLE || E >= VEC) {  // a vector that ends past the row is read from where it ends with it, and moved
+        const int at = j + VEC <= E ? j : j < E ? E - VEC : 0;
+        raw[i] = *reinterpret_cast<const typename LogitVec<T, VEC>::Loose*>(p + at);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) raw[i][e] = p[min(e, E - 1)];
+      }
     }
   }
   __device__ void widen(int E, int lane, float (*v)[VEC]) const {  // past the end -infinity
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      const int j = (i * 64 + lane) * VEC;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if constexpr (VEC == 1) v[i][e] = (i * 64 + lane) * VEC < E ? (float)raw[i] : -kInf;
-        else v[i][e] = (i * 64 + lane) * VEC < E ? (float)raw[i][e] : -kInf;
+      for (int e = 0; e < VEC; ++e) v[i][e] = j + e < E ? (float)raw[i][e] : -kInf;
+      if (!WHOLE && E >= VEC && j < E && j + VEC > E) {
+        const int shift = j + VEC - E;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float from = -kInf;
+#pragma unroll
+          for (int o = 1; o < VEC; ++o)
+            if (o == shift && e + o < VEC) from = (float)raw[i][e + o];
+          v[i][e] = from;
+        }
       }
+    }
   }
 };
 
@@ -76,7 +90,7 @@ __device__ inline void wave_order() {
 }
 // grid: parts.  Wave w of part p takes rows p W + w, then parts W further (W waves); the part's sums of p and of lse^2 and
 // its counts go to one row of the workspace.  2048 x 256: bound by the way to memory and back, two rows a wave.
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, bool WHOLE, int NV>
 __global__ void __launch_bounds__(64 * (waves_of<VEC, NV>()))
 k_balance(BalanceArgs a) {
   constexpr int W = waves_of<VEC, NV>();
@@ -92,7 +106,7 @@ k_balance(BalanceArgs a) {
     for (int e = 0; e < VEC; ++e) sum[i][e] = 0.f;
   // a row is in flight while the one before it is used, masked or not; past the end the last row again, which is not used
   const int64_t step = (int64_t)gridDim.x * W;
-  LogitRow<T, VEC, NV> next;
+  LogitRow<T, VEC, WHOLE, NV> next;
   int next_id = -1, next_set = 1;
   auto fetch = [&](int64_t t) {
     t = min(t, a.T - 1);
@@ -254,7 +268,7 @@ k_balance_join(BalanceArgs a, const int2* __restrict__ part, int parts) {
 }
 
 // grid: as many workgroups as fill the chip; a wave per row.  f of the lane's columns stays in registers.
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, bool WHOLE, int NV>
 __global__ void __launch_bounds__(64 * kGradWaves)
 k_balance_grad(BalanceGradArgs a) {
   constexpr int W = kGradWaves;
@@ -282,7 +296,7 @@ k_balance_grad(BalanceGradArgs a) {
   }
   // a row is in flight while the one before it is used, live or not; past the end the last row again, which is not used
   const int64_t step = (int64_t)gridDim.x * W;
-  LogitRow<T, VEC, NV> next;
+  LogitRow<T, VEC, WHOLE, NV> next;
   float next_lse = -kInf, next_w = 0.f, next_dw = 0.f;
   int next_id = -1;
   auto fetch = [&](int64_t t) {
@@ -367,40 +381,41 @@ k_balance_grad(BalanceGradArgs a) {
     for (int i = 0; i < NV; ++i) {
       const int j = (i * 64 + lane) * VEC;
       if (j >= E) continue;
-      typename LogitVec<T, VEC>::V o;
-      if constexpr (VEC == 1) {
-        o = (T)v[i][0];
-      } else {
+      if (WHOLE || j + VEC <= E) {
+        typename LogitVec<T, VEC>::V o;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) o[e] = (T)v[i][e];
+        *reinterpret_cast<typename LogitVec<T, VEC>::Loose*>(out + j) = o;
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (j + e < E) out[j + e] = (T)v[i][e];
       }
-      *reinterpret_cast<typename LogitVec<T, VEC>::V*>(out + j) = o;
     }
   }
 }
 
-// calls f with the logits' type, the vector width and the vectors of a lane
-template <typename T, int VEC, typename F>
-void with_vectors(int E, F f) {
+// calls f with the logits' type, the vector width, whether it divides E, and the vectors of a lane
+template <typename T, int VEC, typename W, typename F>
+void with_vectors(int E, W whole, F f) {
+  const std::integral_constant<int, VEC> v;
   const int n = (E + 64 * VEC - 1) / (64 * VEC);
-  if (n <= 1) f(T{}, std::integral_constant<int, VEC>{}, std::integral_constant<int, 1>{});
-  else if (n <= 2) f(T{}, std::integral_constant<int, VEC>{}, std::integral_constant<int, 2>{});
-  else if (n <= 4) f(T{}, std::integral_constant<int, VEC>{}, std::integral_constant<int, 4>{});
-  else if (n <= 8) f(T{}, std::integral_constant<int, VEC>{}, std::integral_constant<int, 8>{});
-  else if constexpr (VEC < 8) {
-    if (n <= 16) f(T{}, std::integral_constant<int, VEC>{}, std::integral_constant<int, 16>{});
-    else if constexpr (VEC == 1) f(T{}, std::integral_constant<int, VEC>{}, std::integral_constant<int, 64>{});
-  }
+  if (n <= 1) f(T{}, v, whole, std::integral_constant<int, 1>{});
+  else if (n <= 2) f(T{}, v, whole, std::integral_constant<int, 2>{});
+  else if (n <= 4) f(T{}, v, whole, std::integral_constant<int, 4>{});
+  else if (n <= 8) f(T{}, v, whole, std::integral_constant<int, 8>{});
+  else if constexpr (VEC < 8) f(T{}, v, whole, std::integral_constant<int, 16>{});
 }
 template <typename F>
-void with_logits(int dtype, bool vec, int E, F f) {
-  if (dtype == EFF_DT_F32) vec ? with_vectors<float, 4>(E, f) : with_vectors<float, 1>(E, f);
-  else if (dtype == EFF_DT_BF16) vec ? with_vectors<bf16_t, 8>(E, f) : with_vectors<bf16_t, 1>(E, f);
-  else vec ? with_vectors<f16_t, 8>(E, f) : with_vectors<f16_t, 1>(E, f);
-}
-bool rows_of_vectors(int dtype, int E, const void* p, int64_t ld, const void* q, int64_t ldq) {
-  const int64_t b = dtype == EFF_DT_F32 ? 4 : 2;
-  return E * b % 16 == 0 && (uintptr_t)p % 16 == 0 && ld * b % 16 == 0 && (uintptr_t)q % 16 == 0 && ldq * b % 16 == 0;
+void with_logits(int dtype, int E, F f) {
+  auto go = [&](auto t) {
+    typedef decltype(t) T;
+    constexpr int VEC = 16 / (int)sizeof(T);
+    E % VEC ? with_vectors<T, VEC>(E, std::false_type{}, f) : with_vectors<T, VEC>(E, std::true_type{}, f);
+  };
+  if (dtype == EFF_DT_F32) go(float{});
+  else if (dtype == EFF_DT_BF16) go(bf16_t{});
+  else go(f16_t{});
 }
 
 }  // namespace
@@ -413,9 +428,9 @@ int64_t balance_workspace(int64_t T, int E) { return ((balance_parts(T) + 1) * (
 hipError_t launch_balance(BalanceArgs a, void* workspace, hipStream_t s) {
   int parts = (int)balance_parts(a.T);
   a.part = static_cast<int2*>(workspace);
-  with_logits(a.dtype, rows_of_vectors(a.dtype, a.E, a.logits, a.ld, nullptr, 0), a.E, [&](auto t, auto vec, auto nv) {
+  with_logits(a.dtype, a.E, [&](auto t, auto vec, auto whole, auto nv) {
     constexpr int V = decltype(vec)::value, N = decltype(nv)::value;
-    hipLaunchKernelGGL((k_balance<decltype(t), V, N>), dim3(parts), dim3(64 * waves_of<V, N>()), (a.E + 1) * 4, s, a);
+    hipLaunchKernelGGL((k_balance<decltype(t), V, decltype(whole)::value, N>), dim3(parts), dim3(64 * waves_of<V, N>()), (a.E + 1) * 4, s, a);
   });
   const int2* part = a.part;
   if ((int64_t)parts * (a.E + 1) > 65536) {
@@ -429,9 +444,9 @@ hipError_t launch_balance(BalanceArgs a, void* workspace, hipStream_t s) {
 
 hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s) {
   const int grid = (int)std::min<int64_t>(1024, (a.T + kGradWaves - 1) / kGradWaves);
-  with_logits(a.dtype, rows_of_vectors(a.dtype, a.E, a.logits, a.ld, a.dlogits, a.ldd), a.E, [&](auto t, auto vec, auto nv) {
+  with_logits(a.dtype, a.E, [&](auto t, auto vec, auto whole, auto nv) {
     constexpr int V = decltype(vec)::value, N = decltype(nv)::value;
-    hipLaunchKernelGGL((k_balance_grad<decltype(t), V, N>), dim3(grid), dim3(64 * kGradWaves), a.w ? kGradWaves * 64 * V * N * 4 : 0, s, a);
+    hipLaunchKernelGGL((k_balance_grad<decltype(t), V, decltype(whole)::value, N>), dim3(grid), dim3(64 * kGradWaves), a.w ? kGradWaves * 64 * V * N * 4 : 0, s, a);
   });
   return hipGetLastError();
 }

@@ -18,51 +18,58 @@ namespace {
 typedef _Float16 f16_t;
 typedef __bf16 bf16_t;
 
+// VEC consecutive values at any place (the hardware takes 16-byte accesses at any address)
 template <typename T, int VEC>
 struct NormVec {
   typedef T V __attribute__((ext_vector_type(VEC)));
-};
-template <typename T>
-struct NormVec<T, 1> {
-  typedef T V;
+  typedef V Loose __attribute__((aligned(sizeof(T))));
 };
 template <typename T, int VEC>
 __device__ inline void norm_widen(const typename NormVec<T, VEC>::V& v, float* o) {
-  if constexpr (VEC == 1) {
-    o[0] = (float)v;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) o[i] = (float)v[i];
+}
+// values h .. h + VEC - 1 of a row of H (h < H); WHOLE: H is a multiple of VEC, else zeros past the end
+template <typename T, int VEC, bool WHOLE>
+__device__ inline typename NormVec<T, VEC>::V norm_load(const void* p, int64_t i, int64_t h, int64_t H) {
+  const T* s = reinterpret_cast<const T*>(p) + i + h;
+  typename NormVec<T, VEC>::V v = {};
+  if (WHOLE || h + VEC <= H) {
+    v = *reinterpret_cast<const typename NormVec<T, VEC>::Loose*>(s);
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) o[i] = (float)v[i];
+    for (int e = 0; e < VEC; ++e)
+      if (h + e < H) v[e] = s[e];
   }
+  return v;
 }
-template <typename T, int VEC>
-__device__ inline typename NormVec<T, VEC>::V norm_load(const void* p, int64_t i) {
-  return *reinterpret_cast<const typename NormVec<T, VEC>::V*>(reinterpret_cast<const T*>(p) + i);
-}
-// VEC values of another type than the rows' (weights): as many 16-byte accesses as they take
-template <typename T, int VEC>
-__device__ inline void norm_get(const void* p, int64_t i, float* o) {
+// the same of another type than the rows' (weights): as many 16-byte accesses as they take
+template <typename T, int VEC, bool WHOLE>
+__device__ inline void norm_get(const void* p, int64_t h, int64_t H, float* o) {
   constexpr int C = VEC * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : VEC;
 #pragma unroll
-  for (int c = 0; c < VEC; c += C) norm_widen<T, C>(norm_load<T, C>(p, i + c), o + c);
+  for (int c = 0; c < VEC; c += C) {
+    if (WHOLE || h + c < H) {
+      norm_widen<T, C>(norm_load<T, C, WHOLE>(p, 0, h + c, H), o + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < C; ++e) o[c + e] = 0.f;
+    }
+  }
 }
-template <typename T, int VEC>
-__device__ inline void norm_store(void* p, int64_t i, const float* v) {
-  typename NormVec<T, VEC>::V o;
-  if constexpr (VEC == 1) {
-    o = (T)v[0];
-  } else {
+template <typename T, int VEC, bool WHOLE>
+__device__ inline void norm_store(void* p, int64_t i, int64_t h, int64_t H, const float* v) {
+  T* d = reinterpret_cast<T*>(p) + i + h;
+  if (WHOLE || h + VEC <= H) {
+    typename NormVec<T, VEC>::V o;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) o[e] = (T)v[e];
-  }
-  *reinterpret_cast<typename NormVec<T, VEC>::V*>(reinterpret_cast<T*>(p) + i) = o;
-}
-
-template <int VEC>
-__device__ inline void norm_put_f32(float* p, const float* v) {
-  constexpr int C = VEC > 4 ? 4 : VEC;
+    *reinterpret_cast<typename NormVec<T, VEC>::Loose*>(d) = o;
+  } else {
 #pragma unroll
-  for (int c = 0; c < VEC; c += C) norm_store<float, C>(p, c, v + c);
+    for (int e = 0; e < VEC; ++e)
+      if (h + e < H) d[e] = (T)v[e];
+  }
 }
 
 // sums of N values over the TH threads of a row (TH = 64: the wave; else the wave's sums meet in LDS, s: [TH / 64][N],
@@ -87,31 +94,26 @@ __device__ inline void row_sum(float* v, float* s) {
   }
 }
 
-// grid: ceil(T / R) workgroups of R rows, TH threads each
-template <typename T, typename W, int VEC, int TH, int NV, int R>
+// grid: ceil(T / R) workgroups of R rows, TH threads each.  Bound by HBM: 8192 x 4096 bf16 30 us, 4.5 TB/s (a plain copy 5.0).
+template <typename T, typename W, int VEC, bool WHOLE, int TH, int NV, int R>
 __global__ void __launch_bounds__(TH * R)
 k_norm(NormArgs a) {
   __shared__ float s_sum[R][2][TH / 64 * 2];
   const int sub = threadIdx.x / TH, tid = threadIdx.x % TH;
   const int64_t row = (int64_t)blockIdx.x * R + sub;
   const bool live = row < a.T;
-  const T* x = reinterpret_cast<const T*>(a.x) + (live ? row : a.T - 1) * a.ldx;
+  const int64_t at = (live ? row : a.T - 1) * a.ldx;
   const float inv = 1.0f / (float)a.H;
-  typename NormVec<T, VEC>::V raw[NV];
+  float v[NV][VEC], sum[2] = {0.f, 0.f};
+  typename NormVec<T, VEC>::V raw[NV] = {};
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int64_t h = (int64_t)(i * TH + tid) * VEC;
-    if (h < a.H) raw[i] = norm_load<T, VEC>(x, h);
+    if (h < a.H) raw[i] = norm_load<T, VEC, WHOLE>(a.x, at, h, a.H);
   }
-  float v[NV][VEC], sum[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if ((int64_t)(i * TH + tid) * VEC < a.H) {
-      norm_widen<T, VEC>(raw[i], v[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[i][e] = 0.f;
-    }
+    norm_widen<T, VEC>(raw[i], v[i]);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) sum[0] += v[i][e];
   }
@@ -119,15 +121,17 @@ k_norm(NormArgs a) {
   const float first = sum[0] * inv;
   float dev[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if ((int64_t)(i * TH + tid) * VEC < a.H) {
+  for (int i = 0; i < NV; ++i) {
+    const int64_t h = (int64_t)(i * TH + tid) * VEC;
+    if (h < a.H) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        v[i][e] -= first;
+        v[i][e] = WHOLE || h + e < a.H ? v[i][e] - first : 0.f;
         dev[0] += v[i][e];
         dev[1] = fmaf(v[i][e], v[i][e], dev[1]);
       }
     }
+  }
   row_sum<TH, 2>(dev, s_sum[sub][1]);
   const float more = dev[0] * inv;
   const float rstd = 1.0f / sqrtf(fmaxf(dev[1] * inv - more * more, 0.f) + a.eps + 0.f * dev[1]);
@@ -141,8 +145,8 @@ k_norm(NormArgs a) {
     const int64_t h = (int64_t)(i * TH + tid) * VEC;
     if (h >= a.H) continue;
     float w[VEC], b[VEC];
-    if (a.w) norm_get<W, VEC>(a.w, h, w);
-    if (a.b) norm_get<W, VEC>(a.b, h, b);
+    if (a.w) norm_get<W, VEC, WHOLE>(a.w, h, a.H, w);
+    if (a.b) norm_get<W, VEC, WHOLE>(a.b, h, a.H, b);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       float y = (v[i][e] - more) * rstd;
@@ -150,7 +154,7 @@ k_norm(NormArgs a) {
       if (a.b) y += b[e];
       v[i][e] = y;
     }
-    norm_store<T, VEC>(a.y, row * a.ldy + h, v[i]);
+    norm_store<T, VEC, WHOLE>(a.y, row * a.ldy, h, a.H, v[i]);
   }
 }
 
@@ -191,10 +195,17 @@ k_norm_long(NormArgs a) {
 
 // ---- gradients -------------------------------------------------------------------------------------------
 
+template <int VEC, bool WHOLE>
+__device__ inline void put_f32(float* p, int64_t h, int64_t H, const float* v) {
+#pragma unroll
+  for (int c = 0; c < VEC; c += 4)
+    if (WHOLE || h + c < H) norm_store<float, 4, WHOLE>(p, 0, h + c, H, v + c);
+}
+
 // grid: parts workgroups, workgroup p takes rows p R + sub, then parts R further.  dx as rows go by; the columns' sums of
 // dy xh and dy stay in the registers of the thread that owns the column, are added over the workgroup's R rows in LDS and
 // written as one row of partial sums [parts][2][H], which k_norm_join adds in order.
-template <typename T, typename W, int VEC, int TH, int NV, int R>
+template <typename T, typename W, int VEC, bool WHOLE, int TH, int NV, int R>
 __global__ void __launch_bounds__(TH * R)
 k_norm_grad(NormGradArgs a) {
   __shared__ float s_sum[R][2][TH / 64 * 2];
@@ -208,7 +219,7 @@ k_norm_grad(NormGradArgs a) {
     const int64_t h = (int64_t)(i * TH + tid) * VEC;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) w[i][e] = 1.f, sw[i][e] = sb[i][e] = 0.f;
-    if (a.w && h < a.H) norm_get<W, VEC>(a.w, h, w[i]);
+    if (a.w && h < a.H) norm_get<W, VEC, WHOLE>(a.w, h, a.H, w[i]);
   }
   // a row is in flight while the one before it is used, where the registers hold both; past the end the last row again, not used
   constexpr bool AHEAD = NV * VEC <= 8;
@@ -221,9 +232,9 @@ k_norm_grad(NormGradArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t h = (int64_t)(i * TH + tid) * VEC, at = h < a.H ? h : 0;
-      xn[i] = norm_load<T, VEC>(a.x, row * a.ldx + at);
-      dn[i] = norm_load<T, VEC>(a.dy, row * a.lddy + at);
-      if (a.residual) rn[i] = norm_load<T, VEC>(a.residual, row * a.ldr + at);
+      xn[i] = norm_load<T, VEC, WHOLE>(a.x, row * a.ldx, at, a.H);
+      dn[i] = norm_load<T, VEC, WHOLE>(a.dy, row * a.lddy, at, a.H);
+      if (a.residual) rn[i] = norm_load<T, VEC, WHOLE>(a.residual, row * a.ldr, at, a.H);
     }
   };
   int phase = 0;
@@ -275,7 +286,7 @@ k_norm_grad(NormGradArgs a) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) g[i][e] += r[e];
       }
-      norm_store<T, VEC>(a.dx, row * a.lddx + h, g[i]);
+      norm_store<T, VEC, WHOLE>(a.dx, row * a.lddx, h, a.H, g[i]);
     }
   }
   if (!cols) return;
@@ -298,10 +309,10 @@ k_norm_grad(NormGradArgs a) {
             for (int r = 1; r < R; ++r) v += s_col[(r * VEC + e) * TH + tid];
             (k ? sb : sw)[i][e] = v;
           }
-          norm_put_f32<VEC>(part + k * a.H + h, (k ? sb : sw)[i]);
+          put_f32<VEC, WHOLE>(part + k * a.H, h, a.H, (k ? sb : sw)[i]);
         }
       } else if (h < a.H) {
-        norm_put_f32<VEC>(part + k * a.H + h, (k ? sb : sw)[i]);
+        put_f32<VEC, WHOLE>(part + k * a.H, h, a.H, (k ? sb : sw)[i]);
       }
     }
 }
@@ -375,57 +386,32 @@ k_norm_join(const float* __restrict__ part, int64_t parts, int64_t H, void* dw, 
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-bool whole_vectors(int bytes, int64_t H, std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> lds) {
-  if (H * bytes % 16) return false;
-  for (const void* p : ptrs)
-    if ((uintptr_t)p % 16) return false;
-  for (int64_t l : lds)
-    if (l * bytes % 16) return false;
-  return true;
-}
-
 template <int TH, int NV, int R>
 struct NormShape {
   static constexpr int th = TH, nv = NV, r = R;
 };
 
 // calls f with the shape for rows of n vectors, or g where the registers hold no such row
-template <bool VECTORS, typename F, typename G>
+template <typename F, typename G>
 void with_shape(int64_t n, F f, G g) {
-  if constexpr (VECTORS) {
-    if (n <= 64) f(NormShape<64, 1, 4>{});
-    else if (n <= 128) f(NormShape<64, 2, 4>{});
-    else if (n <= 256) f(NormShape<256, 1, 2>{});
-    else if (n <= 512) f(NormShape<256, 2, 2>{});
-    else if (n <= 1024) f(NormShape<256, 4, 2>{});
-    else if (n <= 2048) f(NormShape<1024, 2, 1>{});
-    else g();
-  } else {
-    if (n <= 256) f(NormShape<64, 4, 4>{});
-    else if (n <= 1024) f(NormShape<256, 4, 2>{});
-    else if (n <= 4096) f(NormShape<256, 16, 2>{});
-    else if (n <= 16384) f(NormShape<1024, 16, 1>{});
-    else g();
-  }
+  if (n <= 64) f(NormShape<64, 1, 4>{});
+  else if (n <= 128) f(NormShape<64, 2, 4>{});
+  else if (n <= 256) f(NormShape<256, 1, 2>{});
+  else if (n <= 512) f(NormShape<256, 2, 2>{});
+  else if (n <= 1024) f(NormShape<256, 4, 2>{});
+  else if (n <= 2048) f(NormShape<1024, 2, 1>{});
+  else g();
 }
 // the same for the gradients, whose threads hold the columns' sums besides
-template <bool VECTORS, typename F, typename G>
+template <typename F, typename G>
 void with_grad_shape(int64_t n, F f, G g) {
-  if constexpr (VECTORS) {
-    if (n <= 64) f(NormShape<64, 1, 4>{});
-    else if (n <= 128) f(NormShape<128, 1, 4>{});
-    else if (n <= 256) f(NormShape<256, 1, 2>{});
-    else if (n <= 512) f(NormShape<512, 1, 2>{});
-    else if (n <= 1024) f(NormShape<1024, 1, 1>{});
-    else if (n <= 2048) f(NormShape<1024, 2, 1>{});
-    else g();
-  } else {
-    if (n <= 256) f(NormShape<64, 4, 4>{});
-    else if (n <= 1024) f(NormShape<256, 4, 2>{});
-    else if (n <= 4096) f(NormShape<512, 8, 2>{});
-    else if (n <= 16384) f(NormShape<1024, 16, 1>{});
-    else g();
-  }
+  if (n <= 64) f(NormShape<64, 1, 4>{});
+  else if (n <= 128) f(NormShape<128, 1, 4>{});
+  else if (n <= 256) f(NormShape<256, 1, 2>{});
+  else if (n <= 512) f(NormShape<512, 1, 2>{});
+  else if (n <= 1024) f(NormShape<1024, 1, 1>{});
+  else if (n <= 2048) f(NormShape<1024, 2, 1>{});
+  else g();
 }
 
 // calls f with the rows' and the weights' types
@@ -442,9 +428,6 @@ constexpr int64_t kNormGrid = 1 << 22;  // workgroups of up to 1024 threads: a g
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-  const int b = a.dtype == EFF_DT_F32 ? 4 : 2;
-  // the weights' vectors are no larger than 16 bytes: 16-byte aligned is enough
-  const bool vec = whole_vectors(b, a.H, {a.x, a.y, a.w, a.b}, {a.ldx, a.ldy});
   with_types(a.dtype, a.w_dtype, [&](auto t, auto wt) {
     typedef decltype(t) T;
     typedef decltype(wt) W;
@@ -460,19 +443,15 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
         launch(p, dim3((unsigned)cdiv(p.T, per)));
       }
     };
-    auto lengthy = [&] {
-      rows([&](const NormArgs& p, dim3 g) { hipLaunchKernelGGL((k_norm_long<T, W>), g, dim3(kLongThreads), 0, s, p); }, 1);
+    auto go = [&](auto sh, auto whole) {
+      typedef decltype(sh) S;
+      rows([&](const NormArgs& p, dim3 g) {
+        hipLaunchKernelGGL((k_norm<T, W, VEC, decltype(whole)::value, S::th, S::nv, S::r>), g, dim3(S::th * S::r), 0, s, p);
+      }, S::r);
     };
-    if (vec)
-      with_shape<true>(a.H / VEC, [&](auto sh) {
-        typedef decltype(sh) S;
-        rows([&](const NormArgs& p, dim3 g) { hipLaunchKernelGGL((k_norm<T, W, VEC, S::th, S::nv, S::r>), g, dim3(S::th * S::r), 0, s, p); }, S::r);
-      }, lengthy);
-    else
-      with_shape<false>(a.H, [&](auto sh) {
-        typedef decltype(sh) S;
-        rows([&](const NormArgs& p, dim3 g) { hipLaunchKernelGGL((k_norm<T, W, 1, S::th, S::nv, S::r>), g, dim3(S::th * S::r), 0, s, p); }, S::r);
-      }, lengthy);
+    with_shape(cdiv(a.H, VEC), [&](auto sh) { a.H % VEC ? go(sh, std::false_type{}) : go(sh, std::true_type{}); }, [&] {
+      rows([&](const NormArgs& p, dim3 g) { hipLaunchKernelGGL((k_norm_long<T, W>), g, dim3(kLongThreads), 0, s, p); }, 1);
+    });
   });
   return hipGetLastError();
 }
@@ -481,8 +460,6 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
 int64_t norm_parts(int64_t T, int64_t H) { return std::min<int64_t>(T, H <= 512 ? 1024 : H <= 2048 ? 512 : 256); }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
-  const int b = a.dtype == EFF_DT_F32 ? 4 : 2;
-  const bool vec = whole_vectors(b, a.H, {a.x, a.dy, a.dx, a.w, a.residual}, {a.ldx, a.lddy, a.dx ? a.lddx : 0, a.residual ? a.ldr : 0});
   const int64_t parts = norm_parts(a.T, a.H);
   with_types(a.dtype, a.w_dtype, [&](auto t, auto wt) {
     typedef decltype(t) T;
@@ -501,18 +478,14 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
       }
       if (a.part) hipLaunchKernelGGL((k_norm_cols_long<T>), dim3((unsigned)cdiv(a.H, 256), (unsigned)parts), dim3(256), 0, s, a);
     };
-    auto go = [&](auto sh, auto vecs) {
+    auto go = [&](auto sh, auto whole) {
       typedef decltype(sh) S;
-      constexpr int V = decltype(vecs)::value;
-      const int64_t grid = std::min(parts, cdiv(a.T, S::r));
-      written = grid;
-      const int lds = S::r > 1 ? S::r * S::th * V * 4 : 0;
-      hipLaunchKernelGGL((k_norm_grad<T, W, V, S::th, S::nv, S::r>), dim3((unsigned)grid), dim3(S::th * S::r), lds, s, a);
+      written = std::min(parts, cdiv(a.T, S::r));
+      const int lds = S::r > 1 ? S::r * S::th * VEC * 4 : 0;
+      hipLaunchKernelGGL((k_norm_grad<T, W, VEC, decltype(whole)::value, S::th, S::nv, S::r>), dim3((unsigned)written), dim3(S::th * S::r),
+                         lds, s, a);
     };
-    if (a.T > 0) {
-      if (vec) with_grad_shape<true>(a.H / VEC, [&](auto sh) { go(sh, std::integral_constant<int, VEC>{}); }, lengthy);
-      else with_grad_shape<false>(a.H, [&](auto sh) { go(sh, std::integral_constant<int, 1>{}); }, lengthy);
-    }
+    if (a.T > 0) with_grad_shape(cdiv(a.H, VEC), [&](auto sh) { a.H % VEC ? go(sh, std::false_type{}) : go(sh, std::true_type{}); }, lengthy);
     if (a.dw || a.db)
       hipLaunchKernelGGL((k_norm_join<W>), dim3((unsigned)cdiv(a.H, 64), 2), dim3(1024), 0, s, a.part, a.T > 0 ? written : 0, a.H, a.dw, a.db);
   });
