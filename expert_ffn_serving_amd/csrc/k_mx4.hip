@@ -711,7 +711,7 @@ int plan_mx4(const Mx4Args& a) {
       {MX_BIG, MxBig::BM, MxBig::BN, 1, 1.65, 1.65, 12}, {MX_MID, MxMid::BM, MxMid::BN, 2, 1.05, 1.5, 4.5},
       {MX_LOW, MxLow::BM, MxLow::BN, 2, 0.62, 0.9, 3.5}, {MX_THIN, MxThin::BM, MxThin::BN, 2, 0.45, 0.7, 3.3}};
   for (const auto& t : tiles) {
-    if (far * std::max(t.bm, t.bn) >= (int64_t)1 << 32 || (t.kind == MX_THIN && (!grouped || rows > 8))) continue;
+    if (far > 0xffffffffll / std::max(t.bm, t.bn) || (t.kind == MX_THIN && (!grouped || rows > 8))) continue;
     const double rt = grouped ? std::max<double>((double)ceil_div(rows, t.bm) * groups, e.M / (double)t.bm) : (double)ceil_div(e.M, t.bm);
     const double count = rt * ceil_div(n, t.bn), full = std::floor(count / (256.0 * t.occ)), rest = count - full * 256 * t.occ;
     offer(t.kind, full * (t.step * steps + t.fixed) + (rest > 0 ? (rest <= 256 ? t.alone : t.step) * steps + t.fixed : 0));
@@ -773,7 +773,7 @@ hipError_t launch_mx4_matmul(const Mx4Args& in, hipStream_t s) {
   e.vec = aligned16({e.y, e.bias, e.residual, e.pre}, {e.N, e.ldy, e.residual ? e.ldr : 0, e.pre ? e.ldp : 0}, 2);
   e.stream = e.M * e.N * (e.y_f32 ? 4 : 2) > (int64_t)256 << 20;  // past the caches, as launch_matmul
   e.simple = e.vec && !e.bias && !e.pre && !e.y_f32 && (e.act == EFF_ACT_NONE || e.act == EFF_ACT_SWIGLU);
-  const int kind = plan_mx4(a);
+  const int kind = a.xs ? plan_mx4(a) : MX_FEW1;  // the other kernels take no 16-bit x
   const bool glu = e.act == EFF_ACT_SWIGLU;
   if (e.dtype == EFF_DT_BF16) return glu ? launch_mx4_kind<bf16_t, true>(a, kind, s) : launch_mx4_kind<bf16_t, false>(a, kind, s);
   return glu ? launch_mx4_kind<f16_t, true>(a, kind, s) : launch_mx4_kind<f16_t, false>(a, kind, s);

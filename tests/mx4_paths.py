@@ -12,3 +12,7 @@ PATHS = [
     (BIG, 4090, 4088, 1100, 0, 0), (BIG, 4000, 2040, 1152, 4, 0), (BIG, 8000, 4088, 1100, 0, 4), (BIG, 8000, 2040, 1152, 4, 4),
     (THIN, 100, 520, 1152, 0, 64), (THIN, 130, 264, 1100, 4, 64), (THIN, 300, 1032, 500, 0, 70),
 ]
+
+# (m, n, k) of few rows and many columns of a row so wide that codes of such rows, each at its own place, would lie too far apart
+# for a tile, while one row in place of all does not
+ONE_ROW_WIDE = (16, 32768, 1 << 26)

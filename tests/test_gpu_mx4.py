@@ -7,7 +7,7 @@ import torch
 from tests import block_ref as B
 from tests import ops_ref as R
 from tests.matmul_paths import group_sizes
-from tests.mx4_paths import PATHS
+from tests.mx4_paths import ONE_ROW_WIDE, PATHS
 
 pytestmark = pytest.mark.gpu
 BF, HF, F32, I32, U8 = torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8
@@ -354,6 +354,22 @@ def test_16_bit_rows_quantised_inside(eff, m, n, k, act, dt):
     x[m - 1, k - 1] = INF
     eff.mx4_matmul(x.cuda(), wq, ws, g3, act=act)
     assert torch.isnan(g3[m - 1]).all() and torch.equal(g3[:m - 1], want[:m - 1])
+
+
+def test_one_very_wide_16_bit_row_for_all(eff):
+    """x and W one row each, broadcast: -1, 0 and 1 are whole numbers in 4 bits, and so are the sums below 2^24 in fp32, in any order."""
+    m, n, k = ONE_ROW_WIDE
+    g = torch.Generator().manual_seed(3)
+    x, w = (torch.randint(-1, 2, (1, k), generator=g, dtype=torch.int8) for _ in range(2))
+    want = int((x.int() * w.int()).sum())
+    assert 0 < abs(want) < 1 << 24 and int((x & 1).sum()) > 1 << 24
+    xc = x.cuda().to(BF)
+    wq, ws = quantised(eff, w.cuda().to(BF))
+    y = torch.empty(m, n, dtype=F32, device="cuda")
+    eff.mx4_matmul(xc.expand(m, -1), wq.expand(n, -1), ws.expand(n, -1), y)
+    assert (y == want).all()
+    del x, w, xc, wq, ws, y
+    torch.cuda.empty_cache()
 
 
 def test_residual_in_place_and_no_rows(eff):

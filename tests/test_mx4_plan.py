@@ -7,7 +7,7 @@ import subprocess
 import pytest
 
 from expert_ffn_serving_amd.ops import Mx4Desc, mx4_row_bytes
-from tests.mx4_paths import BIG, FEW1, FEW2, FEW4, LOW, MID, PATHS, THIN
+from tests.mx4_paths import BIG, FEW1, FEW2, FEW4, LOW, MID, ONE_ROW_WIDE, PATHS, THIN
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 TILE_ROWS = {BIG: 256, MID: 128, LOW: 128, THIN: 128}     # the larger side of a tile
@@ -51,3 +51,12 @@ def test_what_a_tiles_offsets_reach(choice):
         if kind in TILE_ROWS:
             assert TILE_ROWS[kind] * ld < 1 << 32
     assert choice(8192, 4096, 4096) == BIG and choice(8192, 4096, 4096, ld=1 << 24) == MID and choice(8192, 4096, 4096, ld=1 << 25) == FEW4
+    assert choice(8192, 4096, 4096, ld=1 << 58) == FEW4    # whose product with a tile's rows passes 64 bits
+
+
+def test_16_bit_rows_are_planned_once(choice):
+    """Distances of x decide with whether a tile can be taken.  16-bit rows that the kernel quantises itself have other ones than
+    their codes would: a case where the two would choose differently, which tests/test_gpu_mx4.py runs."""
+    m, n, k = ONE_ROW_WIDE
+    cb, _ = mx4_row_bytes(k)
+    assert choice(m, n, k, ld=cb) == FEW1 and choice(m, n, k, ld=16) in TILE_ROWS
