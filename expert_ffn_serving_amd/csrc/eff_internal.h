@@ -492,6 +492,7 @@ struct Mx4Args {
   const uint8_t *x, *xs, *w, *ws;
   int64_t ldx, ldxs, ldw, ldws, sw, sws;  // bytes between rows, and between groups
   int units;
+  int tiles;  // set by the launch
 };
 // Which kernel a product takes: W streamed past 16, 32 or 64 rows, or tiles of 256 x 256, 128 x 128, 64 x 128 or 16 x 128.
 enum { MX_FEW1, MX_FEW2, MX_FEW4, MX_BIG, MX_MID, MX_LOW, MX_THIN };

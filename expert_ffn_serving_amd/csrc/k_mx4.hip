@@ -254,6 +254,12 @@ __device__ inline f32x4_t mfma4(i32x4_t w, i32x4_t x, f32x4_t c, int sw, int sx)
 //
 // Scales come to LDS for two steps at a time, 16 bytes a row (one line of a row holds those of 16 steps: fetched step by step
 // it would be requested as often as the codes' lines): [buffer][row][16], x rows first.
+//
+// 256 x 256 (AHEAD) is bound by the power that the matrix cores draw: 8192 x 8192 x 8192 270 us, 4.1 PFLOP/s, 8192 x 2 x 4096 x 4096
+// SwiGLU 155 us, 3.5; the instructions alone, on random codes in registers, reach 6.1 (8.7 on zeros).  Its workgroups, one a
+// CU, take tile after tile where the sums are stored from registers, the next tile's first step on its way meanwhile: 162 -> 157,
+// 277 -> 271 us.  64 x 128 for groups is bound by W's way through LDS: 12288 rows over 256 experts, 4096 -> 2 x 2048, 470 us,
+// 4.9 TB/s of W.
 template <int BM, int BN, int WM, int WN, int S, bool AHEAD>
 using MxCfg = TileCfg<BM, BN, WM, WN, 64, S, AHEAD>;
 
@@ -264,7 +270,7 @@ constexpr int scale_buffers(int S) { return (S + 2) / 2; }
 template <typename T, class C, bool GLU>
 __global__ void __launch_bounds__(C::TH)
 k_mx4_tile(Mx4Args a) {
-  constexpr int BM = C::BM, BN = C::BN, S = C::S, TH = C::TH, CK = 8, KB = 256;
+  constexpr int BM = C::BM, BN = C::BN, S = C::S, TH = C::TH, CK = 8;
   constexpr int TM = BM / C::WM, TN = BN / C::WN, MT = TM / 16, NT = TN / 16;
   constexpr int HALVES = GLU ? 2 : 1, NTH = NT / HALVES, TNH = TN / HALVES, BNH = BN / HALVES, RUN = NTH * 4;
   constexpr int XB = BM * 128, WB = BN * 128, STEP = XB + WB, SCALES = (BM + BN) * 16, SB = scale_buffers(S);
@@ -274,46 +280,54 @@ k_mx4_tile(Mx4Args a) {
   constexpr int CP = (ALL_X ? SX : 0) + SW;  // at least
   static_assert(C::BK == 64 && BN * CK % TH == 0 && BN * 4 % TH == 0 && (ALL_X || SX == 1) && (ALL_XS || SCX == 1) && TNH % 16 == 0 && NT % HALVES == 0, "tile");
   extern __shared__ __attribute__((aligned(128))) uint8_t s_tile[];
-  const int tid = threadIdx.x, lane = tid & 63, q = lane >> 4, r = lane & 15;
+  int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave % C::WM, wn = wave / C::WM;
   const MmArgs& e = a.e;
 
   const int nt = (int)((e.N + BNH - 1) / BNH);
-  int g = 0, nt_i;
-  int64_t m0, m1;
-  if (e.mode == MM_ROW_GROUPS) {
-    nt_i = blockIdx.x % nt;
-    if (!find_tile<BM>(e.offsets, e.groups, e.M, blockIdx.x / nt, reinterpret_cast<int*>(s_tile), &g, &m0, &m1)) return;
-  } else {
-    // an XCD's workgroups take a contiguous part of the tiles, in bands of 8 row tiles, as in k_mm_tile
-    const int all = gridDim.x, xcd = blockIdx.x & 7, id = xcd * (all >> 3) + min(xcd, all & 7) + (blockIdx.x >> 3);
+  int g = 0, nt_i, job = blockIdx.x;
+  int64_t m0, m1, n0;
+  // an XCD's workgroups take a contiguous part of the tiles, in bands of 8 row tiles, as in k_mm_tile
+  auto locate = [&]() __attribute__((always_inline)) {
+    const int all = a.tiles, xcd = job & 7, id = xcd * (all >> 3) + min(xcd, all & 7) + (job >> 3);
     const int mts = all / nt, band = id / (8 * nt), in_band = id - band * 8 * nt, height = min(8, mts - band * 8);
     nt_i = in_band / height;
     m0 = (int64_t)(band * 8 + in_band % height) * BM;
     m1 = min(e.M, m0 + BM);
+    n0 = (int64_t)nt_i * BNH;
+  };
+  if (e.mode == MM_ROW_GROUPS) {
+    nt_i = blockIdx.x % nt;
+    if (!find_tile<BM>(e.offsets, e.groups, e.M, blockIdx.x / nt, reinterpret_cast<int*>(s_tile), &g, &m0, &m1)) return;
+    n0 = (int64_t)nt_i * BNH;
+  } else {
+    locate();
   }
-  const int64_t n0 = (int64_t)nt_i * BNH;
 
-  // this thread's copies: byte offsets from uniform addresses that advance with the steps (plan_mx4 keeps them < 2^32)
-  const uint8_t *bx = a.x + m0 * a.ldx, *bw = a.w + g * a.sw + n0 * a.ldw;
-  const int64_t up_codes = GLU ? e.N * a.ldw : 0;
+  const int64_t up_codes = GLU ? e.N * a.ldw : 0, up_scales = GLU ? e.N * a.ldws : 0;
   const int bytes = a.units * 64;
-  uint32_t ox[SX], ow[SW], osx[SCX], osw[SCW];
-  const int cx = (tid % CK) ^ swz_rows<64, 1>(tid / CK), cw = (tid % CK) ^ swz_rows<64, RUN>(tid / CK);  // the chunk of every copy
-  static_assert(TH / CK % 8 == 0 && TH / CK % (2 * RUN) == 0, "copies TH / CK rows apart have the same chunk");
-  auto x_row_at = [&](int row) { return min((int64_t)row, m1 - 1 - m0); };                                // of an LDS row, from m0
-  auto w_row_at = [&](int row) { return min((int64_t)((row / TN) * TNH + row % TNH), e.N - 1 - n0); };  // and from n0
-#pragma unroll
-  for (int i = 0; i < SX; ++i) ox[i] = (uint32_t)(x_row_at((i * TH + tid) / CK) * a.ldx + cx * 16);
-#pragma unroll
-  for (int i = 0; i < SW; ++i) ow[i] = (uint32_t)(w_row_at((i * TH + tid) / CK) * a.ldw + cw * 16);
-#pragma unroll
-  for (int i = 0; i < SCX; ++i) osx[i] = (uint32_t)(x_row_at((i * TH + tid) / 4) * a.ldxs + (tid & 3) * 4);
-#pragma unroll
-  for (int i = 0; i < SCW; ++i) osw[i] = (uint32_t)(w_row_at((i * TH + tid) / 4) * a.ldws + (tid & 3) * 4);
-  const uint8_t *bxs = a.xs + m0 * a.ldxs, *bws = a.ws + g * a.sws + n0 * a.ldws;
-  const int64_t up_scales = GLU ? e.N * a.ldws : 0;
+  // This thread's copies: byte offsets from uniform addresses that advance with the steps (plan_mx4 keeps them < 2^32), of the
+  // first one and of the tile's last row; the others are a fixed number of rows further and end there.
+  const uint8_t *bx, *bw, *bxs, *bws;
+  uint32_t ox, ow, osx, osw, endx, endw, endsx, endsw;
+  constexpr int PER = TH / CK, PERS = TH / 4;  // LDS rows of a copy
+  static_assert((PER % TNH == 0 || TNH % PER == 0) && (PERS % TNH == 0 || TNH % PERS == 0), "copies of rows side by side");
+  auto w_at = [](int row) { return (row / TN) * TNH + row % TNH; };
+  // the chunk of every copy
+  auto chunk_x = [&] { return (tid % CK) ^ swz_rows<64, 1>(tid / CK); };
+  auto chunk_w = [&] { return (tid % CK) ^ swz_rows<64, RUN>(tid / CK); };
+  static_assert(PER % 8 == 0 && PER % (2 * RUN) == 0, "copies PER rows apart have the same chunk");
+  auto aim = [&]() __attribute__((always_inline)) {
+    const int64_t lx = m1 - 1 - m0, lw = e.N - 1 - n0;
+    ox = (uint32_t)(tid / CK * a.ldx) + chunk_x() * 16, endx = (uint32_t)(lx * a.ldx) + chunk_x() * 16;
+    ow = (uint32_t)(w_at(tid / CK) * a.ldw) + chunk_w() * 16, endw = (uint32_t)(min(lw, (int64_t)BN - 1) * a.ldw) + chunk_w() * 16;
+    osx = (uint32_t)(tid / 4 * a.ldxs) + (tid & 3) * 4, endsx = (uint32_t)(lx * a.ldxs) + (tid & 3) * 4;
+    osw = (uint32_t)(w_at(tid / 4) * a.ldws) + (tid & 3) * 4, endsw = (uint32_t)(min(lw, (int64_t)BN - 1) * a.ldws) + (tid & 3) * 4;
+    bx = a.x + m0 * a.ldx, bw = a.w + g * a.sw + n0 * a.ldw;
+    bxs = a.xs + m0 * a.ldxs, bws = a.ws + g * a.sws + n0 * a.ldws;
+  };
+  aim();
   const uint32_t lds0 = lds_address(s_tile), lds_s = lds0 + S * STEP;
   const int steps = (a.units + 1) / 2;
 
@@ -324,12 +338,12 @@ k_mx4_tile(Mx4Args a) {
     const uint8_t *sx = bx + (int64_t)t * 128, *sw = bw + (int64_t)t * 128;
     // a wave copies whole rows, on one side of a tile's gate and up rows
     auto side = [&](int i) { return GLU && ((i * TH + wave * 64) / CK) % TN >= TNH ? sw + up_codes : sw; };
-    const uint32_t back_x = left < 128 && cx >= 4 ? 64 : 0, back_w = left < 128 && cw >= 4 ? 64 : 0;
+    const uint32_t back_x = left < 128 && chunk_x() >= 4 ? 64 : 0, back_w = left < 128 && chunk_w() >= 4 ? 64 : 0;
 #pragma unroll
     for (int i = 0; i < SX; ++i)
-      if (ALL_X || wave * 64 < BM * CK) lds_copy16(sx, ox[i] - back_x, base + i * (TH * 16));
+      if (ALL_X || wave * 64 < BM * CK) lds_copy16(sx, min(ox + i * PER * (uint32_t)a.ldx, endx) - back_x, base + i * (TH * 16));
 #pragma unroll
-    for (int i = 0; i < SW; ++i) lds_copy16(side(i), ow[i] - back_w, base + XB + i * (TH * 16));
+    for (int i = 0; i < SW; ++i) lds_copy16(side(i), min(ow + w_at(i * PER) * (uint32_t)a.ldw, endw) - back_w, base + XB + i * (TH * 16));
     if (t % 2 == 0) {  // the scales of steps t and t + 1, 4 units: a wave's copy has 16 rows of 4 times 4 bytes
       const uint32_t at = lds_s + (t / 2 % SB) * SCALES + wave * 256;
       const int units = a.units - t * 2;
@@ -337,151 +351,172 @@ k_mx4_tile(Mx4Args a) {
       const uint32_t back = (tid & 3) < units ? 0 : (tid & 3) * 4;
 #pragma unroll
       for (int i = 0; i < SCX; ++i)
-        if (ALL_XS || wave * 64 < BM * 4) lds_copy4(sxs, osx[i] - back, at + i * (TH * 4));
+        if (ALL_XS || wave * 64 < BM * 4) lds_copy4(sxs, min(osx + i * PERS * (uint32_t)a.ldxs, endsx) - back, at + i * (TH * 4));
 #pragma unroll
       for (int i = 0; i < SCW; ++i)
-        lds_copy4(GLU && (i * (TH / 4) + wave * 16) % TN >= TNH ? sws + up_scales : sws, osw[i] - back, at + BM * 16 + i * (TH * 4));
+        lds_copy4(GLU && (i * (TH / 4) + wave * 16) % TN >= TNH ? sws + up_scales : sws, min(osw + w_at(i * PERS) * (uint32_t)a.ldws, endsw) - back, at + BM * 16 + i * (TH * 4));
     }
   };
 
-  f32x4_t acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  auto x_row = [&](int i) { return wm * TM + i * 16 + r; };
-  auto w_row = [&](int j) { return wn * TN + (j / NTH) * TNH + (r >> 2) * RUN + (j % NTH) * 4 + (r & 3); };
-  auto frag_x = [&](const uint8_t* b, int i, int ks) __attribute__((always_inline)) {
-    const int row = x_row(i);
-    return *reinterpret_cast<const i32x4_t*>(b + row * 128 + (((2 * q + ks) ^ swz_rows<64, 1>(row)) << 4));
-  };
-  auto frag_w = [&](const uint8_t* b, int j, int ks) __attribute__((always_inline)) {
-    const int row = w_row(j);
-    return *reinterpret_cast<const i32x4_t*>(b + XB + row * 128 + (((2 * q + ks) ^ swz_rows<64, RUN>(row)) << 4));
-  };
-  auto scale_of = [&](int t, int row) -> int {
-    return *reinterpret_cast<const uint16_t*>(s_tile + S * STEP + (t / 2 % SB) * SCALES + row * 16 + (t & 1) * 8 + q * 2);
-  };
-  auto buffer = [&](int t) { return s_tile + (t % S) * STEP; };
-
-  // this wave's operands of a step's instruction ks
-  i32x4_t fw[2][NT], fx[MT];
-  int sw[NT], sx[MT];
-  auto read_w = [&](int into, int t, int ks) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) fw[into][j] = frag_w(buffer(t), j, ks);
-  };
-  auto products = [&](auto ks, int i) __attribute__((always_inline)) {
-    constexpr int B = decltype(ks)::value;
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = mfma4<B>(fw[B][j], fx[i], acc[i][j], sw[j], sx[i]);
-    if constexpr (C::AHEAD) {
-      // the products stay on this side of the barrier and of the branches around it (no instruction, only a use of the sums),
-      // and an operand is read again behind them, not into a second register
-#pragma unroll
-      for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  // the last step's second unit where there is none: zeros on W's side, for the lanes q >= 2 that hold it
-  const bool odd = a.units & 1;
-  auto drop = [&](int set) __attribute__((always_inline)) {
-    if (odd && q >= 2) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) fw[set][j] = i32x4_t{0, 0, 0, 0}, sw[j] = 0;
-    }
-  };
-  const std::integral_constant<int, 0> first;
-  const std::integral_constant<int, 1> second;
 #pragma unroll
   for (int t = 0; t < S - 1; ++t)
     if (t < steps) issue(t);
-  if constexpr (C::AHEAD) {
-    // as in k_mm_tile: an x operand is read again as soon as its products are issued, the w operands half a step ahead into a
-    // second set, and the barrier of a step stands inside the last half's products
-    static_assert(S == 2, "two buffers");
-    constexpr int LATE = 2;  // x operands whose products stand before the barrier
-    vm_wait<0>();
-    meet();
-    if (steps > 1) issue(1);
-    read_w(0, 0, 0);
+  while (true) {
+    if (C::AHEAD) asm volatile("" : "+v"(tid));  // what depends on it is computed again and holds no registers from tile to tile
+    const int lane = tid & 63, q = lane >> 4, r = lane & 15;
+    f32x4_t acc[MT][NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) sw[j] = scale_of(0, BM + w_row(j));
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      sx[i] = scale_of(0, x_row(i));
-      fx[i] = frag_x(buffer(0), i, 0);
-    }
-    for (int t = 0; t < steps - 1; ++t) {
-      read_w(1, t, 1);
+      for (int j = 0; j < NT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    auto x_row = [&](int i) { return wm * TM + i * 16 + r; };
+    auto w_row = [&](int j) { return wn * TN + (j / NTH) * TNH + (r >> 2) * RUN + (j % NTH) * 4 + (r & 3); };
+    auto frag_x = [&](const uint8_t* b, int i, int ks) __attribute__((always_inline)) {
+      const int row = x_row(i);
+      return *reinterpret_cast<const i32x4_t*>(b + row * 128 + (((2 * q + ks) ^ swz_rows<64, 1>(row)) << 4));
+    };
+    auto frag_w = [&](const uint8_t* b, int j, int ks) __attribute__((always_inline)) {
+      const int row = w_row(j);
+      return *reinterpret_cast<const i32x4_t*>(b + XB + row * 128 + (((2 * q + ks) ^ swz_rows<64, RUN>(row)) << 4));
+    };
+    auto scale_of = [&](int t, int row) -> int {
+      return *reinterpret_cast<const uint16_t*>(s_tile + S * STEP + (t / 2 % SB) * SCALES + row * 16 + (t & 1) * 8 + q * 2);
+    };
+    auto buffer = [&](int t) { return s_tile + (t % S) * STEP; };
+
+    // this wave's operands of a step's instruction ks
+    i32x4_t fw[2][NT], fx[MT];
+    int sw[NT], sx[MT];
+    auto read_w = [&](int into, int t, int ks) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fw[into][j] = frag_w(buffer(t), j, ks);
+    };
+    auto products = [&](auto ks, int i) __attribute__((always_inline)) {
+      constexpr int B = decltype(ks)::value;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = mfma4<B>(fw[B][j], fx[i], acc[i][j], sw[j], sx[i]);
+      if constexpr (C::AHEAD) {
+        // the products stay on this side of the barrier and of the branches around it (no instruction, only a use of the sums),
+        // and an operand is read again behind them, not into a second register
+#pragma unroll
+        for (int j = 0; j < NT; ++j) asm volatile("" : "+v"(acc[i][j]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // the last step's second unit where there is none: zeros on W's side, for the lanes q >= 2 that hold it
+    const bool odd = a.units & 1;
+    auto drop = [&](int set) __attribute__((always_inline)) {
+      if (odd && q >= 2) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fw[set][j] = i32x4_t{0, 0, 0, 0}, sw[j] = 0;
+      }
+    };
+    const std::integral_constant<int, 0> first;
+    const std::integral_constant<int, 1> second;
+    if constexpr (C::AHEAD) {
+      // as in k_mm_tile: an x operand is read again as soon as its products are issued, the w operands half a step ahead into a
+      // second set, and the barrier of a step stands inside the last half's products
+      static_assert(S == 2, "two buffers");
+      constexpr int LATE = 2;  // x operands whose products stand before the barrier
+      vm_wait<0>();
+      meet();
+      if (steps > 1) issue(1);
+      read_w(0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) sw[j] = scale_of(0, BM + w_row(j));
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        sx[i] = scale_of(0, x_row(i));
+        fx[i] = frag_x(buffer(0), i, 0);
+      }
+      for (int t = 0; t < steps - 1; ++t) {
+        read_w(1, t, 1);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          products(first, i);
+          fx[i] = frag_x(buffer(t), i, 1);
+        }
+#pragma unroll
+        for (int i = 0; i < LATE; ++i) products(second, i);
+        vm_wait<0>();
+        meet();  // step t + 1 is in LDS and step t in registers
+        if (t + 2 < steps) issue(t + 2);
+        read_w(0, t + 1, 0);
+        int next[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) next[j] = scale_of(t + 1, BM + w_row(j));
+#pragma unroll
+        for (int i = 0; i < LATE; ++i) {
+          sx[i] = scale_of(t + 1, x_row(i));
+          fx[i] = frag_x(buffer(t + 1), i, 0);
+        }
+#pragma unroll
+        for (int i = LATE; i < MT; ++i) {
+          products(second, i);
+          sx[i] = scale_of(t + 1, x_row(i));
+          fx[i] = frag_x(buffer(t + 1), i, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sw[j] = next[j];
+      }
+      read_w(1, steps - 1, 1);
+      drop(0);
+      drop(1);
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         products(first, i);
-        fx[i] = frag_x(buffer(t), i, 1);
+        fx[i] = frag_x(buffer(steps - 1), i, 1);
       }
 #pragma unroll
-      for (int i = 0; i < LATE; ++i) products(second, i);
-      vm_wait<0>();
-      meet();  // step t + 1 is in LDS and step t in registers
-      if (t + 2 < steps) issue(t + 2);
-      read_w(0, t + 1, 0);
-      int next[NT];
+      for (int i = 0; i < MT; ++i) products(second, i);
+    } else {
+      for (int t = 0; t < steps; ++t) {
+        // copies issued after step t's: at least CP for every later step (scales beside, which only makes the wait stricter)
+        if (t + S - 1 > steps) vm_wait<0>();
+        else vm_wait<(S - 2) * CP>();
+        meet();
+        if (t + S - 1 < steps) issue(t + S - 1);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) next[j] = scale_of(t + 1, BM + w_row(j));
+        for (int i = 0; i < MT; ++i) sx[i] = scale_of(t, x_row(i));
 #pragma unroll
-      for (int i = 0; i < LATE; ++i) {
-        sx[i] = scale_of(t + 1, x_row(i));
-        fx[i] = frag_x(buffer(t + 1), i, 0);
-      }
+        for (int j = 0; j < NT; ++j) sw[j] = scale_of(t, BM + w_row(j));
 #pragma unroll
-      for (int i = LATE; i < MT; ++i) {
-        products(second, i);
-        sx[i] = scale_of(t + 1, x_row(i));
-        fx[i] = frag_x(buffer(t + 1), i, 0);
-      }
+        for (int ks = 0; ks < 2; ++ks) {
+          read_w(ks, t, ks);
+          if (t == steps - 1) drop(ks);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) sw[j] = next[j];
-    }
-    read_w(1, steps - 1, 1);
-    drop(0);
-    drop(1);
+          for (int i = 0; i < MT; ++i) fx[i] = frag_x(buffer(t), i, ks);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      products(first, i);
-      fx[i] = frag_x(buffer(steps - 1), i, 1);
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) products(second, i);
-  } else {
-    for (int t = 0; t < steps; ++t) {
-      // copies issued after step t's: at least CP for every later step (scales beside, which only makes the wait stricter)
-      if (t + S - 1 > steps) vm_wait<0>();
-      else vm_wait<(S - 2) * CP>();
-      meet();
-      if (t + S - 1 < steps) issue(t + S - 1);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) sx[i] = scale_of(t, x_row(i));
-#pragma unroll
-      for (int j = 0; j < NT; ++j) sw[j] = scale_of(t, BM + w_row(j));
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        read_w(ks, t, ks);
-        if (t == steps - 1) drop(ks);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) fx[i] = frag_x(buffer(t), i, ks);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          if (ks == 0) products(first, i);
-          else products(second, i);
+          for (int i = 0; i < MT; ++i) {
+            if (ks == 0) products(first, i);
+            else products(second, i);
+          }
         }
       }
     }
+    if (!e.simple) {
+      // through LDS where there is more to do than SwiGLU and a residual, whose code would stand there for every piece
+      if constexpr (C::BM < 64) store_regs<T, C, GLU, false>(e, acc, g, m0, m1, n0);
+      else store_tile<T, C, true, GLU>(e, acc, s_tile, g, m0, m1, n0);
+      return;
+    }
+    const int64_t done0 = m0, done1 = m1, done_n = n0;
+    bool more = false;
+    if constexpr (C::AHEAD) {  // the next tile's first step is on its way while this one's sums are stored
+      job += gridDim.x;
+      more = e.mode != MM_ROW_GROUPS && job < a.tiles;
+      if (more) {
+        asm volatile("" : "+v"(tid));
+        locate();
+        aim();
+        meet();  // every wave has read the last step
+        issue(0);
+      }
+    }
+    store_regs<T, C, GLU, true>(e, acc, g, done0, done1, done_n);
+    if (!more) return;
   }
-  // through LDS where there is more to do than SwiGLU and a residual, whose code would stand there for every piece
-  if (e.simple) store_regs<T, C, GLU, true>(e, acc, g, m0, m1, n0);
-  else if constexpr (C::BM < 64) store_regs<T, C, GLU, false>(e, acc, g, m0, m1, n0);
-  else store_tile<T, C, true, GLU>(e, acc, s_tile, g, m0, m1, n0);
 }
 
 // ---- few rows --------------------------------------------------------------------------------------------
@@ -491,7 +526,7 @@ k_mx4_tile(Mx4Args a) {
 // barrier before the end, where the waves' sums meet in LDS in wave order.
 //
 // RAW: x comes in 16 bits and every wave quantises what it multiplies, a lane its own blocks: for up to 16 rows, whose x
-// is small next to W (16 rows, 4096 -> 2 x 2048: one launch of 7.5 us instead of two of 2.8 and 6, and no workspace).
+// is small next to W (16 rows, 4096 -> 2 x 2048: 8.5 us and not 12.3 for two launches and their workspace).
 template <int MT>
 constexpr int mx4_unroll() { return MT >= 4 ? 1 : 2; }
 
@@ -727,7 +762,11 @@ hipError_t launch_mx4_tile(const Mx4Args& a, hipStream_t s) {
   static std::atomic<uint64_t> done{0};
   const hipError_t set = allow_lds(reinterpret_cast<const void*>(fn), lds, &done);
   if (set != hipSuccess) return set;
-  hipLaunchKernelGGL(fn, dim3((unsigned)tiles), dim3(C::TH), lds, s, a);
+  Mx4Args p = a;
+  p.tiles = (int)tiles;
+  // one workgroup a CU that goes on to the next tile, where the sums go out of registers
+  const int64_t grid = C::AHEAD && a.e.simple && a.e.mode != MM_ROW_GROUPS ? std::min<int64_t>(tiles, 256) : tiles;
+  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(C::TH), lds, s, p);
   return hipGetLastError();
 }
 

@@ -10,6 +10,7 @@ PATHS = [
     (LOW, 1000, 1000, 640, 0, 0), (LOW, 900, 520, 1000, 4, 0), (LOW, 1300, 520, 1152, 0, 40), (LOW, 1400, 264, 300, 4, 33),
     (MID, 2040, 4104, 300, 0, 0), (MID, 2100, 2056, 512, 4, 0), (MID, 5000, 1032, 640, 0, 40), (MID, 4900, 520, 300, 4, 40),
     (BIG, 4090, 4088, 1100, 0, 0), (BIG, 4000, 2040, 1152, 4, 0), (BIG, 8000, 4088, 1100, 0, 4), (BIG, 8000, 2040, 1152, 4, 4),
+    (BIG, 7800, 4088, 1100, 0, 0), (BIG, 8000, 2040, 1024, 4, 0),     # more tiles than workgroups
     (THIN, 100, 520, 1152, 0, 64), (THIN, 130, 264, 1100, 4, 64), (THIN, 300, 1032, 500, 0, 70),
 ]
 
