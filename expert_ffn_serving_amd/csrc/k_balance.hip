@@ -70,12 +70,14 @@ struct LogitRow {
   }
 };
 
-// e^x to about 2 units in the last place and 0 below 2^-126, for x <= 0 or NaN: 2^(x log2 e), the product's rounding error
-// put back
+// e^x to about 2 units in the last place and 0 below 2^-126, for x <= 0 or NaN.  With log2 e = a + b, a its nearest float: t = fl(x a)
+// leaves d = (x a - t) + x b, and e^x = 2^t 2^d, where 2^d = 1 + d ln 2 to fp32, |d| being below 2^-16.
 __device__ inline float exp_down(float x) {
+  constexpr double log2e = 1.4426950408889634074;  // 1 / ln 2
+  constexpr float a = (float)log2e, b = (float)(log2e - (double)a), ln2 = (float)(1.0 / log2e);
   x = x < -104.f ? -104.f : x;
-  const float t = x * 1.44269504088896341f, lo = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269504088896341f, -t));
-  return __builtin_amdgcn_exp2f(t) * fmaf(lo, 0.693147180559945309f, 1.0f);
+  const float t = x * a, d = fmaf(x, b, fmaf(x, a, -t));
+  return __builtin_amdgcn_exp2f(t) * fmaf(d, ln2, 1.0f);
 }
 
 // A copy that stays one: the value is taken out of the register that the next load goes to before that load is issued (else the
@@ -88,9 +90,9 @@ __device__ inline void wave_order() {
   asm volatile("" : : : "memory");
   __builtin_amdgcn_wave_barrier();
 }
+
 // grid: parts.  Wave w of part p takes rows p W + w, then parts W further (W waves); the part's sums of p and of lse^2 and
-// its counts go to one row of the workspace.  2048 x 256 fp32 4.9 us: the way to
-// memory and back, two rows a wave.
+// its counts go to one row of the workspace.  2048 x 256 fp32 4.9 us: the way to memory and back, two rows a wave.
 template <typename T, int VEC, bool WHOLE, int NV>
 __global__ void __launch_bounds__(64 * (waves_of<VEC, NV>()))
 k_balance(BalanceArgs a) {
