@@ -22,6 +22,7 @@ typedef __bf16 bf16_t;
 // A wave takes a row; waves of a workgroup, 16 where the registers of so many hold it.
 template <int VEC, int NV>
 constexpr int waves_of() { return VEC * NV <= 16 ? 16 : 4; }
+constexpr int waves_for(int E) { return E <= 16 * 64 ? 16 : 4; }  // the same: VEC NV is the number of columns of a lane
 constexpr int kGradWaves = 4;
 constexpr float kInf = __builtin_inff();
 
@@ -91,14 +92,23 @@ __device__ inline void wave_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// sum: over the experts of their sum of p times their count; z: the sum of lse^2
+__device__ inline void put_losses(const BalanceArgs& a, double sum, double z, int live) {
+  const double n = (double)live;
+  a.losses[0] = live ? (float)(sum * a.E / (n * n * a.K)) : 0.f;
+  a.losses[1] = live ? (float)(z / n) : 0.f;
+}
+
 // grid: parts.  Wave w of part p takes rows p W + w, then parts W further (W waves); the part's sums of p and of lse^2 and
 // its counts go to one row of the workspace.  2048 x 256 fp32 4.9 us: the way to memory and back, two rows a wave.
+// One part alone finishes by itself.
 template <typename T, int VEC, bool WHOLE, int NV>
 __global__ void __launch_bounds__(64 * (waves_of<VEC, NV>()))
 k_balance(BalanceArgs a) {
   constexpr int W = waves_of<VEC, NV>();
   extern __shared__ int s_count[];  // [E + 1], the last: live tokens
   __shared__ float s_p[W][64 * VEC], s_z[W];
+  __shared__ double s_share[W];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), E = a.E, K = a.K;
   for (int e = threadIdx.x; e <= E; e += 64 * W) s_count[e] = 0;
   __syncthreads();
@@ -162,6 +172,8 @@ k_balance(BalanceArgs a) {
     if (lane == 0) atomicAdd(&s_count[E], 1);
   }
   if (lane == 0) s_z[wave] = z;
+  const bool alone = gridDim.x == 1;
+  double share = 0.0;  // alone: of the sum of f P
   int2* part = a.part + (int64_t)blockIdx.x * (E + 1);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {  // the waves' sums in wave order, 64 VEC columns at a time
@@ -173,13 +185,31 @@ k_balance(BalanceArgs a) {
       float v = s_p[0][c];
 #pragma unroll
       for (int w = 1; w < W; ++w) v += s_p[w][c];
-      if (j < E) part[j] = make_int2(__float_as_int(v), s_count[j]);
+      if (j >= E) continue;
+      if (alone) {
+        share += (double)v * (double)s_count[j];
+        a.counts[j] = s_count[j];
+      } else {
+        part[j] = make_int2(__float_as_int(v), s_count[j]);
+      }
     }
+    __syncthreads();
+  }
+  if (alone) {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) share += __shfl_xor(share, o);
+    if (lane == 0) s_share[wave] = share;
     __syncthreads();
   }
   if (threadIdx.x) return;
   for (int w = 1; w < W; ++w) z += s_z[w];
-  part[E] = make_int2(__float_as_int(z), s_count[E]);
+  if (!alone) {
+    part[E] = make_int2(__float_as_int(z), s_count[E]);
+    return;
+  }
+  for (int w = 1; w < W; ++w) share += s_share[w];
+  a.counts[E] = s_count[E];
+  put_losses(a, share, z, s_count[E]);
 }
 
 // Column sums over the parts, in double and in order: many columns or parts are added up by many workgroups first
@@ -265,9 +295,7 @@ k_balance_join(BalanceArgs a, const int2* __restrict__ part, int parts) {
   __syncthreads();
   if (tid) return;
   for (int w = 1; w < kJoin / 64; ++w) sum += s_sum[w];
-  const double n = (double)s_n;
-  a.losses[0] = n > 0 ? (float)(sum * E / (n * n * a.K)) : 0.f;
-  a.losses[1] = n > 0 ? (float)(s_z / n) : 0.f;
+  put_losses(a, sum, s_z, s_n);
 }
 
 // grid: as many workgroups as fill the chip; a wave per row.  f of the lane's columns stays in registers.  Bound by HBM:
@@ -424,18 +452,23 @@ void with_logits(int dtype, int E, F f) {
 
 }  // namespace
 
-// Workgroups of the pass over the logits: one per CU, fewer where its 16 waves (at most) would have fewer than two rows each.
-int64_t balance_parts(int64_t T) { return std::max<int64_t>(1, std::min<int64_t>(kParts, (T + 31) / 32)); }
+// Workgroups of the pass over the logits: one per CU, fewer where its waves would have fewer than two rows each, and one alone, which
+// needs no second launch, for up to four rows a wave: 64 x 256 fp32 9.0 us and not 11.6, 128 rows 10.7 and 11.6, 256 rows 18 and 11.7.
+int64_t balance_parts(int64_t T, int E) {
+  const int W = waves_for(E);
+  return T <= 4 * W ? 1 : std::min<int64_t>(kParts, (T + 2 * W - 1) / (2 * W));
+}
 
-int64_t balance_workspace(int64_t T, int E) { return ((balance_parts(T) + 1) * (E + 1) * 8 + 255) / 256 * 256; }
+int64_t balance_workspace(int64_t T, int E) { return ((balance_parts(T, E) + 1) * (E + 1) * 8 + 255) / 256 * 256; }
 
 hipError_t launch_balance(BalanceArgs a, void* workspace, hipStream_t s) {
-  int parts = (int)balance_parts(a.T);
+  int parts = (int)balance_parts(a.T, a.E);
   a.part = static_cast<int2*>(workspace);
   with_logits(a.dtype, a.E, [&](auto t, auto vec, auto whole, auto nv) {
     constexpr int V = decltype(vec)::value, N = decltype(nv)::value;
     hipLaunchKernelGGL((k_balance<decltype(t), V, decltype(whole)::value, N>), dim3(parts), dim3(64 * waves_of<V, N>()), (a.E + 1) * 4, s, a);
   });
+  if (parts == 1) return hipGetLastError();
   const int2* part = a.part;
   if ((int64_t)parts * (a.E + 1) > 65536) {
     int2* out = a.part + (int64_t)parts * (a.E + 1);

@@ -77,6 +77,13 @@ def test_tokens(eff, T):
     check_grad(eff, logits, ids, counts, lse, torch.tensor([1e-2, 1e-3]), w, dw)
 
 
+@pytest.mark.parametrize("T,E", [(16, 1100), (17, 1100), (63, 40), (64, 1024), (65, 40), (66, 1024)])
+def test_few_tokens(eff, T, E):
+    """About where one workgroup no longer takes all of them."""
+    logits, ids, _, _ = batch(T, E, 4, BF, T + E)
+    check(eff, logits, ids, torch.arange(T) % 5 != 3)
+
+
 def test_parts_of_the_gradient(eff):
     logits, ids, w, dw = batch(33, 24, 3, F32, 5)
     counts, lse, _ = check(eff, logits, ids)
