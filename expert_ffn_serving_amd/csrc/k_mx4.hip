@@ -525,8 +525,9 @@ k_mx4_tile(Mx4Args a) {
 // k_mm_few does for 16 bits: every wave keeps U chunks of 256 k (2 KiB of W each) in flight in registers, nothing waits for a
 // barrier before the end, where the waves' sums meet in LDS in wave order.
 //
-// RAW: x comes in 16 bits and every wave quantises what it multiplies, a lane its own blocks: for up to 16 rows, whose x
-// is small next to W (16 rows, 4096 -> 2 x 2048: 8.5 us and not 12.3 for two launches and their workspace).
+// RAW: x comes in 16 bits and every wave quantises what it multiplies, a lane its own blocks: for 16 rows, whose x
+// is small next to W (16 rows, 4096 -> 2 x 2048: 8.5 us and not 12.3 for two launches and their workspace), and for more
+// where there is little to compute (mx4_takes_raw).
 template <int MT>
 constexpr int mx4_unroll() { return MT >= 4 ? 1 : 2; }
 
@@ -727,7 +728,7 @@ int64_t mx4_rows(const MmArgs& e, int64_t BM) { return e.mode == MM_ROW_GROUPS ?
 // 48, 64, 96 and 128 rows, 4096 -> 2 x 2048: 388, 486, 669; 457, 513, 683; 539, 526, 690; 647, 600, 709; 776, 740, 729.
 // Groups of up to 8 rows stream W in 16 x 128 tiles, four steps of it in LDS: 512 groups, 2560 -> 2 x 640, a row each 134 and
 // 138 (64 x 128); 4 rows 155 and 160; 16 rows 203 and 177.
-int plan_mx4(const Mx4Args& a) {
+int plan_mx4(const Mx4Args& a, double* us = nullptr) {
   const MmArgs& e = a.e;
   const bool grouped = e.mode == MM_ROW_GROUPS;
   const int64_t n = e.act == EFF_ACT_SWIGLU ? 2 * e.N : e.N, groups = grouped ? std::min<int64_t>(e.groups, std::max<int64_t>(1, e.M)) : 1;
@@ -751,6 +752,7 @@ int plan_mx4(const Mx4Args& a) {
     const double count = rt * ceil_div(n, t.bn), full = std::floor(count / (256.0 * t.occ)), rest = count - full * 256 * t.occ;
     offer(t.kind, full * (t.step * steps + t.fixed) + (rest > 0 ? (rest <= 256 ? t.alone : t.step) * steps + t.fixed : 0));
   }
+  if (us) *us = least;
   return best;
 }
 
@@ -796,7 +798,22 @@ hipError_t launch_mx4_kind(const Mx4Args& a, int kind, hipStream_t s) {
 }  // namespace
 
 int mx4_choice(const Mx4Args& a) { return plan_mx4(a); }
-bool mx4_takes_raw(const Mx4Args& a) { return a.e.K % 8 == 0 && plan_mx4(a) == MX_FEW1; }
+
+// Quantising in every workgroup of 16 rows and 16 W rows against once, in a launch of its own, and the kernel planned then.  us of
+// both in a row (and of the calls, bound by the host beyond): 256 x 1024, 256 rows 4.8, 7.8 (7.4, 11.2); 256 x 4096, 256 rows 8.8, 12.9;
+// 2 x 640 x 2560, 48 rows 7.0, 8.8, 128 rows 13.6, 9.4; 1024 x 2048, 64 rows 5.9, 9.0, 256 rows 13.3, 9.4; 2048 x 4096, 32 rows
+// 8.5, 9.6, 64 rows 13.5, 12.3; 4096 x 4096, 16 rows 8.9, 8.3 (8.8, 11.9), 32 rows 14.1, 9.6.  Fitted to up to 1024 rows.
+bool mx4_takes_raw(const Mx4Args& a) {
+  const MmArgs& e = a.e;
+  double coded;
+  const int kind = plan_mx4(a, &coded);
+  const int64_t jobs = ceil_div(e.N, e.act == EFF_ACT_SWIGLU ? 8 : 16) * mx4_rows(e, 16);
+  if (e.K % 8 || e.M > 1024 || !fits(jobs, 1024)) return false;
+  const double raw = 3.5 + (0.2 + 1.2e-3 * (double)e.K) * (double)ceil_div(jobs, 256);
+  // the second launch, a long k's way through few workgroups, x read and its codes written
+  const double first = 3.5 + 5e-4 * (double)e.K + 5e-7 * (double)e.M * (double)e.K;
+  return raw <= coded + first || (kind == MX_FEW1 && e.M <= 16);
+}
 
 // whether the launch holds the problem (a grid's threads stay below 2^32)
 bool mx4_matmul_fits(const Mx4Args& a) {

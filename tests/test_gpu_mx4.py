@@ -330,7 +330,8 @@ def test_operand_strides(eff):
 
 
 @pytest.mark.parametrize("dt", [BF, HF])
-@pytest.mark.parametrize("m,n,k,act", [(1, 40, 8, 0), (3, 72, 136, 4), (16, 64, 1000, 0), (9, 520, 2560, 4), (13, 40, 264, 4), (5, 24, 520, 0)])
+@pytest.mark.parametrize("m,n,k,act", [(1, 40, 8, 0), (3, 72, 136, 4), (16, 64, 1000, 0), (9, 520, 2560, 4), (13, 40, 264, 4), (5, 24, 520, 0),
+                                     (40, 264, 520, 0), (250, 40, 1032, 4), (129, 130, 2568, 0)])
 def test_16_bit_rows_quantised_inside(eff, m, n, k, act, dt):
     """Few rows: the kernel quantises x itself, at any place and row distance, k inside a block, a unit and a chunk of two: the bits
     of quantising first.  What lies beside the rows may hold anything."""
