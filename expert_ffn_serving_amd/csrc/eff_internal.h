@@ -420,6 +420,9 @@ hipError_t launch_combine_tokens_grad(int dtype, const void* dout, int64_t ldd, 
                                       const int32_t* pos, const float* w, int64_t T, int K, int64_t H, void* dys,
                                       int64_t lddys, float* dw, hipStream_t s);
 
+// Workgroups of so many threads that one launch holds: a grid's threads stay below 2^32.
+constexpr int64_t most_workgroups(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
+
 // Layer norm (k_norm.hip): rows of dtype, weights of w_dtype (dtype or fp32); w, b, mean, rstd may be null.
 struct NormArgs {
   const void* x;
@@ -431,6 +434,8 @@ struct NormArgs {
   int dtype, w_dtype;
 };
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+// rows that one launch takes, `per` to a workgroup of `threads`
+int64_t norm_at_once(int threads, int64_t per);
 
 // dx null: not written.  part: norm_parts rows of 2 H fp32 where dw or db is wanted, else null.
 struct NormGradArgs {

@@ -424,19 +424,20 @@ void with_types(int dtype, int w_dtype, F f) {
   else f(float{}, float{});
 }
 
-constexpr int64_t kNormGrid = 1 << 22;  // workgroups of up to 1024 threads: a grid's threads stay below 2^32
-
 }  // namespace
+
+int64_t norm_at_once(int threads, int64_t per) { return most_workgroups(threads) * per; }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   with_types(a.dtype, a.w_dtype, [&](auto t, auto wt) {
     typedef decltype(t) T;
     typedef decltype(wt) W;
     constexpr int VEC = 16 / (int)sizeof(T);
-    auto rows = [&](auto launch, int64_t per) {  // per: rows of a workgroup
-      for (int64_t t0 = 0; t0 < a.T; t0 += kNormGrid * per) {
+    auto rows = [&](auto launch, int threads, int64_t per) {  // per: rows of a workgroup
+      const int64_t most = norm_at_once(threads, per);
+      for (int64_t t0 = 0; t0 < a.T; t0 += most) {
         NormArgs p = a;
-        p.T = std::min(kNormGrid * per, a.T - t0);
+        p.T = std::min(most, a.T - t0);
         p.x = reinterpret_cast<const T*>(a.x) + t0 * a.ldx;
         p.y = reinterpret_cast<T*>(a.y) + t0 * a.ldy;
         if (a.mean) p.mean = a.mean + t0;
@@ -448,10 +449,10 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
       typedef decltype(sh) S;
       rows([&](const NormArgs& p, dim3 g) {
         hipLaunchKernelGGL((k_norm<T, W, VEC, decltype(whole)::value, S::th, S::nv, S::r>), g, dim3(S::th * S::r), 0, s, p);
-      }, S::r);
+      }, S::th * S::r, S::r);
     };
     with_shape(cdiv(a.H, VEC), [&](auto sh) { a.H % VEC ? go(sh, std::false_type{}) : go(sh, std::true_type{}); }, [&] {
-      rows([&](const NormArgs& p, dim3 g) { hipLaunchKernelGGL((k_norm_long<T, W>), g, dim3(kLongThreads), 0, s, p); }, 1);
+      rows([&](const NormArgs& p, dim3 g) { hipLaunchKernelGGL((k_norm_long<T, W>), g, dim3(kLongThreads), 0, s, p); }, kLongThreads, 1);
     });
   });
   return hipGetLastError();
@@ -468,9 +469,10 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
     constexpr int VEC = 16 / (int)sizeof(T);
     int64_t written = parts;  // rows of partial sums that the pass writes
     auto lengthy = [&] {
-      for (int64_t t0 = 0; a.dx && t0 < a.T; t0 += kNormGrid) {
+      const int64_t most = norm_at_once(kLongThreads, 1);
+      for (int64_t t0 = 0; a.dx && t0 < a.T; t0 += most) {
         NormGradArgs p = a;
-        p.T = std::min(kNormGrid, a.T - t0);
+        p.T = std::min(most, a.T - t0);
         p.x = reinterpret_cast<const T*>(a.x) + t0 * a.ldx;
         p.dy = reinterpret_cast<const T*>(a.dy) + t0 * a.lddy;
         if (a.residual) p.residual = reinterpret_cast<const T*>(a.residual) + t0 * a.ldr;

@@ -429,8 +429,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t group_tiles(int64_t M, int64_t groups, int64_t BM) { return M / BM + std::min(groups, M); }
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
-// whether one launch holds so many workgroups: its threads stay below 2^32
-bool fits(int64_t workgroups, int threads) { return workgroups * threads < (int64_t)1 << 32; }
+bool fits(int64_t workgroups, int threads) { return workgroups <= most_workgroups(threads); }
 
 bool aligned16(std::initializer_list<const void*> ptrs, std::initializer_list<int64_t> sizes, int bytes) {
   for (const void* p : ptrs)
