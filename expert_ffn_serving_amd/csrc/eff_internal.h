@@ -436,6 +436,8 @@ struct NormArgs {
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 // rows that one launch takes, `per` to a workgroup of `threads`
 int64_t norm_at_once(int threads, int64_t per);
+// columns whose partial sums one launch adds up
+int64_t norm_columns_at_once();
 
 // dx null: not written.  part: norm_parts rows of 2 H fp32 where dw or db is wanted, else null.
 struct NormGradArgs {

@@ -361,16 +361,18 @@ k_norm_cols_long(NormGradArgs a) {
   part[a.H + h] = sb;
 }
 
-// grid: (ceil(H / 64), 2).  The partial sums of 64 columns of dw (y = 0) or db: 16 waves take every 16th part, their sums
-// are added in wave order.
+// grid: (64 columns from h0 on each, 2).  The partial sums of 64 columns of dw (y = 0) or db: 16 waves take every 16th part, their
+// sums are added in wave order.
+constexpr int kJoinThreads = 1024;
+
 template <typename W>
-__global__ void __launch_bounds__(1024)
-k_norm_join(const float* __restrict__ part, int64_t parts, int64_t H, void* dw, void* db) {
+__global__ void __launch_bounds__(kJoinThreads)
+k_norm_join(const float* __restrict__ part, int64_t parts, int64_t H, int64_t h0, void* dw, void* db) {
   __shared__ float s_sum[16][64];
   W* out = reinterpret_cast<W*>(blockIdx.y ? db : dw);
   if (!out) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t h = (int64_t)blockIdx.x * 64 + lane;
+  const int64_t h = h0 + (int64_t)blockIdx.x * 64 + lane;
   const float* p = part + blockIdx.y * H + h;
   float sum = 0.f;
   if (h < H) {
@@ -427,6 +429,7 @@ void with_types(int dtype, int w_dtype, F f) {
 }  // namespace
 
 int64_t norm_at_once(int threads, int64_t per) { return most_workgroups(threads) * per; }
+int64_t norm_columns_at_once() { return most_workgroups(kJoinThreads) * 64; }
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
   with_types(a.dtype, a.w_dtype, [&](auto t, auto wt) {
@@ -489,8 +492,9 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
                          lds, s, a);
     };
     if (a.T > 0) with_grad_shape(cdiv(a.H, VEC), [&](auto sh) { a.H % VEC ? go(sh, std::false_type{}) : go(sh, std::true_type{}); }, lengthy);
-    if (a.dw || a.db)
-      hipLaunchKernelGGL((k_norm_join<W>), dim3((unsigned)cdiv(a.H, 64), 2), dim3(1024), 0, s, a.part, a.T > 0 ? written : 0, a.H, a.dw, a.db);
+    for (int64_t h0 = 0; (a.dw || a.db) && h0 < a.H; h0 += norm_columns_at_once())
+      hipLaunchKernelGGL((k_norm_join<W>), dim3((unsigned)cdiv(std::min(norm_columns_at_once(), a.H - h0), 64), 2), dim3(kJoinThreads), 0, s,
+                         a.part, a.T > 0 ? written : 0, a.H, h0, a.dw, a.db);
   });
   return hipGetLastError();
 }

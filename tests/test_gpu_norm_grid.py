@@ -1,5 +1,5 @@
 """Layer norm over more rows than one launch takes: 2^32 threads are refused, so the rows of workgroups of 1024 threads are split
-after 2^22 - 1.  x and dy are windows into one vector, a value further from row to row; the outputs take 69 and 137 GB."""
+after 2^22 - 1.  x and dy are windows into one vector, a value further from row to row; the outputs take 69 and 137 GB.  The same for the columns of dw and db, 64 to a workgroup."""
 import pytest
 import torch
 
@@ -69,4 +69,21 @@ def test_gradients(eff):
         rx, xe = B.norm_grad64(dy[r:r + 1].cpu(), x[r:r + 1].cpu(), None, mean[r:r + 1].cpu(), rstd[r:r + 1].cpu(), None)[:2]
         R.assert_within(dx[r:r + 1], rx, xe, "dx of row %d" % r)
     del dx
+    torch.cuda.empty_cache()
+
+
+def test_columns(eff):
+    """dw and db of more columns than the last launch adds up at once."""
+    H = 64 * SPLIT + 4099
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, dy = [torch.randn(1, H, generator=g, device="cuda", dtype=BF) for _ in range(2)]
+    mean, rstd = torch.full((1,), 0.125, device="cuda"), torch.full((1,), 0.75, device="cuda")
+    dw, db = [torch.full((H,), float("nan"), device="cuda") for _ in range(2)]
+    eff.layer_norm_backward(dy, x, mean, rstd, dw=dw, db=db)
+    assert torch.equal(db, dy[0].float())
+    for at in range(0, H, 1 << 26):
+        c = slice(at, at + (1 << 26))
+        want = dy[0, c].double() * (x[0, c].double() - 0.125) * 0.75
+        R.assert_within(dw[c], want, 8 * B.U * want.abs(), "dw")
+    del x, dy, dw, db, want
     torch.cuda.empty_cache()

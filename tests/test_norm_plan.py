@@ -1,4 +1,4 @@
-"""How many rows one launch of layer norm takes, asked of the library without a GPU."""
+"""How many rows and columns one launch of layer norm takes, asked of the library without a GPU."""
 import ctypes
 import os
 import subprocess
@@ -30,3 +30,10 @@ def test_a_launchs_threads_stay_below_2_32(shim, threads, per):
     rows = f(threads, per)
     assert rows % per == 0
     assert rows // per * threads < 1 << 32 <= (rows // per + 1) * threads
+
+
+def test_the_columns_of_a_launch_too(shim):
+    """64 columns to a workgroup of 1024 threads, which add up the partial sums of dw and db."""
+    shim.shim_norm_columns_at_once.restype = ctypes.c_int64
+    cols = shim.shim_norm_columns_at_once()
+    assert cols % 64 == 0 and cols // 64 * 1024 < 1 << 32
