@@ -5,7 +5,7 @@
 //
 // A row stays in the registers of TH threads (NV vectors of VEC values each), so it is read once: the mean, then the
 // deviations from it, whose own mean corrects the rounding of the first (a stream whose offset is far above its spread
-// loses nothing).  All statistics and sums are fp32.
+// loses nothing).  All statistics and sums are fp32; a row whose squares leave its range is scaled by a power of two.
 #include <algorithm>
 #include <type_traits>
 
@@ -94,6 +94,85 @@ __device__ inline void row_sum(float* v, float* s) {
   }
 }
 
+// the variance from the deviations' sums (NaN stays: a maximum drops it)
+__device__ inline float variance_of(const float* dev, float inv, float more) {
+  return fmaxf(dev[1] * inv - more * more, 0.f) + 0.f * dev[1];
+}
+// A row's squared deviations leave fp32's range where their sum is no finite number, and lose digits where their mean and eps are
+// below 2^-100.  Such a row is taken times a power of two that brings the largest magnitude into [1, 4), in the second case only up
+// and by 2^110 at most, where eps has room.  What becomes subnormal on the way is nothing next to the largest.  Infinities and
+// NaN stay.
+__device__ inline bool out_of_range(float squares, float inv, float eps) {
+  return !(squares < __builtin_inff()) || fmaf(squares, inv, eps) < 0x1p-100f;
+}
+struct Scaled {
+  float scale, rstd, mean, value;  // rstd of the scaled deviations; the row's own mean and rstd
+  __device__ Scaled(float largest, float squares) {
+    const int e = (int)(__float_as_uint(largest) >> 23) - 127, most = squares < __builtin_inff() ? 0 : 126;
+    scale = __uint_as_float((uint32_t)(127 - min(max(e, -110), most)) << 23);
+  }
+  __device__ void finish(const float* dev, float inv, float first, float more, float eps) {
+    const float var = variance_of(dev, inv, more);
+    rstd = 1.0f / sqrtf(var + eps * scale * scale);
+    value = rstd * scale;
+    if (scale < 1.f && var == 0.f && eps > 0.f) {  // no spread: eps alone, of which its scaled form keeps nothing
+      rstd = fminf(rstd, 0x1.fffffep127f);
+      value = 1.0f / sqrtf(eps);
+    }
+    mean = (first + more) * __uint_as_float((254u << 23) - __float_as_uint(scale));
+  }
+};
+
+// A row out of range: each of its waves takes the statistics by itself (no barrier, whatever the other rows of the workgroup are) and
+// its threads store again what they stored.
+template <typename T, typename W, int VEC, int TH>
+__device__ void norm_again(const NormArgs& a, int64_t row, int tid, float squares) {
+  const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
+  const int lane = threadIdx.x & 63, H = (int)a.H;
+  const float inv = 1.0f / (float)a.H;
+  constexpr int N = 8;  // sums of a lane: a value goes through 32 additions of the longest row's
+  auto each = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (int h = lane; h < H; h += 64 * N)
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (h + j * 64 < H) f(j, (float)x[h + j * 64]);
+  };
+  auto total = [&](float* p) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 1; j < N; ++j) p[0] += p[j];
+    return wave_sum(p[0]);
+  };
+  float top = 0.f, sum[N] = {}, square[N] = {}, dev[2];
+  each([&](int, float v) __attribute__((always_inline)) { top = fmaxf(top, fabsf(v)); });
+  Scaled s(wave_max(top), squares);
+  each([&](int j, float v) __attribute__((always_inline)) { sum[j] += v * s.scale; });
+  const float first = total(sum) * inv;
+#pragma unroll
+  for (int j = 0; j < N; ++j) sum[j] = 0.f;
+  each([&](int j, float v) __attribute__((always_inline)) {
+    const float d = v * s.scale - first;
+    sum[j] += d;
+    square[j] = fmaf(d, d, square[j]);
+  });
+  dev[0] = total(sum), dev[1] = total(square);
+  const float more = dev[0] * inv;
+  s.finish(dev, inv, first, more, a.eps);
+  if (tid == 0) {
+    if (a.mean) a.mean[row] = s.mean;
+    if (a.rstd) a.rstd[row] = s.value;
+  }
+#pragma unroll 1
+  for (int i = tid; i * VEC < H; i += TH)
+#pragma unroll 1
+    for (int h = i * VEC; h < min(H, i * VEC + VEC); ++h) {
+      float y = ((float)x[h] * s.scale - first - more) * s.rstd;
+      if (a.w) y *= (float)reinterpret_cast<const W*>(a.w)[h];
+      if (a.b) y += (float)reinterpret_cast<const W*>(a.b)[h];
+      reinterpret_cast<T*>(a.y)[row * a.ldy + h] = (T)y;
+    }
+}
+
 // grid: ceil(T / R) workgroups of R rows, TH threads each.  Bound by HBM: 8192 x 4096 bf16 30 us, 4.5 TB/s (a plain copy 5.0).
 template <typename T, typename W, int VEC, bool WHOLE, int TH, int NV, int R>
 __global__ void __launch_bounds__(TH * R)
@@ -134,7 +213,7 @@ k_norm(NormArgs a) {
   }
   row_sum<TH, 2>(dev, s_sum[sub][1]);
   const float more = dev[0] * inv;
-  const float rstd = 1.0f / sqrtf(fmaxf(dev[1] * inv - more * more, 0.f) + a.eps + 0.f * dev[1]);
+  const float rstd = 1.0f / sqrtf(variance_of(dev, inv, more) + a.eps);
   if (!live) return;
   if (tid == 0) {
     if (a.mean) a.mean[row] = first + more;
@@ -156,6 +235,19 @@ k_norm(NormArgs a) {
     }
     norm_store<T, VEC, WHOLE>(a.y, row * a.ldy, h, a.H, v[i]);
   }
+  if (out_of_range(dev[1], inv, a.eps)) norm_again<T, W, VEC, TH>(a, row, tid, dev[1]);  // behind the stores: before them it cost 3 %
+}
+
+// the largest of v >= 0 over the TH threads of a row, as row_sum; s: [TH / 64]
+template <int TH>
+__device__ inline float row_max(float v, float* s) {
+  v = wave_max(v);
+  if ((threadIdx.x & 63) == 0) s[(threadIdx.x % TH) >> 6] = v;
+  __syncthreads();
+  v = s[0];
+#pragma unroll
+  for (int w = 1; w < TH / 64; ++w) v = fmaxf(v, s[w]);
+  return v;
 }
 
 // Rows longer than the registers hold: a workgroup of 1024 threads reads its row three times (the second and third
@@ -165,32 +257,49 @@ constexpr int kLongThreads = 1024;
 template <typename T, typename W>
 __global__ void __launch_bounds__(kLongThreads)
 k_norm_long(NormArgs a) {
-  __shared__ float s_sum[2][kLongThreads / 64 * 2];
+  __shared__ float s_sum[2][kLongThreads / 64 * 2], s_max[kLongThreads / 64];
   const int64_t row = blockIdx.x;
   const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
   const float inv = 1.0f / (float)a.H;
-  float sum[2] = {0.f, 0.f}, dev[2] = {0.f, 0.f};
-  for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) sum[0] += (float)x[h];
-  row_sum<kLongThreads, 1>(sum, s_sum[0]);
-  const float first = sum[0] * inv;
-  for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) {
-    const float d = (float)x[h] - first;
-    dev[0] += d;
-    dev[1] = fmaf(d, d, dev[1]);
+  float first, dev[2];
+  auto statistics = [&](float scale) __attribute__((always_inline)) {
+    float sum = 0.f;
+    for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) sum += (float)x[h] * scale;
+    row_sum<kLongThreads, 1>(&sum, s_sum[0]);
+    first = sum * inv;
+    dev[0] = dev[1] = 0.f;
+    for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) {
+      const float d = (float)x[h] * scale - first;
+      dev[0] += d;
+      dev[1] = fmaf(d, d, dev[1]);
+    }
+    row_sum<kLongThreads, 2>(dev, s_sum[1]);
+  };
+  auto put = [&](float scale, float more, float rstd, float mean, float value) __attribute__((always_inline)) {
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = value;
+    }
+    for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) {
+      float y = ((float)x[h] * scale - first - more) * rstd;
+      if (a.w) y *= (float)reinterpret_cast<const W*>(a.w)[h];
+      if (a.b) y += (float)reinterpret_cast<const W*>(a.b)[h];
+      reinterpret_cast<T*>(a.y)[row * a.ldy + h] = (T)y;
+    }
+  };
+  statistics(1.f);
+  if (!__builtin_amdgcn_readfirstlane(out_of_range(dev[1], inv, a.eps))) {
+    const float more = dev[0] * inv, rstd = 1.0f / sqrtf(variance_of(dev, inv, more) + a.eps);
+    put(1.f, more, rstd, first + more, rstd);
+    return;
   }
-  row_sum<kLongThreads, 2>(dev, s_sum[1]);
+  float top = 0.f;
+  for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) top = fmaxf(top, fabsf((float)x[h]));
+  Scaled s(row_max<kLongThreads>(top, s_max), dev[1]);
+  statistics(s.scale);
   const float more = dev[0] * inv;
-  const float rstd = 1.0f / sqrtf(fmaxf(dev[1] * inv - more * more, 0.f) + a.eps + 0.f * dev[1]);
-  if (threadIdx.x == 0) {
-    if (a.mean) a.mean[row] = first + more;
-    if (a.rstd) a.rstd[row] = rstd;
-  }
-  for (int64_t h = threadIdx.x; h < a.H; h += kLongThreads) {
-    float y = ((float)x[h] - first - more) * rstd;
-    if (a.w) y *= (float)reinterpret_cast<const W*>(a.w)[h];
-    if (a.b) y += (float)reinterpret_cast<const W*>(a.b)[h];
-    reinterpret_cast<T*>(a.y)[row * a.ldy + h] = (T)y;
-  }
+  s.finish(dev, inv, first, more, a.eps);
+  put(s.scale, more, s.rstd, s.mean, s.value);
 }
 
 // ---- gradients -------------------------------------------------------------------------------------------

@@ -473,7 +473,8 @@ int eff_combine_tokens_backward(int dtype, const void* dout, int64_t ld_dout, co
 
 /* Layer norm of T rows: y = (x - mean) rstd w + b, mean and 1 / sqrt(variance + eps) of each row of H values in fp32.
  * dtype: EFF_DT_* of x and y; w_dtype: of w and b [H], dtype or EFF_DT_F32; w, b, mean and rstd may be NULL (1, 0, not
- * written).  mean and rstd fp32 [T]. */
+ * written).  mean and rstd fp32 [T].  Rows of finite values of any size are right, also where their variance is beyond fp32; a
+ * row with an infinity or a NaN is NaN. */
 int eff_layer_norm(int dtype, int w_dtype, const void* x, int64_t ld_x, const void* w, const void* b, float eps, int64_t T,
                    int64_t H, void* y, int64_t ld_y, float* mean, float* rstd, eff_stream_t stream);
 
