@@ -4,8 +4,9 @@
 // dx = r (g - mean g - xh mean(g xh)) + residual, dw = sum over rows of dy xh, db = sum over rows of dy.
 //
 // A row stays in the registers of TH threads (NV vectors of VEC values each), so it is read once: the mean, then the
-// deviations from it, whose own mean corrects the rounding of the first (a stream whose offset is far above its spread
-// loses nothing).  All statistics and sums are fp32; a row whose squares leave its range is scaled by a power of two.
+// deviations from it, whose own mean corrects the rounding of the first (y of a stream whose offset is far above its spread
+// loses nothing; the gradients take xh from the saved mean, one fp32 number: an offset of 2^k spreads shifts their xh by up to
+// 2^(k - 24)).  All statistics and sums are fp32; a row whose squares leave its range is scaled by a power of two.
 #include <algorithm>
 #include <type_traits>
 

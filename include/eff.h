@@ -480,6 +480,8 @@ int eff_layer_norm(int dtype, int w_dtype, const void* x, int64_t ld_x, const vo
 
 /* Its gradients from dy (dtype), x, w and the saved mean and rstd, with xh = (x - mean) rstd and g = dy w:
  *   dx = rstd (g - mean(g) - xh mean(g xh)) + residual;   dw = sum over rows of dy xh;   db = sum over rows of dy.
+ * mean and rstd are taken as they are, so the rounding of a mean far above the row's spread (2^k times) shifts xh by up to
+ * 2^(k - 24), in dw and dx.
  * residual (NULL: none; ld_residual 0: one row for all): the gradient that reaches x past the norm, as by a skip
  * connection.  dx, dw and db may be NULL; dw, db of w_dtype.  T = 0 writes zeros to dw and db.  The workspace is needed for
  * dw or db. */
