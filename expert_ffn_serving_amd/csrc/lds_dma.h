@@ -26,11 +26,7 @@ __device__ inline void lds_copy16(const void* base, uint32_t off, uint32_t lds) 
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
 
-// 4 bytes per lane from src into LDS at lds + 4 * lane, in the same way
-__device__ inline void lds_copy4(const void* src, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"(lds), "v"(src) : "memory", "m0");
-}
-
+// 4 bytes per lane from base + off into LDS at lds + 4 * lane, in the same way
 __device__ inline void lds_copy4(const void* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
