@@ -255,11 +255,12 @@ __device__ inline f32x4_t mfma4(i32x4_t w, i32x4_t x, f32x4_t c, int sw, int sx)
 // Scales come to LDS for two steps at a time, 16 bytes a row (one line of a row holds those of 16 steps: fetched step by step
 // it would be requested as often as the codes' lines): [buffer][row][16], x rows first.
 //
-// 256 x 256 (AHEAD) is bound by the power that the matrix cores draw: 8192 x 8192 x 8192 270 us, 4.1 PFLOP/s, 8192 x 2 x 4096 x 4096
-// SwiGLU 155 us, 3.5; the instructions alone, on random codes in registers, reach 6.1 (8.7 on zeros).  Its workgroups, one a
-// CU, take tile after tile where the sums are stored from registers, the next tile's first step on its way meanwhile: 162 -> 157,
-// 277 -> 271 us.  64 x 128 for groups is bound by W's way through LDS: 12288 rows over 256 experts, 4096 -> 2 x 2048, 470 us,
-// 4.9 TB/s of W.
+// 256 x 256 (AHEAD): 8192 x 8192 x 8192 270 us, 4.1 PFLOP/s, 8192 x 2 x 4096 x 4096 SwiGLU 155 us, 3.5; the instructions alone, on
+// random codes in registers, reach 6.1 (8.7 on zeros: the clock gives way to the power drawn).  By the fit at plan_mx4 the steps run at
+// 5.2 and a tile spends 12 us outside them; what takes those has not been measured.  Its workgroups, one a CU, take tile
+// after tile where the sums are stored from registers, the next tile's first step on its way meanwhile: 162 -> 157,
+// 277 -> 271 us.  64 x 128 for groups: 12288 rows over 256 experts, 4096 -> 2 x 2048, 470 us, 4.9 TB/s of W; with a row a group
+// (512 groups, 2560 -> 2 x 640, 138 us) W comes at 6.5 through the same LDS.
 template <int BM, int BN, int WM, int WN, int S, bool AHEAD>
 using MxCfg = TileCfg<BM, BN, WM, WN, 64, S, AHEAD>;
 
@@ -728,6 +729,9 @@ int64_t mx4_rows(const MmArgs& e, int64_t BM) { return e.mode == MM_ROW_GROUPS ?
 // 48, 64, 96 and 128 rows, 4096 -> 2 x 2048: 388, 486, 669; 457, 513, 683; 539, 526, 690; 647, 600, 709; 776, 740, 729.
 // Groups of up to 8 rows stream W in 16 x 128 tiles, four steps of it in LDS: 512 groups, 2560 -> 2 x 640, a row each 134 and
 // 138 (64 x 128); 4 rows 155 and 160; 16 rows 203 and 177.
+// Of groups the host knows M and their number alone: every row counts as routed and every group as an average one.  The tiles' part
+// has no term for W's bytes, so it tells tiles apart and not how long they take where W bounds them: for 64 rows a group it has 286 and
+// 456 us for the 539 and 526 above, and takes the former.
 int plan_mx4(const Mx4Args& a, double* us = nullptr) {
   const MmArgs& e = a.e;
   const bool grouped = e.mode == MM_ROW_GROUPS;
